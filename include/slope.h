@@ -552,4 +552,7 @@ slope_status slope_spmm_e4m3_packed(slope_dtype out_dt, const uint8_t* Xq, const
 }
 #endif
 
+/* The RMS norm with 8-bit codes, its gradient, and the int8 products. */
+#include "slope_int8.h"
+
 #endif /* SLOPE_H_ */

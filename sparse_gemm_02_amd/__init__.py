@@ -2,8 +2,8 @@
 
 Argument marshalling only: every function below checks that its tensors are
 contiguous device tensors, reads their shapes and dtypes, and calls the C ABI
-function of the same name (declared in include/slope.h) on the current HIP
-stream.  All computation happens in the library's HIP kernels; there is no
+function of the same name (declared in include/slope.h and slope_int8.h) on the
+current HIP stream.  All computation happens in the library's HIP kernels; there is no
 fallback.  If the shared library has not been built, every call raises.
 
 Tensor conventions (see include/slope.h):
@@ -36,6 +36,9 @@ __all__ = [
     "slope_lowrank_grads_packed", "slope_adamw", "slope_adamw_double_prune", "AdamWParams",
     "slope_double_prune_packed", "slope_adamw_double_prune_packed", "slope_prune_compress24", "EXPORTED_SYMBOLS",
     "slope_quantize_e4m3", "slope_packed_sparse_e4m3_bytes", "slope_pack_sparse_e4m3", "slope_spmm_e4m3_packed",
+    "slope_rmsnorm", "slope_rmsnorm_bwd_workspace_bytes", "slope_rmsnorm_bwd", "slope_quantize_rows_i8",
+    "slope_packed_sparse_i8_bytes", "slope_pack_sparse_i8", "slope_spmm_i8_packed", "slope_spmm_i8_decode",
+    "I8_DECODE_MAX_TOKENS", "I8_MAX_COLS", "EXPORTED_SYMBOLS_INT8",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -109,6 +112,20 @@ _SIGS = {
 }
 EXPORTED_SYMBOLS = tuple(_SIGS)
 
+# include/slope_int8.h
+_f64 = ctypes.c_double
+_SIGS_INT8 = {
+    "slope_rmsnorm": (_i32, [_i32, _vp, _vp, _i32, _vp, _i64, _i64, _f64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "slope_rmsnorm_bwd_workspace_bytes": (_i32, [_i64, _i64, _P_I64]),
+    "slope_rmsnorm_bwd": (_i32, [_i32, _vp, _vp, _vp, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _vp, _i64, _vp]),
+    "slope_quantize_rows_i8": (_i32, [_i32, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "slope_packed_sparse_i8_bytes": (_i32, [_i64, _i64, _P_I64]),
+    "slope_pack_sparse_i8": (_i32, [_i32, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp]),
+    "slope_spmm_i8_packed": (_i32, [_i32, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "slope_spmm_i8_decode": (_i32, [_i32, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
+}
+EXPORTED_SYMBOLS_INT8 = tuple(_SIGS_INT8)
+
 _lib = None
 
 
@@ -126,7 +143,7 @@ def library() -> ctypes.CDLL:
             raise RuntimeError(f"{library_path} is missing: build it first "
                                "(python -m sparse_gemm_02_amd.build); there is no fallback path")
         lib = ctypes.CDLL(library_path)
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in (*_SIGS.items(), *_SIGS_INT8.items()):
             f = getattr(lib, name)
             f.restype, f.argtypes = res, args
         _lib = lib
@@ -505,3 +522,141 @@ def slope_spmm_e4m3_packed(Xq, x_scale, packed_w, w_scale, N, Y, stream=None) ->
     _check("slope_spmm_e4m3_packed", library().slope_spmm_e4m3_packed(_dt(Y), _nn(Xq), _nn(x_scale), T, K,
                                                                       _nn(packed_w), _nb(packed_w), _nn(w_scale), N,
                                                                       _nn(Y), _s(stream)))
+
+
+# ------------------------------------------------------------------ RMS norm, row-scaled int8 codes and products
+# Codes travel as torch.int8 tensors, scales as torch.float32 tensors with one
+# element for each token or channel.  These calls check shapes, dtypes and that
+# all tensors are on one device, and run on that device's current stream (the
+# caller's current device may be another) unless `stream` says otherwise.
+
+I8_DECODE_MAX_TOKENS = 64   # SLOPE_I8_DECODE_MAX_TOKENS
+I8_MAX_COLS = 1 << 18       # SLOPE_I8_MAX_COLS
+
+
+def _rows(t, name):
+    """(T, K) of a matrix with one token per row."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions [T, K], got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _arg(t, name, shape, dtype, like):
+    """Address of a contiguous tensor of this shape and dtype on `like`'s device."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    return t.data_ptr() if t.numel() else 256      # never dereferenced: the size is zero
+
+
+def _opt(t, name, shape, dtype, like):
+    return None if t is None else _arg(t, name, shape, dtype, like)
+
+
+def _buffer(t, name, like):
+    """(address, bytes) of a contiguous scratch or operand buffer on `like`'s device."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    n = t.numel() * t.element_size()
+    return (t.data_ptr() if n else 256), n
+
+
+def _on_device(fn, like, stream, *args):
+    """fn(*args, stream) on `like`'s device."""
+    dev = like.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live in GPU memory")
+    f = getattr(library(), fn)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, s)
+    if st != 0:
+        raise SlopeError(fn, st)
+
+
+def slope_rmsnorm(X, gamma, eps, residual=None, H=None, Y=None, q=None, q_scale=None, rstd=None, stream=None) -> None:
+    """h = X + residual; Y = h * rstd * gamma; q, q_scale its int8 codes and
+    scales; H, Y, (q, q_scale) and rstd are outputs, each may be None.  gamma:
+    X's dtype or float32, or None for ones."""
+    T, K = shape = _rows(X, "X")
+    dt = X.dtype
+    gdt = dt if gamma is None else gamma.dtype
+    _on_device("slope_rmsnorm", X, stream, _dt(dt), _arg(X, "X", shape, dt, X), _opt(residual, "residual", shape, dt, X),
+               _dt(gdt), _opt(gamma, "gamma", (K,), gdt, X), T, K, eps, _opt(H, "H", shape, dt, X),
+               _opt(Y, "Y", shape, dt, X), _opt(q, "q", shape, torch.int8, X),
+               _opt(q_scale, "q_scale", (T,), torch.float32, X), _opt(rstd, "rstd", (T,), torch.float32, X))
+
+
+def slope_rmsnorm_bwd_workspace_bytes(T: int, K: int) -> int:
+    b = ctypes.c_int64()
+    _check("slope_rmsnorm_bwd_workspace_bytes", library().slope_rmsnorm_bwd_workspace_bytes(T, K, ctypes.byref(b)))
+    return b.value
+
+
+def slope_rmsnorm_bwd(dY, H, rstd, gamma, dX=None, dgamma=None, workspace=None, dH=None, accumulate=False,
+                      stream=None) -> None:
+    """dX = gradient of X and residual (with dH, the gradient reaching h by other
+    ways, added); dgamma (added to with accumulate).  workspace:
+    slope_rmsnorm_bwd_workspace_bytes(T, K) bytes, needed with dgamma."""
+    T, K = shape = _rows(dY, "dY")
+    dt = dY.dtype
+    gdt = gamma.dtype if gamma is not None else dgamma.dtype if dgamma is not None else dt
+    wp, wb = _buffer(workspace, "workspace", dY)
+    _on_device("slope_rmsnorm_bwd", dY, stream, _dt(dt), _arg(dY, "dY", shape, dt, dY), _arg(H, "H", shape, dt, dY),
+               _arg(rstd, "rstd", (T,), torch.float32, dY), _dt(gdt), _opt(gamma, "gamma", (K,), gdt, dY),
+               _opt(dH, "dH", shape, dt, dY), T, K, _opt(dX, "dX", shape, dt, dY),
+               _opt(dgamma, "dgamma", (K,), gdt, dY), int(bool(accumulate)), wp, wb)
+
+
+def slope_quantize_rows_i8(X, q, scale, stream=None) -> None:
+    """int8 codes q [T, K] and scales [T] of the rows of a bf16 or fp16 X [T, K]."""
+    T, K = shape = _rows(X, "X")
+    _on_device("slope_quantize_rows_i8", X, stream, _dt(X), _arg(X, "X", shape, X.dtype, X), T, K,
+               _arg(q, "q", shape, torch.int8, X), _arg(scale, "scale", (T,), torch.float32, X))
+
+
+def slope_packed_sparse_i8_bytes(rows: int, cols: int) -> int:
+    b = ctypes.c_int64()
+    _check("slope_packed_sparse_i8_bytes", library().slope_packed_sparse_i8_bytes(rows, cols, ctypes.byref(b)))
+    return b.value
+
+
+def slope_pack_sparse_i8(values, meta, rows, cols, w_scale, packed, stream=None) -> None:
+    """int8 tile chunks of a compressed 16-bit matrix, with its rows' scales in w_scale [rows]."""
+    pp, pb = _buffer(packed, "packed", values)
+    _on_device("slope_pack_sparse_i8", values, stream, _dt(values),
+               _arg(values, "values", (rows, cols // 2), values.dtype, values),
+               _arg(meta, "meta", (rows, (cols // 4 + 7) // 8), torch.int32, values), rows, cols,
+               _arg(w_scale, "w_scale", (rows,), torch.float32, values), pp, pb)
+
+
+def _spmm_i8(fn, Xq, x_scale, packed_w, w_scale, N, Y, stream):
+    T, K = shape = _rows(Xq, "Xq")
+    pp, pb = _buffer(packed_w, "packed_w", Xq)
+    _on_device(fn, Xq, stream, _dt(Y), _arg(Xq, "Xq", shape, torch.int8, Xq),
+               _arg(x_scale, "x_scale", (T,), torch.float32, Xq), T, K, pp, pb,
+               _arg(w_scale, "w_scale", (N,), torch.float32, Xq), N, _arg(Y, "Y", (T, N), Y.dtype, Xq))
+
+
+def slope_spmm_i8_packed(Xq, x_scale, packed_w, w_scale, N, Y, stream=None) -> None:
+    """Y [T, N] = (Xq . W_q^T) * x_scale[t] * w_scale[n] on int8 codes, any T."""
+    _spmm_i8("slope_spmm_i8_packed", Xq, x_scale, packed_w, w_scale, N, Y, stream)
+
+
+def slope_spmm_i8_decode(Xq, x_scale, packed_w, w_scale, N, Y, stream=None) -> None:
+    """slope_spmm_i8_packed for at most I8_DECODE_MAX_TOKENS tokens: the same result, bit for bit."""
+    _spmm_i8("slope_spmm_i8_decode", Xq, x_scale, packed_w, w_scale, N, Y, stream)

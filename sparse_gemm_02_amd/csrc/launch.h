@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace slope {
 
 enum class Dt { F32 = 0, BF16 = 1, F16 = 2 };
@@ -174,5 +176,45 @@ hipError_t launch_pack_sparse_e4m3(Dt dt, const void* values, const uint32_t* me
                                    float* scale, void* packed, hipStream_t s);
 hipError_t launch_spmm_e4m3(Dt out, const uint8_t* Xq, const float* x_scale, int64_t T, int64_t Kred,
                             const void* packed, const float* w_scale, int64_t M, void* Y, hipStream_t s);
+
+// Raises a kernel's dynamic LDS limit, once on each device it is launched on
+// (one object per kernel, static; a device past the 64th sets it every time).
+struct LdsLimit {
+  std::atomic<uint64_t> done{0};
+  hipError_t set(const void* kernel, int bytes) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit & done.load(std::memory_order_acquire)) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
+
+// RMS norm with residual addition and int8 codes (each output may be null; q
+// and qs together), its gradient (part: rmsnorm_bwd_workspace_bytes(T, K) of
+// fp32 scratch, only used with dgamma), and the codes of plain rows.  gamma and
+// dgamma in gamma_dt (dt or F32).
+hipError_t launch_rmsnorm(Dt dt, const void* X, const void* res, Dt gamma_dt, const void* gamma, int64_t T, int64_t K,
+                          float eps, void* H, void* Y, int8_t* q, float* qs, float* rstd, hipStream_t s);
+int64_t rmsnorm_bwd_workspace_bytes(int64_t T, int64_t K);
+hipError_t launch_rmsnorm_bwd(Dt dt, const void* dY, const void* H, const float* rstd, Dt gamma_dt, const void* gamma,
+                              const void* dH, int64_t T, int64_t K, void* dX, void* dgamma, int accumulate,
+                              void* workspace, hipStream_t s);
+hipError_t launch_quantize_rows_i8(Dt dt, const void* X, int64_t T, int64_t K, int8_t* q, float* scale,
+                                   hipStream_t s);
+
+// int8 2:4 products: tile chunks of a compressed 16-bit matrix with a scale for
+// each row; Y [T, M] = (Xq . W_q^T) x_scale[t] w_scale[m], for any T and for T
+// <= 64 (the same results).
+int64_t packed_sparse_i8_bytes(int64_t rows, int64_t cols);
+hipError_t launch_pack_sparse_i8(Dt dt, const void* values, const uint32_t* meta, int64_t M, int64_t K, float* scale,
+                                 void* packed, hipStream_t s);
+hipError_t launch_spmm_i8(Dt out, const int8_t* Xq, const float* x_scale, int64_t T, int64_t K, const void* packed,
+                          const float* w_scale, int64_t M, void* Y, hipStream_t s);
+hipError_t launch_spmm_i8_decode(Dt out, const int8_t* Xq, const float* x_scale, int64_t T, int64_t K,
+                                 const void* packed, const float* w_scale, int64_t M, void* Y, hipStream_t s);
 
 }  // namespace slope
