@@ -274,86 +274,101 @@ hipError_t spmm_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, 
 
 // ---------------------------------------------------------------- few tokens
 // T <= 64: the weight's stream from HBM is the cost (0.625 bytes per dense
-// weight).  A block owns 32 rows and all of K; its waves take the stages in
-// turn and read their operands straight from memory into registers, U stages'
-// loads together.  The waves' int32 sums are added through LDS (exact in any
-// order), so one launch makes the output and nothing is scratch.
-constexpr int kDecodeWaves = 8, kDecodeStages = 4;
+// weight).  A block owns 32 FM rows and all of K; its W waves take the stages
+// in turn, and their int32 sums are added through LDS (exact in any order), so
+// one launch makes the output and nothing is scratch.  The weight goes straight
+// from memory into registers; X (which every block reads, from L2) comes as
+// whole 128-byte lines, eight lanes a token, and passes through the wave's own
+// piece of LDS, for a wave that loads its fragments from memory touches 32
+// lines with every load (64 tokens, 20480 -> 5120: 46 us that way, 23 so).
+//
+// Within a stage of 128 k the MFMA steps are not the stage's halves: step s
+// takes metadata words s (lanes 0..31) and 2 + s (lanes 32..63), so that a lane
+// needs two neighbouring words (one 8-byte load) and two neighbouring granules.
+// Its B operand is then k 32s + 16h .. and 64 + 32s + 16h .. (h = lane / 32).
+//
+// Measured (bf16 out; floor: the weight at a copy's 5.13 TB/s): 9216 -> 27648 at
+// 1 / 16 / 64 tokens 31.2 / 34.1 / 44.9 us (floor 31.0), 9216 -> 9216 11.1 /
+// 11.8 / 16.4 (10.3), 5120 -> 15360 10.4 / 10.7 / 12.6 (9.6), 20480 -> 5120 12.6
+// / 14.4 / 23.2 (12.8), 36864 -> 9216 42.3 / 50.8 / 74.4 (41.4).  At one token
+// HBM bounds it; at 64 the L1s, through which every block draws all of X.
+template <int FM>
+struct DecodeA {
+  i32x4 a[FM][2];
+  u32x2 ix[FM];
+};
 
-template <int FT, typename O>
-__global__ __launch_bounds__(64 * kDecodeWaves) void decode_i8_kernel(const int8_t* __restrict__ Xq,
-                                                                     const char* __restrict__ packed, int M, int T,
-                                                                     int Kred, const float* __restrict__ x_scale,
-                                                                     const float* __restrict__ w_scale,
-                                                                     O* __restrict__ Y) {
-  constexpr int W = kDecodeWaves, U = kDecodeStages;
-  __shared__ i32x4 sums[W][FT][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int stages = (Kred + kChunkCols - 1) / kChunkCols;
-  const int tile = blockIdx.x >> 3, r = (int)(blockIdx.x & 7) * 32 + (lane & 31);
-  const __amdgpu_buffer_rsrc_t ra = make_rsrc(packed + (int64_t)tile * stages * kChunkBytes, (int64_t)stages * kChunkBytes);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(Xq, (int64_t)T * Kred);
-  uint32_t a_off[2], m_off[2], x_off[FT];
+// The weight of the block's 32 FM rows, stage by stage.
+template <int FM>
+struct DecodeIn {
+  __amdgpu_buffer_rsrc_t ra;
+  uint32_t a_off[FM][2], m_off[FM];
+  int stages;
+  __device__ __forceinline__ DecodeIn(const char* packed, int Kred, int lane) {
+    constexpr int PER = kChunkRows / (32 * FM);      // blocks a row tile
+    stages = (Kred + kChunkCols - 1) / kChunkCols;
+    const int tile = blockIdx.x / PER, h = lane >> 5;
+    ra = make_rsrc(packed + (int64_t)tile * stages * kChunkBytes, (int64_t)stages * kChunkBytes);
 #pragma unroll
-  for (int ks = 0; ks < 2; ++ks) {
-    a_off[ks] = r * 64 + (((2 * ks + (lane >> 5)) ^ ((r >> 2) & 3)) << 4);
-    m_off[ks] = kChunkValueBytes + r * 16 + (2 * ks + (lane >> 5)) * 4;
-  }
+    for (int fm = 0; fm < FM; ++fm) {
+      const int r = (int)(blockIdx.x % PER) * 32 * FM + fm * 32 + (lane & 31);
 #pragma unroll
-  for (int ft = 0; ft < FT; ++ft) {
-    const int t = ft * 32 + (lane & 31);
-    x_off[ft] = t < T ? (uint32_t)t * Kred + 16 * (lane >> 5) : kOutOfRange;
-  }
-  i32x16 acc[FT];
-#pragma unroll
-  for (int ft = 0; ft < FT; ++ft) acc[ft] = i32x16{};
-  for (int sb = wave; sb < stages; sb += W * U) {
-    i32x4 a[U][2], lo[U][2][FT], hi[U][2][FT];
-    int ix[U][2];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int s = sb + u * W;
-      const bool live = s < stages;
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const uint32_t c = (uint32_t)s * kChunkBytes;
-        a[u][ks] = __builtin_bit_cast(i32x4, load16(ra, live ? c + a_off[ks] : kOutOfRange));
-        ix[u][ks] = (int)__builtin_amdgcn_raw_buffer_load_b32(ra, live ? c + m_off[ks] : kOutOfRange, 0, 0);
-        const int k0 = s * kChunkCols + 64 * ks;     // K % 16 == 0: 16 codes inside or outside a row
-        const bool in_lo = live && k0 + 16 * (lane >> 5) < Kred, in_hi = live && k0 + 32 + 16 * (lane >> 5) < Kred;
-#pragma unroll
-        for (int ft = 0; ft < FT; ++ft) {
-          const bool ok = x_off[ft] != kOutOfRange;
-          lo[u][ks][ft] = __builtin_bit_cast(i32x4, load16(rx, ok && in_lo ? x_off[ft] + k0 : kOutOfRange));
-          hi[u][ks][ft] = __builtin_bit_cast(i32x4, load16(rx, ok && in_hi ? x_off[ft] + k0 + 32 : kOutOfRange));
-        }
-      }
+      for (int s = 0; s < 2; ++s) a_off[fm][s] = r * 64 + (((2 * h + s) ^ ((r >> 2) & 3)) << 4);
+      m_off[fm] = kChunkValueBytes + r * 16 + h * 8;
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-        for (int ft = 0; ft < FT; ++ft) {
-          const i32x8 b = __builtin_shufflevector(lo[u][ks][ft], hi[u][ks][ft], 0, 1, 2, 3, 4, 5, 6, 7);
-          acc[ft] = __builtin_amdgcn_smfmac_i32_32x32x64_i8(a[u][ks], b, acc[ft], ix[u][ks], 0, 0);
-        }
   }
+  __device__ __forceinline__ void load(DecodeA<FM>& d, int s) const {
+    const uint32_t c = s < stages ? (uint32_t)s * kChunkBytes : kOutOfRange;   // beyond: zero codes
 #pragma unroll
-  for (int ft = 0; ft < FT; ++ft)
+    for (int fm = 0; fm < FM; ++fm) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      sums[wave][ft][q][lane] = i32x4{acc[ft][4 * q], acc[ft][4 * q + 1], acc[ft][4 * q + 2], acc[ft][4 * q + 3]};
+      for (int i = 0; i < 2; ++i) d.a[fm][i] = __builtin_bit_cast(i32x4, load16(ra, c + a_off[fm][i]));
+      d.ix[fm] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(ra, c + m_off[fm], 0, 0));
+    }
+  }
+};
+
+// The block's sums over its W waves (through `lds`, W / 2 * FM * FT * 4 KB: the
+// upper half of the waves hands its sums to the lower half first), scaled and
+// stored.  Columns t >= T are not.
+template <int W, int FM, int FT, typename O>
+__device__ __forceinline__ void decode_store(char* lds, const i32x16 (&acc)[FM][FT], int M, int T,
+                                             const float* __restrict__ x_scale, const float* __restrict__ w_scale,
+                                             O* __restrict__ Y) {
+  constexpr int HALF = W / 2, ALL = FM * FT * 256;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  i32x4* sums = reinterpret_cast<i32x4*>(lds);
+  __syncthreads();                                   // every wave is done with its X rows
+  i32x4* mine = sums + (wave % HALF) * ALL + lane;
+  if (wave >= HALF) {
+#pragma unroll
+    for (int f = 0; f < FM * FT; ++f)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const i32x16& v = acc[f / FT][f % FT];
+        mine[(f * 4 + q) * 64] = i32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
+  }
   __syncthreads();
-  // group g = (ft, q, lane): token ft*32 + lane%32, rows 8q + 4*(lane/32) .. +3
-  for (int g = threadIdx.x; g < FT * 4 * 64; g += 64 * W) {
-    const int ft = g >> 8, q = (g >> 6) & 3, l = g & 63;
-    const int t = ft * 32 + (l & 31);
-    const int64_t m = (int64_t)tile * kChunkRows + (blockIdx.x & 7) * 32 + 8 * q + 4 * (l >> 5);
-    if (t >= T || m >= M) continue;
-    i32x4 v = sums[0][ft][q][l];
+  if (wave < HALF) {
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += sums[w][ft][q][l];
+    for (int f = 0; f < FM * FT; ++f)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const i32x16& v = acc[f / FT][f % FT];
+        mine[(f * 4 + q) * 64] += i32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
+  }
+  __syncthreads();
+  // group g = (fm, ft, q, lane): token ft*32 + lane%32, rows fm*32 + 8q + 4*(lane/32) .. +3
+  for (int g = threadIdx.x; g < ALL; g += 64 * W) {
+    const int f = g >> 8, fm = f / FT, ft = f % FT, q = (g >> 6) & 3, l = g & 63;
+    const int t = ft * 32 + (l & 31);
+    const int64_t m = ((int64_t)blockIdx.x * FM + fm) * 32 + 8 * q + 4 * (l >> 5);
+    if (t >= T || m >= M) continue;
+    i32x4 v = sums[g];
+#pragma unroll
+    for (int w = 1; w < HALF; ++w) v += sums[w * ALL + g];
     const float st = x_scale[t];
     float y[4];
 #pragma unroll
@@ -362,17 +377,130 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void decode_i8_kernel(const int8
   }
 }
 
+// R loads of eight tokens bring a stage's X rows; D sets of G stages are in
+// flight.  No barrier in the loop, since no wave reads another's piece of LDS.
+// Lanes of columns t >= T read a row that is there (their sums are not stored).
+template <int R, int FM, int G, int D, int W, int WPS, typename O>
+__global__ __launch_bounds__(64 * W, WPS) void decode_i8_kernel(const int8_t* __restrict__ Xq,
+                                                                     const char* __restrict__ packed, int M, int T,
+                                                                     int Kred, const float* __restrict__ x_scale,
+                                                                     const float* __restrict__ w_scale,
+                                                                     O* __restrict__ Y) {
+  constexpr int FT = R > 4 ? 2 : 1, XB = R * 1024;   // LDS bytes of a stage's X rows
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const DecodeIn<FM> in(packed, Kred, lane);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(Xq, (int64_t)T * Kred);
+  char* own = lds + wave * (G * XB);
+  uint32_t x_src[R];
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const int t = j * 8 + (lane >> 3);
+    x_src[j] = (uint32_t)(t < T ? t : T - 1) * Kred;
+  }
+  const int c16 = (lane & 7) * 16;                   // this lane's granule of a row's 128 bytes
+  struct Set {
+    DecodeA<FM> a[G];
+    u32x4 x[G][R];
+  };
+  auto load_x = [&](Set& f, int s) {
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+      const int k = (s + u * W) * kChunkCols + c16;  // K % 16 == 0: a granule is inside or outside a row
+#pragma unroll
+      for (int j = 0; j < R; ++j) f.x[u][j] = load16(rx, k < Kred ? x_src[j] + k : kOutOfRange);
+    }
+  };
+  auto load_a = [&](Set& f, int s) {
+#pragma unroll
+    for (int u = 0; u < G; ++u) in.load(f.a[u], s + u * W);
+  };
+  i32x16 acc[FM][FT];
+#pragma unroll
+  for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+    for (int ft = 0; ft < FT; ++ft) acc[fm][ft] = i32x16{};
+  auto step = [&](Set& f, int s) {
+#pragma unroll
+    for (int u = 0; u < G; ++u)
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const int t = j * 8 + (lane >> 3);
+        *reinterpret_cast<u32x4*>(own + u * XB + t * 128 + (((lane & 7) ^ ((t ^ (t >> 3)) & 7)) << 4)) = f.x[u][j];
+      }
+    compiler_fence();                                // the wave's LDS operations run in order: no wait, no barrier
+    load_x(f, s + D * G * W);
+#pragma unroll
+    for (int u = 0; u < G; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int ft = 0; ft < FT; ++ft) {
+          const int t0 = ft * 32 + (lane & 31), t = t0 < 8 * R ? t0 : 8 * R - 1;
+          const int sw = (t ^ (t >> 3)) & 7, c = 2 * i + (lane >> 5);
+          const char* row = own + u * XB + t * 128;
+          const i32x4 lo = *reinterpret_cast<const i32x4*>(row + ((c ^ sw) << 4));
+          const i32x4 hi = *reinterpret_cast<const i32x4*>(row + (((c + 4) ^ sw) << 4));
+          const i32x8 b = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+          for (int fm = 0; fm < FM; ++fm)
+            acc[fm][ft] = __builtin_amdgcn_smfmac_i32_32x32x64_i8(f.a[u].a[fm][i], b, acc[fm][ft],
+                                                                  (int)f.a[u].ix[fm][i], 0, 0);
+        }
+    load_a(f, s + D * G * W);
+    compiler_fence();                                // the next step's writes stay behind these reads
+  };
+  Set f[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    load_x(f[d], wave + d * G * W);
+    load_a(f[d], wave + d * G * W);
+  }
+  for (int s = wave; s < in.stages; s += D * G * W) {
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (s + d * G * W < in.stages) step(f[d], s + d * G * W);
+  }
+  decode_store<W, FM, FT, O>(lds, acc, M, T, x_scale, w_scale, Y);
+}
+
+template <typename O>
+struct DecodeArgs {
+  const int8_t* Xq;
+  const char* packed;
+  int M, T, K;
+  const float *xs, *ws;
+  O* Y;
+  hipStream_t s;
+};
+template <int R, int FM, int G, int D, int W, int WPS, typename O>
+hipError_t decode_go(const DecodeArgs<O>& a) {
+  constexpr int FT = R > 4 ? 2 : 1;
+  constexpr int LDS = W * (G * R * 1024 > FM * FT * 2048 ? G * R * 1024 : FM * FT * 2048);   // X rows; sums
+  static LdsLimit limit;
+  auto kern = decode_i8_kernel<R, FM, G, D, W, WPS, O>;
+  const hipError_t e = limit.set((const void*)kern, LDS);
+  if (e != hipSuccess) return e;
+  kern<<<(unsigned)cdiv(a.M, 32 * FM), 64 * W, LDS, a.s>>>(a.Xq, a.packed, a.M, a.T, a.K, a.xs, a.ws, a.Y);
+  return hipGetLastError();
+}
+
+// 64 rows a block where that leaves 128 blocks or more (9216 outputs, 9216 wide,
+// 32 tokens: 11.9 us against 16.4 with 32 rows): every block draws all of X, so
+// wider ones draw it less often.  Below, 64 rows would leave too many compute
+// units idle (5120 outputs, 20480 wide, 32 tokens: 20.4 us against 16.6).
+// Waves, stages and sets as measured best over the five shapes above: the
+// registers are kept to 128 (two blocks a compute unit) up to 32 tokens; at 64
+// the 64-row block needs more, and four waves beat eight (44.9 against 46.8 us).
 template <typename O>
 hipError_t decode_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, const void* packed, const float* ws,
                          int64_t M, void* Y, hipStream_t s) {
-  const unsigned blocks = (unsigned)cdiv(M, 32);
-  if (T <= 32)
-    decode_i8_kernel<1, O><<<blocks, 64 * kDecodeWaves, 0, s>>>(Xq, (const char*)packed, (int)M, (int)T, (int)K, xs,
-                                                               ws, (O*)Y);
-  else
-    decode_i8_kernel<2, O><<<blocks, 64 * kDecodeWaves, 0, s>>>(Xq, (const char*)packed, (int)M, (int)T, (int)K, xs,
-                                                               ws, (O*)Y);
-  return hipGetLastError();
+  const DecodeArgs<O> a{Xq, (const char*)packed, (int)M, (int)T, (int)K, xs, ws, (O*)Y, s};
+  const bool wide = M > 127 * 64;
+  if (T <= 8) return wide ? decode_go<1, 2, 1, 2, 8, 4, O>(a) : decode_go<1, 1, 2, 2, 8, 4, O>(a);
+  if (T <= 16) return wide ? decode_go<2, 2, 1, 2, 8, 4, O>(a) : decode_go<2, 1, 1, 2, 16, 4, O>(a);
+  if (T <= 32) return wide ? decode_go<4, 2, 1, 1, 8, 4, O>(a) : decode_go<4, 1, 1, 2, 8, 4, O>(a);
+  return wide ? decode_go<8, 2, 1, 1, 4, 2, O>(a) : decode_go<8, 1, 1, 1, 8, 4, O>(a);
 }
 
 }  // namespace
