@@ -93,184 +93,321 @@ __device__ __forceinline__ void store4(O* p, const float (&y)[4]) {
 }
 
 // ---------------------------------------------------------------- the GEMM
-// 256 x 256 transposed output tile Out^T = W_q . Xq^T, eight waves of 128 x 64,
-// stages of 128 dense k in a ring of three LDS slots filled by buffer-to-LDS
-// loads; one barrier a stage, the slot refilled among the second k step's
-// MFMAs.  LDS granules: A row r c ^ ((r>>2)&3), B row r c ^ ((r^(r>>3))&7), so
-// that fragment reads are free of bank conflicts.
+// Transposed output tiles Out^T = W_q . Xq^T of BM x BT, stages of 128 dense k in
+// a ring of three LDS slots filled by buffer-to-LDS loads of 16 bytes a lane.
+// LDS granules: A row r c ^ ((r>>2)&3), B row r c ^ ((r^(r>>3))&7), so that
+// fragment reads are free of bank conflicts.  MFMA step s of a stage takes
+// granules 2h + s of A, words 2h + s of its metadata, and granules 2s + h and 4 +
+// 2s + h of B (h = lane / 32; the few-token kernel below says why).
+//
+// Every source and LDS address is kept and stepped (one add a load and stage):
+// with offsets, ring slots and bounds computed anew each stage the same schedule
+// took 436 us for 8192 x 9216 x 9216, against 389.
+template <int BM_, int BT_, int WGM_, int WGT_, int BLOCKS_>
 struct GeoI8 {
-  static constexpr int BM = 256, BT = 256, WGM = 2, WGT = 4, WAVES = 8, THREADS = 512;
+  static constexpr int BM = BM_, BT = BT_, WGM = WGM_, WGT = WGT_, WAVES = WGM * WGT, THREADS = 64 * WAVES;
   static constexpr int WM = BM / WGM, WT = BT / WGT, FM = WM / 32, FT = WT / 32;
-  static constexpr int KS = 128, NST = 3;
-  static constexpr int A_BYTES = BM * 64, B_BYTES = BT * 128, META_STAGE = BM * 16;
-  static constexpr int CHUNK_BYTES = A_BYTES + META_STAGE;
-  static constexpr int SLOT = A_BYTES + B_BYTES + META_STAGE, LDS_BYTES = NST * SLOT;
-  static constexpr int A_DMA = A_BYTES / 1024 / WAVES, B_DMA = B_BYTES / 1024 / WAVES, M_DMA = META_STAGE / 256 / WAVES;
-  static constexpr int DMA_PER_STAGE = A_DMA + B_DMA + M_DMA;
-  static_assert(CHUNK_BYTES == kChunkBytes && A_BYTES == kChunkValueBytes, "chunks are the stage slices");
-  static_assert(LDS_BYTES <= 160 * 1024, "LDS budget");
+  static constexpr int KS = kChunkCols, NST = 3;
+  static constexpr int BLOCKS = BLOCKS_;             // blocks a compute unit holds
+  static constexpr int A_BYTES = BM * 64, B_BYTES = BT * 128, META_BYTES = BM * 16;
+  static constexpr int SLOT = A_BYTES + B_BYTES + META_BYTES, LDS_BYTES = NST * SLOT;
+  // 1 KB loads of a wave and stage; the metadata's go to the first META_WAVES waves
+  static constexpr int A_DMA = A_BYTES / 1024 / WAVES, B_DMA = B_BYTES / 1024 / WAVES, META_WAVES = META_BYTES / 1024;
+  static constexpr int PER_CHUNK = kChunkRows / BM;  // tiles in a chunk's rows
+  static_assert(kChunkRows % BM == 0 && A_BYTES % (1024 * WAVES) == 0 && B_BYTES % (1024 * WAVES) == 0 &&
+                META_BYTES % 1024 == 0 && META_WAVES <= WAVES, "tile and wave split");
+  static_assert(BLOCKS * LDS_BYTES <= 160 * 1024, "LDS budget");
 };
 
-template <typename O>
-__global__ __launch_bounds__(GeoI8::THREADS, 1) void spmm_i8_kernel(const int8_t* __restrict__ Xq,
-                                                                  const char* __restrict__ packed, int M, int T,
-                                                                  int Kred, const float* __restrict__ x_scale,
-                                                                  const float* __restrict__ w_scale,
-                                                                  O* __restrict__ Y) {
-  typedef GeoI8 G;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave % G::WGM, wt = wave / G::WGM;
-  const int tiles_m = (M + G::BM - 1) / G::BM, tiles_t = (T + G::BT - 1) / G::BT;
-  int tm, tt;
-  tile_of_block(blockIdx.x, gridDim.x, tiles_m, tiles_t, 8, tm, tt);
-  const int64_t m0 = (int64_t)tm * G::BM, t0 = (int64_t)tt * G::BT;
-  const int stages = (Kred + G::KS - 1) / G::KS;
-  const int rows_t = (int)((T - t0) < G::BT ? (T - t0) : G::BT);
-  const __amdgpu_buffer_rsrc_t ra =
-      make_rsrc(packed + (int64_t)tm * stages * G::CHUNK_BYTES, (int64_t)stages * G::CHUNK_BYTES);
-  const __amdgpu_buffer_rsrc_t rb = make_rsrc(Xq + t0 * Kred, (int64_t)rows_t * Kred);
+template <class G>
+struct FragsI8 {                                     // one step's operands
+  i32x4 a[G::FM];
+  i32x8 b[G::FT];
+};
 
-  uint32_t b_src[G::B_DMA];
-  int b_k[G::B_DMA];
-#pragma unroll
-  for (int j = 0; j < G::B_DMA; ++j) {
-    const int row = wave * (G::BT / G::WAVES) + j * 8 + (lane >> 3);
-    const int c = (lane & 7) ^ ((row ^ (row >> 3)) & 7);
-    b_src[j] = (uint32_t)row * Kred + c * 16;
-    b_k[j] = c * 16;                                 // first k of the granule within the stage
-  }
-  auto issue = [&](int s) {
-    char* base = lds + (s % G::NST) * G::SLOT;
-    const uint32_t chunk = (uint32_t)s * G::CHUNK_BYTES;
-    const bool live = s < stages;
-#pragma unroll
-    for (int j = 0; j < G::A_DMA; ++j) {
-      const uint32_t part = wave * (G::A_BYTES / G::WAVES) + j * 1024;
-      dma16(ra, base + part, live ? chunk + part + lane * 16 : kOutOfRange);
-    }
+// What a wave of a tile loads, reads and stores.
+template <class G>
+struct TileI8 {
+  __amdgpu_buffer_rsrc_t ra, rb;
+  char* lds;
+  int lane, wave, wm, wt, stages, M, T;
+  int64_t m0, t0;
+  // Next stage's source offsets.  Past the last stage A's lie beyond its resource
+  // (zeros), B's in the next row or beyond; neither is multiplied.  A stage that
+  // ends past K brings the next row's first codes too: the weight's codes there
+  // are zero.
+  uint32_t a_src, m_src, b_src[G::B_DMA];
+  int a_off[2], m_off, b_off[2][G::FT][2];           // fragment addresses within a slot
+
+  // tile (tm, tt) of BM rows and BT tokens
+  __device__ __forceinline__ TileI8(char* lds_, const int8_t* Xq, const char* packed, int M_, int T_, int Kred, int tm,
+                                    int tt)
+      : lds(lds_), M(M_), T(T_) {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    wm = wave % G::WGM;
+    wt = wave / G::WGM;
+    m0 = (int64_t)tm * G::BM;
+    t0 = (int64_t)tt * G::BT;
+    stages = (Kred + G::KS - 1) / G::KS;
+    const int rows_t = (int)((T - t0) < G::BT ? (T - t0) : G::BT);
+    ra = make_rsrc(packed + (int64_t)(tm / G::PER_CHUNK) * stages * kChunkBytes, (int64_t)stages * kChunkBytes);
+    rb = make_rsrc(Xq + t0 * Kred, (int64_t)rows_t * Kred);
+    const uint32_t row0 = (uint32_t)(tm % G::PER_CHUNK) * G::BM;    // the tile's first row within the chunk
+    a_src = row0 * 64 + wave * (G::A_BYTES / G::WAVES) + lane * 16;
+    m_src = kChunkValueBytes + row0 * 16 + wave * 1024 + lane * 16;
 #pragma unroll
     for (int j = 0; j < G::B_DMA; ++j) {
-      const bool ok = live && s * G::KS + b_k[j] < Kred;
-      dma16(rb, base + G::A_BYTES + wave * (G::B_BYTES / G::WAVES) + j * 1024, ok ? b_src[j] + s * G::KS : kOutOfRange);
+      const int row = wave * (G::BT / G::WAVES) + j * 8 + (lane >> 3);
+      b_src[j] = (uint32_t)row * Kred + (((lane & 7) ^ ((row ^ (row >> 3)) & 7)) << 4);
     }
+    const int h = lane >> 5, arow = wm * G::WM + (lane & 31);
+    m_off = G::A_BYTES + G::B_BYTES + arow * 16 + h * 8;
 #pragma unroll
-    for (int j = 0; j < G::M_DMA; ++j) {
-      const uint32_t part = wave * (G::META_STAGE / G::WAVES) + j * 256;
-      dma4(ra, base + G::A_BYTES + G::B_BYTES + part, live ? chunk + G::A_BYTES + part + lane * 4 : kOutOfRange);
-    }
-  };
-
-  int a_off[2][G::FM], m_off[2][G::FM], b_off[2][G::FT][2];
+    for (int s = 0; s < 2; ++s) {
+      a_off[s] = arow * 64 + (((2 * h + s) ^ ((arow >> 2) & 3)) << 4);
 #pragma unroll
-  for (int fm = 0; fm < G::FM; ++fm) {
-    const int row = wm * G::WM + fm * 32 + (lane & 31);
-    const int sw = (row >> 2) & 3;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      a_off[ks][fm] = row * 64 + (((2 * ks + (lane >> 5)) ^ sw) * 16);
-      m_off[ks][fm] = G::A_BYTES + G::B_BYTES + row * 16 + (2 * ks + (lane >> 5)) * 4;
+      for (int ft = 0; ft < G::FT; ++ft) {
+        const int row = wt * G::WT + ft * 32 + (lane & 31), sw = (row ^ (row >> 3)) & 7;
+        b_off[s][ft][0] = G::A_BYTES + row * 128 + (((2 * s + h) ^ sw) << 4);
+        b_off[s][ft][1] = G::A_BYTES + row * 128 + (((4 + 2 * s + h) ^ sw) << 4);
+      }
     }
   }
+  static __device__ __forceinline__ int after(int slot) { return slot == (G::NST - 1) * G::SLOT ? 0 : slot + G::SLOT; }
+  // this wave's share of the next stage, into the slot at `slot`
+  __device__ __forceinline__ void issue(int slot) {
+    char* a = lds + slot + wave * (G::A_BYTES / G::WAVES);
 #pragma unroll
-  for (int ft = 0; ft < G::FT; ++ft) {
-    const int row = wt * G::WT + ft * 32 + (lane & 31);
-    const int sw = (row ^ (row >> 3)) & 7;
+    for (int j = 0; j < G::A_DMA; ++j) dma16(ra, a + j * 1024, a_src + j * 1024);
+    char* b = lds + slot + G::A_BYTES + wave * (G::B_BYTES / G::WAVES);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      b_off[ks][ft][0] = G::A_BYTES + row * 128 + (((4 * ks + (lane >> 5)) ^ sw) * 16);
-      b_off[ks][ft][1] = G::A_BYTES + row * 128 + (((4 * ks + 2 + (lane >> 5)) ^ sw) * 16);
-    }
+    for (int j = 0; j < G::B_DMA; ++j) dma16(rb, b + j * 1024, b_src[j]);
+    if (wave < G::META_WAVES) dma16(ra, lds + slot + G::A_BYTES + G::B_BYTES + wave * 1024, m_src);
+    a_src += kChunkBytes;
+    m_src += kChunkBytes;
+#pragma unroll
+    for (int j = 0; j < G::B_DMA; ++j) b_src[j] += G::KS;
   }
-  struct Frags {
-    i32x4 a[G::FM];
-    int ix[G::FM];
-    i32x8 b[G::FT];
-  };
-  auto read_frags = [&](Frags& f, int s, int ks) {
-    const char* base = lds + (s % G::NST) * G::SLOT;
+  // until this wave's share of all but its newest stage is in LDS
+  __device__ __forceinline__ void wait_older() const {
+    if (wave < G::META_WAVES) wait_vmcnt<G::A_DMA + G::B_DMA + 1>();
+    else wait_vmcnt<G::A_DMA + G::B_DMA>();
+  }
+  __device__ __forceinline__ void read_meta(u32x2 (&x)[G::FM], int slot) const {
 #pragma unroll
-    for (int fm = 0; fm < G::FM; ++fm) {
-      f.a[fm] = *reinterpret_cast<const i32x4*>(base + a_off[ks][fm]);
-      f.ix[fm] = *reinterpret_cast<const int*>(base + m_off[ks][fm]);
-    }
+    for (int fm = 0; fm < G::FM; ++fm) x[fm] = *reinterpret_cast<const u32x2*>(lds + slot + m_off + fm * 512);
+  }
+  __device__ __forceinline__ void read(FragsI8<G>& f, int slot, int s) const {
 #pragma unroll
     for (int ft = 0; ft < G::FT; ++ft) {
-      const i32x4 lo = *reinterpret_cast<const i32x4*>(base + b_off[ks][ft][0]);
-      const i32x4 hi = *reinterpret_cast<const i32x4*>(base + b_off[ks][ft][1]);
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(lds + slot + b_off[s][ft][0]);
+      const i32x4 hi = *reinterpret_cast<const i32x4*>(lds + slot + b_off[s][ft][1]);
       f.b[ft] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
-  };
-  i32x16 acc[G::FM][G::FT];
+#pragma unroll
+    for (int fm = 0; fm < G::FM; ++fm) f.a[fm] = *reinterpret_cast<const i32x4*>(lds + slot + a_off[s] + fm * 2048);
+  }
+  static __device__ __forceinline__ void multiply(i32x16 (&acc)[G::FM][G::FT], const FragsI8<G>& f,
+                                                  const u32x2 (&x)[G::FM], int s, int ft) {
+#pragma unroll
+    for (int fm = 0; fm < G::FM; ++fm)
+      acc[fm][ft] = __builtin_amdgcn_smfmac_i32_32x32x64_i8(f.a[fm], f.b[ft], acc[fm][ft], (int)x[fm][s], 0, 0);
+  }
+  // The sums scaled and stored to Y[t][m].  The lane's scales are all loaded
+  // first, from clamped, valid places (a load behind a bounds test would be
+  // waited for by itself); M % 4 == 0: four rows are all inside or all outside.
+  template <typename O>
+  __device__ __forceinline__ void store(const i32x16 (&acc)[G::FM][G::FT], const float* __restrict__ x_scale,
+                                        const float* __restrict__ w_scale, O* __restrict__ Y) const {
+    float st[G::FT];
+    Pack<float, 4> sn[G::FM][4];
+    const int64_t tl = t0 + wt * G::WT + (lane & 31), ml = m0 + wm * G::WM + 4 * (lane >> 5);
+#pragma unroll
+    for (int ft = 0; ft < G::FT; ++ft) st[ft] = x_scale[tl + ft * 32 < T ? tl + ft * 32 : T - 1];
+#pragma unroll
+    for (int fm = 0; fm < G::FM; ++fm)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t m = ml + fm * 32 + 8 * q;
+        sn[fm][q] = load_pack<float, 4>(w_scale + (m < M ? m : M - 4));
+      }
+#pragma unroll
+    for (int ft = 0; ft < G::FT; ++ft) {
+      const int64_t t = tl + ft * 32;
+      if (t >= T) continue;
+#pragma unroll
+      for (int fm = 0; fm < G::FM; ++fm) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t m = ml + fm * 32 + 8 * q;
+          if (m >= M) continue;
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = scaled(acc[fm][ft][4 * q + i], st[ft], sn[fm][q].v[i]);
+          store4<O>(Y + t * M + m, y);
+        }
+      }
+    }
+  }
+};
+
+template <class G>
+__device__ __forceinline__ void clear_acc(i32x16 (&acc)[G::FM][G::FT]) {
 #pragma unroll
   for (int fm = 0; fm < G::FM; ++fm)
 #pragma unroll
     for (int ft = 0; ft < G::FT; ++ft) acc[fm][ft] = i32x16{};
-  auto mma_col = [&](const Frags& f, int ft) {
-#pragma unroll
-    for (int fm = 0; fm < G::FM; ++fm)
-      acc[fm][ft] = __builtin_amdgcn_smfmac_i32_32x32x64_i8(f.a[fm], f.b[ft], acc[fm][ft], f.ix[fm], 0, 0);
-  };
-  auto mma = [&](const Frags& f) {
-#pragma unroll
-    for (int ft = 0; ft < G::FT; ++ft) mma_col(f, ft);
-  };
+}
 
-#pragma unroll
-  for (int p = 0; p < G::NST; ++p) issue(p);
-  wait_vmcnt<G::DMA_PER_STAGE * (G::NST - 1)>();
+// Small tiles, several blocks a compute unit: each step's fragments are read
+// ahead of the step before, one barrier a stage, the slot refilled among the
+// second step's MFMAs; while one block waits, another multiplies.
+template <class G, typename O>
+__global__ __launch_bounds__(G::THREADS, G::BLOCKS* G::WAVES / 4) void spmm_i8_kernel(
+    const int8_t* __restrict__ Xq, const char* __restrict__ packed, int M, int T, int Kred,
+    const float* __restrict__ x_scale, const float* __restrict__ w_scale, O* __restrict__ Y) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  int tm, tt;
+  tile_of_block(blockIdx.x, gridDim.x, (M + G::BM - 1) / G::BM, (T + G::BT - 1) / G::BT, 8, tm, tt);
+  TileI8<G> t(lds, Xq, packed, M, T, Kred, tm, tt);
+  i32x16 acc[G::FM][G::FT];
+  clear_acc<G>(acc);
+  t.issue(0);
+  t.issue(G::SLOT);
+  t.wait_older();
   barrier();
   compiler_fence();
-  Frags f0, f1;
-  read_frags(f0, 0, 0);
-  for (int s = 0; s < stages; ++s) {
-    read_frags(f1, s, 1);
-    mma(f0);
+  FragsI8<G> f0, f1;
+  u32x2 x0[G::FM], x1[G::FM];
+  int cur = 0, next = G::SLOT, refill = 2 * G::SLOT;
+  t.issue(refill);
+  t.read_meta(x0, cur);
+  t.read(f0, cur, 0);
+  for (int s = 0; s < t.stages; ++s) {
+    t.read(f1, cur, 1);
+#pragma unroll
+    for (int ft = 0; ft < G::FT; ++ft) t.multiply(acc, f0, x0, 0, ft);
     __builtin_amdgcn_sched_barrier(0);
-    wait_lgkmcnt0();
-    wait_vmcnt<G::DMA_PER_STAGE * (G::NST - 2)>();
+    wait_lgkmcnt0();                                 // this wave's reads of the stage are complete
+    t.wait_older();
     barrier();
-    if (s + 1 < stages) read_frags(f0, s + 1, 0);
-    mma_col(f1, 0);
+    compiler_fence();
+    t.read_meta(x1, next);                           // (past the last stage: a slot of earlier codes, not multiplied)
+    t.read(f0, next, 0);
+    t.multiply(acc, f1, x0, 1, 0);
     __builtin_amdgcn_sched_barrier(0);
-    issue(s + G::NST);
+    t.issue(cur);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int ft = 1; ft < G::FT; ++ft) mma_col(f1, ft);
+    for (int ft = 1; ft < G::FT; ++ft) t.multiply(acc, f1, x0, 1, ft);
+#pragma unroll
+    for (int fm = 0; fm < G::FM; ++fm) x0[fm] = x1[fm];
+    cur = next;
+    next = t.after(next);
   }
   wait_vmcnt<0>();
+  t.store(acc, x_scale, w_scale, Y);
+}
+
+// The large tiles, eight waves in two groups half a stage apart (waves 0..3 and
+// 4..7, one of each on every SIMD).  While one group multiplies a stage, the
+// other reads its fragments of it from LDS and issues its share of the stage
+// after next, then they change places; a barrier ends each phase.  A wave's LDS
+// reads are complete before the barrier that ends its memory phase, so a slot is
+// free (both groups have read it) in the phase its refill is issued.
+template <class G, typename O>
+__device__ __forceinline__ void ping_pong_tile(char* lds, const int8_t* Xq, const char* packed, int M, int T, int Kred,
+                                               int tm, int tt, const float* __restrict__ x_scale,
+                                               const float* __restrict__ w_scale, O* __restrict__ Y) {
+  static_assert(G::WAVES == 8 && G::NST == 3, "two groups of four waves, three slots");
+  TileI8<G> t(lds, Xq, packed, M, T, Kred, tm, tt);
+  FragsI8<G> f[2];
+  u32x2 x[G::FM];
+  i32x16 acc[G::FM][G::FT];
+  clear_acc<G>(acc);
+  auto phase_end = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+    compiler_fence();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int cur = 0, refill = 2 * G::SLOT;
+  auto memory_phase = [&]() {
+    t.read_meta(x, cur);
+    t.read(f[0], cur, 0);
+    t.read(f[1], cur, 1);
+    t.issue(refill);
+    cur = t.after(cur);
+    refill = t.after(refill);
+    wait_lgkmcnt0();
+  };
+  auto multiply_phase = [&]() {
 #pragma unroll
-  for (int ft = 0; ft < G::FT; ++ft) {
-    const int64_t t = t0 + wt * G::WT + ft * 32 + (lane & 31);
-    if (t >= T) continue;
-    const float st = x_scale[t];
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int fm = 0; fm < G::FM; ++fm) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t m = m0 + wm * G::WM + fm * 32 + 8 * q + 4 * (lane >> 5);
-        if (m >= M) continue;                        // M % 4 == 0: all four inside or outside
-        float y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = scaled(acc[fm][ft][4 * q + i], st, w_scale[m + i]);
-        store4<O>(Y + t * M + m, y);
-      }
+      for (int ft = 0; ft < G::FT; ++ft) t.multiply(acc, f[s], x, s, ft);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  t.issue(0);
+  t.issue(G::SLOT);
+  t.wait_older();
+  phase_end();
+  if (t.wave < 4) {
+    for (int s = 0; s < t.stages; ++s) {
+      memory_phase();
+      phase_end();
+      multiply_phase();
+      t.wait_older();                                // this wave's share of stage s + 1 is there
+      phase_end();
     }
+    phase_end();
+  } else {
+    phase_end();
+    for (int s = 0; s < t.stages; ++s) {
+      memory_phase();
+      t.wait_older();
+      phase_end();
+      multiply_phase();
+      phase_end();
+    }
+  }
+  wait_vmcnt<0>();
+  t.store(acc, x_scale, w_scale, Y);
+}
+
+typedef GeoI8<256, 256, 2, 4, 1> FullI8;
+typedef GeoI8<256, 128, 4, 2, 1> HalfI8;
+typedef GeoI8<128, 128, 2, 2, 2> SmallI8;
+
+// The first rows_full row tiles in 256 x 256 tiles, the others in 256 x 128
+// (full_width_rows: a grid that would end in a partly filled round of blocks
+// ends sooner so; 8192 x 9216 x 9216 has 4.5 rounds of full tiles).
+template <typename O>
+__global__ __launch_bounds__(FullI8::THREADS, 2) void spmm_i8_large_kernel(
+    const int8_t* __restrict__ Xq, const char* __restrict__ packed, int M, int T, int Kred, int rows_full,
+    const float* __restrict__ x_scale, const float* __restrict__ w_scale, O* __restrict__ Y) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int rows = (M + 255) / 256, full = (T + 255) / 256 * rows_full;
+  int tm, tt;
+  if ((int)blockIdx.x < full) {
+    tile_of_block(blockIdx.x, full, rows_full, (T + 255) / 256, 8, tm, tt);
+    ping_pong_tile<FullI8, O>(lds, Xq, packed, M, T, Kred, tm, tt, x_scale, w_scale, Y);
+  } else {
+    tile_of_block(blockIdx.x - full, gridDim.x - full, rows - rows_full, (T + 127) / 128, 8, tm, tt);
+    ping_pong_tile<HalfI8, O>(lds, Xq, packed, M, T, Kred, rows_full + tm, tt, x_scale, w_scale, Y);
   }
 }
 
 template <typename O>
-hipError_t spmm_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, const void* packed, const float* ws,
-                       int64_t M, void* Y, hipStream_t s) {
-  typedef GeoI8 G;
-  const int64_t nb = cdiv(M, G::BM) * cdiv(T, G::BT);
-  auto kern = spmm_i8_kernel<O>;
-  static LdsLimit limit;
-  const hipError_t e = limit.set((const void*)kern, G::LDS_BYTES);
-  if (e != hipSuccess) return e;
-  kern<<<(unsigned)nb, G::THREADS, G::LDS_BYTES, s>>>(Xq, (const char*)packed, (int)M, (int)T, (int)K, xs, ws, (O*)Y);
-  return hipGetLastError();
-}
+struct SpmmArgs {
+  const int8_t* Xq;
+  const char* packed;
+  int M, T, K;
+  const float *xs, *ws;
+  O* Y;
+  hipStream_t s;
+};
 
 // ---------------------------------------------------------------- few tokens
 // T <= 64: the weight's stream from HBM is the cost (0.625 bytes per dense
@@ -390,6 +527,9 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_i8_kernel(const int8_t* __
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const DecodeIn<FM> in(packed, Kred, lane);
+  const int64_t t0 = (int64_t)blockIdx.y * (8 * R);  // the block's tokens (all of them up to 64)
+  Xq += t0 * Kred;
+  T = T - t0 < 8 * R ? (int)(T - t0) : 8 * R;
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(Xq, (int64_t)T * Kred);
   char* own = lds + wave * (G * XB);
   uint32_t x_src[R];
@@ -461,27 +601,18 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_i8_kernel(const int8_t* __
     for (int d = 0; d < D; ++d)
       if (s + d * G * W < in.stages) step(f[d], s + d * G * W);
   }
-  decode_store<W, FM, FT, O>(lds, acc, M, T, x_scale, w_scale, Y);
+  decode_store<W, FM, FT, O>(lds, acc, M, T, x_scale + t0, w_scale, Y + t0 * M);
 }
 
-template <typename O>
-struct DecodeArgs {
-  const int8_t* Xq;
-  const char* packed;
-  int M, T, K;
-  const float *xs, *ws;
-  O* Y;
-  hipStream_t s;
-};
 template <int R, int FM, int G, int D, int W, int WPS, typename O>
-hipError_t decode_go(const DecodeArgs<O>& a) {
+hipError_t decode_go(const SpmmArgs<O>& a) {
   constexpr int FT = R > 4 ? 2 : 1;
   constexpr int LDS = W * (G * R * 1024 > FM * FT * 2048 ? G * R * 1024 : FM * FT * 2048);   // X rows; sums
   static LdsLimit limit;
   auto kern = decode_i8_kernel<R, FM, G, D, W, WPS, O>;
   const hipError_t e = limit.set((const void*)kern, LDS);
   if (e != hipSuccess) return e;
-  kern<<<(unsigned)cdiv(a.M, 32 * FM), 64 * W, LDS, a.s>>>(a.Xq, a.packed, a.M, a.T, a.K, a.xs, a.ws, a.Y);
+  kern<<<dim3((unsigned)cdiv(a.M, 32 * FM), (unsigned)cdiv(a.T, 8 * R)), 64 * W, LDS, a.s>>>(a.Xq, a.packed, a.M, a.T, a.K, a.xs, a.ws, a.Y);
   return hipGetLastError();
 }
 
@@ -495,12 +626,52 @@ hipError_t decode_go(const DecodeArgs<O>& a) {
 template <typename O>
 hipError_t decode_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, const void* packed, const float* ws,
                          int64_t M, void* Y, hipStream_t s) {
-  const DecodeArgs<O> a{Xq, (const char*)packed, (int)M, (int)T, (int)K, xs, ws, (O*)Y, s};
+  const SpmmArgs<O> a{Xq, (const char*)packed, (int)M, (int)T, (int)K, xs, ws, (O*)Y, s};
   const bool wide = M > 127 * 64;
   if (T <= 8) return wide ? decode_go<1, 2, 1, 2, 8, 4, O>(a) : decode_go<1, 1, 2, 2, 8, 4, O>(a);
   if (T <= 16) return wide ? decode_go<2, 2, 1, 2, 8, 4, O>(a) : decode_go<2, 1, 1, 2, 16, 4, O>(a);
   if (T <= 32) return wide ? decode_go<4, 2, 1, 1, 8, 4, O>(a) : decode_go<4, 1, 1, 2, 8, 4, O>(a);
   return wide ? decode_go<8, 2, 1, 1, 4, 2, O>(a) : decode_go<8, 1, 1, 1, 8, 4, O>(a);
+}
+
+// Any number of tokens.  Three kernels, chosen by their estimated time in units
+// of a stage (us for 128 k), fitted to sweeps of 65 .. 8192 tokens over 9216 ->
+// 9216 / 27648, 20480 -> 5120, 5120 -> 5120 / 15360 and 768 -> 2304:
+//   large   0.010 a unit of full_width_rows' cost (100 a round of full tiles, 65
+//           of half tiles)
+//   small   128 x 128 tiles, two a compute unit: 0.42 up to one a unit, then
+//           0.35 + 0.0014 a tile
+//   direct  the few-token kernel over groups of 64 tokens: 0.13 + 0.0006 a block
+// Measured, us (large / small / direct): 9216 -> 9216 at 128 tokens 40 / 29.5 /
+// 24, 256: 41 / 31 / 37, 512: 42 / 49 / 62, 1000: 65 / 79 / 111, 8192: 380 / 491 /
+// 895; 20480 -> 5120 at 256: 79 / 58 / 51, 512: 80 / 59 / 78, 1000: 85 / 103 / 130.
+template <typename O>
+hipError_t spmm_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, const void* packed, const float* ws,
+                       int64_t M, void* Y, hipStream_t s) {
+  const SpmmArgs<O> a{Xq, (const char*)packed, (int)M, (int)T, (int)K, xs, ws, (O*)Y, s};
+  const int64_t cus = device_compute_units(), rows = cdiv(M, 256), cols = cdiv(T, 256), halves = cdiv(T, 128);
+  const int64_t rows_full = full_width_rows(rows, cols, halves, cus);
+  const double large = 0.010 * (100 * cdiv(rows_full * cols, cus) + 65 * cdiv((rows - rows_full) * halves, cus));
+  const int64_t tiles = cdiv(M, 128) * halves;
+  const double small = tiles <= cus ? 0.42 : 0.35 + 0.0014 * (256.0 / cus) * tiles;
+  const double direct = 0.13 + 0.0006 * (256.0 / cus) * (cdiv(M, 64) * cdiv(T, 64));
+  if (direct <= small && direct <= large) return decode_go<8, 2, 1, 1, 4, 2, O>(a);
+  if (small <= large) {
+    static LdsLimit limit;
+    auto kern = spmm_i8_kernel<SmallI8, O>;
+    const hipError_t e = limit.set((const void*)kern, SmallI8::LDS_BYTES);
+    if (e != hipSuccess) return e;
+    kern<<<(unsigned)tiles, SmallI8::THREADS, SmallI8::LDS_BYTES, s>>>(a.Xq, a.packed, a.M, a.T, a.K, xs, ws, a.Y);
+    return hipGetLastError();
+  }
+  static LdsLimit limit;
+  auto kern = spmm_i8_large_kernel<O>;
+  const hipError_t e = limit.set((const void*)kern, FullI8::LDS_BYTES);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = rows_full * cols + (rows - rows_full) * halves;
+  kern<<<(unsigned)blocks, FullI8::THREADS, FullI8::LDS_BYTES, s>>>(a.Xq, a.packed, a.M, a.T, a.K, (int)rows_full, xs,
+                                                                    ws, a.Y);
+  return hipGetLastError();
 }
 
 }  // namespace

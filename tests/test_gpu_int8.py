@@ -135,6 +135,16 @@ def test_product(T, K, N, out):
     assert np.array_equal(c.run(S.slope_spmm_i8_packed, out), c.ref(out))
 
 
+# grids of every kind: full tiles with a last rows of half tiles, half tiles
+# alone, full tiles alone, small tiles; ragged in all three sizes
+@pytest.mark.parametrize("T,K,N", [(4100, 144, 4612), (500, 272, 9216), (1000, 400, 9220), (515, 656, 4100),
+                                   (2050, 128, 9220), (1000, 16, 2304)])
+def test_product_on_many_tiles(T, K, N):
+    say(f"[i8 product] T={T} K={K} N={N}")
+    c = Case(T, K, N, seed=T + N)
+    assert np.array_equal(c.run(S.slope_spmm_i8_packed, "bf16"), c.ref("bf16"))
+
+
 @pytest.mark.parametrize("T", [2, 80])
 def test_long_sums_stay_in_int32(T):
     """The widest reduction with codes at the ends of int8: sums next to 2^31."""
