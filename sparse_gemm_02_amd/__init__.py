@@ -534,6 +534,12 @@ I8_DECODE_MAX_TOKENS = 64   # SLOPE_I8_DECODE_MAX_TOKENS
 I8_MAX_COLS = 1 << 18       # SLOPE_I8_MAX_COLS
 
 
+# raw handle of a device's current stream (torch.cuda.current_stream builds a
+# Stream object first, 2 us of a 10 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _rows(t, name):
     """(T, K) of a matrix with one token per row."""
     if t.dim() != 2:
@@ -541,45 +547,45 @@ def _rows(t, name):
     return t.shape
 
 
-def _arg(t, name, shape, dtype, like):
-    """Address of a contiguous tensor of this shape and dtype on `like`'s device."""
+def _place(index):
+    return "the CPU" if index < 0 else f"GPU {index}"
+
+
+def _arg(t, name, shape, dtype, dev):
+    """Address of a contiguous tensor of this shape and dtype on device `dev`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr() or 256                 # no elements: never dereferenced
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    return t.data_ptr() if t.numel() else 256      # never dereferenced: the size is zero
+    raise ValueError(f"{name} is on {_place(t.get_device())}, not on {_place(dev)}")
 
 
-def _opt(t, name, shape, dtype, like):
-    return None if t is None else _arg(t, name, shape, dtype, like)
+def _opt(t, name, shape, dtype, dev):
+    return None if t is None else _arg(t, name, shape, dtype, dev)
 
 
-def _buffer(t, name, like):
-    """(address, bytes) of a contiguous scratch or operand buffer on `like`'s device."""
+def _buffer(t, name, dev):
+    """(address, bytes) of a contiguous scratch or operand buffer on device `dev`."""
     if t is None:
         return None, 0
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    n = t.numel() * t.element_size()
-    return (t.data_ptr() if n else 256), n
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {_place(t.get_device())}, not on {_place(dev)}")
+    return t.data_ptr() or 256, t.numel() * t.element_size()
 
 
-def _on_device(fn, like, stream, *args):
-    """fn(*args, stream) on `like`'s device."""
-    dev = like.device
-    if dev.type != "cuda":
+def _on_device(fn, dev, stream, *args):
+    """The library's fn(*args, stream) on device `dev`."""
+    if dev < 0:
         raise ValueError("tensors must live in GPU memory")
-    f = getattr(library(), fn)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev.index == torch.cuda.current_device():
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    f = getattr(_lib or library(), fn)
+    if dev == torch.cuda.current_device():
         st = f(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -593,12 +599,12 @@ def slope_rmsnorm(X, gamma, eps, residual=None, H=None, Y=None, q=None, q_scale=
     scales; H, Y, (q, q_scale) and rstd are outputs, each may be None.  gamma:
     X's dtype or float32, or None for ones."""
     T, K = shape = _rows(X, "X")
-    dt = X.dtype
+    dt, d = X.dtype, X.get_device()
     gdt = dt if gamma is None else gamma.dtype
-    _on_device("slope_rmsnorm", X, stream, _dt(dt), _arg(X, "X", shape, dt, X), _opt(residual, "residual", shape, dt, X),
-               _dt(gdt), _opt(gamma, "gamma", (K,), gdt, X), T, K, eps, _opt(H, "H", shape, dt, X),
-               _opt(Y, "Y", shape, dt, X), _opt(q, "q", shape, torch.int8, X),
-               _opt(q_scale, "q_scale", (T,), torch.float32, X), _opt(rstd, "rstd", (T,), torch.float32, X))
+    _on_device("slope_rmsnorm", d, stream, _dt(dt), _arg(X, "X", shape, dt, d), _opt(residual, "residual", shape, dt, d),
+               _dt(gdt), _opt(gamma, "gamma", (K,), gdt, d), T, K, eps, _opt(H, "H", shape, dt, d),
+               _opt(Y, "Y", shape, dt, d), _opt(q, "q", shape, torch.int8, d),
+               _opt(q_scale, "q_scale", (T,), torch.float32, d), _opt(rstd, "rstd", (T,), torch.float32, d))
 
 
 def slope_rmsnorm_bwd_workspace_bytes(T: int, K: int) -> int:
@@ -613,20 +619,21 @@ def slope_rmsnorm_bwd(dY, H, rstd, gamma, dX=None, dgamma=None, workspace=None, 
     ways, added); dgamma (added to with accumulate).  workspace:
     slope_rmsnorm_bwd_workspace_bytes(T, K) bytes, needed with dgamma."""
     T, K = shape = _rows(dY, "dY")
-    dt = dY.dtype
+    dt, d = dY.dtype, dY.get_device()
     gdt = gamma.dtype if gamma is not None else dgamma.dtype if dgamma is not None else dt
-    wp, wb = _buffer(workspace, "workspace", dY)
-    _on_device("slope_rmsnorm_bwd", dY, stream, _dt(dt), _arg(dY, "dY", shape, dt, dY), _arg(H, "H", shape, dt, dY),
-               _arg(rstd, "rstd", (T,), torch.float32, dY), _dt(gdt), _opt(gamma, "gamma", (K,), gdt, dY),
-               _opt(dH, "dH", shape, dt, dY), T, K, _opt(dX, "dX", shape, dt, dY),
-               _opt(dgamma, "dgamma", (K,), gdt, dY), int(bool(accumulate)), wp, wb)
+    wp, wb = _buffer(workspace, "workspace", d)
+    _on_device("slope_rmsnorm_bwd", d, stream, _dt(dt), _arg(dY, "dY", shape, dt, d), _arg(H, "H", shape, dt, d),
+               _arg(rstd, "rstd", (T,), torch.float32, d), _dt(gdt), _opt(gamma, "gamma", (K,), gdt, d),
+               _opt(dH, "dH", shape, dt, d), T, K, _opt(dX, "dX", shape, dt, d),
+               _opt(dgamma, "dgamma", (K,), gdt, d), int(bool(accumulate)), wp, wb)
 
 
 def slope_quantize_rows_i8(X, q, scale, stream=None) -> None:
     """int8 codes q [T, K] and scales [T] of the rows of a bf16 or fp16 X [T, K]."""
     T, K = shape = _rows(X, "X")
-    _on_device("slope_quantize_rows_i8", X, stream, _dt(X), _arg(X, "X", shape, X.dtype, X), T, K,
-               _arg(q, "q", shape, torch.int8, X), _arg(scale, "scale", (T,), torch.float32, X))
+    d = X.get_device()
+    _on_device("slope_quantize_rows_i8", d, stream, _dt(X), _arg(X, "X", shape, X.dtype, d), T, K,
+               _arg(q, "q", shape, torch.int8, d), _arg(scale, "scale", (T,), torch.float32, d))
 
 
 def slope_packed_sparse_i8_bytes(rows: int, cols: int) -> int:
@@ -637,19 +644,21 @@ def slope_packed_sparse_i8_bytes(rows: int, cols: int) -> int:
 
 def slope_pack_sparse_i8(values, meta, rows, cols, w_scale, packed, stream=None) -> None:
     """int8 tile chunks of a compressed 16-bit matrix, with its rows' scales in w_scale [rows]."""
-    pp, pb = _buffer(packed, "packed", values)
-    _on_device("slope_pack_sparse_i8", values, stream, _dt(values),
-               _arg(values, "values", (rows, cols // 2), values.dtype, values),
-               _arg(meta, "meta", (rows, (cols // 4 + 7) // 8), torch.int32, values), rows, cols,
-               _arg(w_scale, "w_scale", (rows,), torch.float32, values), pp, pb)
+    d = values.get_device()
+    pp, pb = _buffer(packed, "packed", d)
+    _on_device("slope_pack_sparse_i8", d, stream, _dt(values),
+               _arg(values, "values", (rows, cols // 2), values.dtype, d),
+               _arg(meta, "meta", (rows, (cols // 4 + 7) // 8), torch.int32, d), rows, cols,
+               _arg(w_scale, "w_scale", (rows,), torch.float32, d), pp, pb)
 
 
 def _spmm_i8(fn, Xq, x_scale, packed_w, w_scale, N, Y, stream):
     T, K = shape = _rows(Xq, "Xq")
-    pp, pb = _buffer(packed_w, "packed_w", Xq)
-    _on_device(fn, Xq, stream, _dt(Y), _arg(Xq, "Xq", shape, torch.int8, Xq),
-               _arg(x_scale, "x_scale", (T,), torch.float32, Xq), T, K, pp, pb,
-               _arg(w_scale, "w_scale", (N,), torch.float32, Xq), N, _arg(Y, "Y", (T, N), Y.dtype, Xq))
+    d = Xq.get_device()
+    pp, pb = _buffer(packed_w, "packed_w", d)
+    _on_device(fn, d, stream, _dt(Y), _arg(Xq, "Xq", shape, torch.int8, d),
+               _arg(x_scale, "x_scale", (T,), torch.float32, d), T, K, pp, pb,
+               _arg(w_scale, "w_scale", (N,), torch.float32, d), N, _arg(Y, "Y", (T, N), Y.dtype, d))
 
 
 def slope_spmm_i8_packed(Xq, x_scale, packed_w, w_scale, N, Y, stream=None) -> None:

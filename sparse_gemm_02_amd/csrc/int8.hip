@@ -43,15 +43,15 @@ __global__ __launch_bounds__(256) void pack_i8_kernel(const In* __restrict__ val
   const int64_t half = K / 2, wpr = (K / 4 + 7) / 8;
   const In* v = vals + (live ? row : 0) * half;
   const uint32_t* m = meta + (live ? row : 0) * wpr;
-  float am = 0.f;
+  RowMax<false> am{};
   for (int64_t c = 8 * k; c < half; c += 64) {
     const Pack<In, 8> p = load_pack<In, 8>(v + c);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) am = max_of(am, finite_or_inf(elem_f32(p.v[e])));
+    for (int e = 0; e < 8; ++e) am.add(elem_f32(p.v[e]), 0.f);
   }
 #pragma unroll
-  for (int x = 4; x >= 1; x >>= 1) am = max_of(am, __shfl_xor(am, x));
-  const RowCodes<float> codes(am);
+  for (int x = 4; x >= 1; x >>= 1) am.join(am.other(x));
+  const RowCodes<false> codes(am);
   if (live && k == 0) scale[row] = codes.scale();
   for (int64_t s = 0; s < stages; ++s) {
     char* chunk = out + (tile * stages + s) * kChunkBytes;
@@ -59,9 +59,16 @@ __global__ __launch_bounds__(256) void pack_i8_kernel(const In* __restrict__ val
     const Pack<In, 8> p = load_pack<In, 8>(v + (c0 < half ? c0 : 0));
     const uint32_t mw = m[word < wpr ? word : 0];
     u32x2 o = {0u, 0u};
+    if (codes.tiny) {                                // (and rows of zeros)
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      o[e >> 2] |= ((uint32_t)codes.code(elem_f32(p.v[e])) & 0xFFu) << (8 * (e & 3));
+      for (int e = 0; e < 8; ++e) o[e >> 2] |= ((uint32_t)codes.code(elem_f32(p.v[e])) & 0xFFu) << (8 * (e & 3));
+    } else if (!codes.bad) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const float f[4] = {elem_f32(p.v[4 * w]), elem_f32(p.v[4 * w + 1]), elem_f32(p.v[4 * w + 2]), elem_f32(p.v[4 * w + 3])};
+        o[w] = codes.four(f, [&](int i) { return (double)f[i]; });
+      }
+    }
     const bool ok = live && c0 < half;               // K % 16 == 0: all eight inside or outside
     if (!ok) o = u32x2{0u, 0u};
     *reinterpret_cast<u32x2*>(chunk + r * 64 + (((k >> 1) ^ ((r >> 2) & 3)) << 4) + 8 * (k & 1)) = o;

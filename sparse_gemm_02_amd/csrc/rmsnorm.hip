@@ -33,46 +33,88 @@ __device__ __forceinline__ float wave_sum(float v) {
   for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
   return v;
 }
-template <typename U>
-__device__ __forceinline__ U wave_max(U v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = max_of(v, __shfl_xor(v, m));
-  return v;
-}
-
 // The vectors of a row of K >= E elements: vector i holds elements E i .. E i +
-// E - 1; the last one, when K is not a multiple of E, is moved back to end at
-// K, and its first `skip` elements belong to the vector before it.
-template <int E>
+// E - 1; the last one, when K is not a multiple of E (RAGGED), is moved back to
+// end at K, and its first `skip` elements belong to the vector before it.  A
+// vector past the row (skip == E) is read at element 0.
+template <int E, bool RAGGED>
 struct RowVec {
   int at, skip;
-  bool live;
   __device__ __forceinline__ RowVec(int i, int K) {
     const int full = E * i;
-    live = full < K;
-    const int last = K - E;
-    at = live ? (full < last ? full : last) : 0;
-    skip = live ? full - at : E;
+    const bool live = full < K;
+    if constexpr (RAGGED) {
+      const int last = K - E;
+      at = live ? (full < last ? full : last) : 0;
+      skip = live ? full - at : E;
+    } else {
+      at = live ? full : 0;
+      skip = live ? 0 : E;
+    }
   }
+  __device__ __forceinline__ bool mine(int e) const { return RAGGED ? e >= skip : skip == 0; }
 };
 
-template <typename V, int E>
-__device__ __forceinline__ void store_vec(V* row, const RowVec<E>& r, const Pack<V, E>& x) {
-  if (!r.live) return;
+template <typename V, int E, bool RAGGED>
+__device__ __forceinline__ void store_vec(V* row, const RowVec<E, RAGGED>& r, const Pack<V, E>& x) {
   if (r.skip == 0) {
     store_pack<V, E>(row + r.at, x);
-  } else {
+  } else if (RAGGED && r.skip < E) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
+    for (int e = 1; e < E; ++e)
       if (e >= r.skip) row[r.at + e] = x.v[e];
   }
 }
 
-// Products h g whose size sets the codes: exact in fp32 for a 16-bit g, in
-// double for an fp32 one.  (fp32 rows have no codes.)
+// Zeros in place of a vector's elements that are not its own, so that no sum or
+// maximum sees them.
+template <typename V, int E, bool RAGGED>
+__device__ __forceinline__ void drop_foreign(Pack<V, E>& x, const RowVec<E, RAGGED>& r) {
+  if (r.skip != 0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (!r.mine(e)) x.v[e] = elem_of<V>(0.f);
+  }
+}
+
+// The compiler takes x for a new value here: what was computed from it before is
+// not kept in registers for later but computed again.
+template <typename V, int E>
+__device__ __forceinline__ void forget(Pack<V, E>& x) {
+  struct Words {
+    uint32_t w[E * sizeof(V) / 4 > 0 ? E * sizeof(V) / 4 : 1];
+  };
+  if constexpr (E * sizeof(V) % 4 == 0) {
+    Words y = __builtin_bit_cast(Words, x);
+#pragma unroll
+    for (uint32_t& w : y.w) asm("" : "+v"(w));
+    x = __builtin_bit_cast(Pack<V, E>, y);
+  }
+}
+
+// gamma's type, or none (all ones)
+struct Ones {};
+template <typename GT> constexpr bool kHasGamma = !std::is_same<GT, Ones>::value;
+template <typename GT, int E>
+struct Gamma {
+  Pack<GT, E> g;
+  __device__ __forceinline__ void load(const GT* p) { g = load_pack<GT, E>(p); }
+  __device__ __forceinline__ float operator()(int e) const { return elem_f32(g.v[e]); }
+  template <bool RAGGED>
+  __device__ __forceinline__ void drop(const RowVec<E, RAGGED>& r) { drop_foreign<GT, E, RAGGED>(g, r); }
+};
+template <int E>
+struct Gamma<Ones, E> {
+  __device__ __forceinline__ void load(const Ones*) {}
+  __device__ __forceinline__ float operator()(int) const { return 1.f; }
+  template <bool RAGGED>
+  __device__ __forceinline__ void drop(const RowVec<E, RAGGED>&) {}
+};
+
+// An fp32 gamma against 16-bit rows: products that fp32 does not hold exactly.
+// (fp32 rows have no codes.)
 template <typename In, typename GT>
-using Prod = typename std::conditional<std::is_same<GT, float>::value && !std::is_same<In, float>::value, double,
-                                       float>::type;
+constexpr bool kWide = std::is_same<GT, float>::value && !std::is_same<In, float>::value;
 
 struct NormOut {
   void *H, *Y;
@@ -81,53 +123,64 @@ struct NormOut {
   bool norm;                                       // false: codes of x itself
 };
 
-// One row per block (WAVE: per wave, four rows a block), N vectors a thread.
-template <typename In, typename GT, int E, int N, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X, const In* res,
-                                                                    const GT* __restrict__ gamma, int64_t T, int K,
-                                                                    float eps, NormOut o) {
-  typedef Prod<In, GT> U;
+// One row per block (WAVE: per wave, four rows a block), N vectors a thread.  All
+// of the row's loads are issued before the first use: written as the formula
+// reads, with loads under `if (residual)`, the compiler waited for each vector
+// before it asked for the next (one row of 9216: 6.2 us against 4.0).
+template <typename In, typename GT, int E, int N, bool WAVE, bool RAGGED>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X, const In* res, const GT* gamma,
+                                                                    int64_t T, int K, float eps, NormOut o) {
+  typedef RowVec<E, RAGGED> Vec;
+  constexpr bool WIDE = kWide<In, GT>;
+  // gamma stays in registers between its two uses unless they would spill
+  constexpr bool KEEP = N < 8;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
   if (WAVE && row >= T) return;
   const int tid = WAVE ? lane : (int)threadIdx.x, tpr = WAVE ? 64 : (int)blockDim.x;
   const In* x = X + row * K;
-  Pack<In, E> h[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) h[j] = load_pack<In, E>(x + RowVec<E>(j * tpr + tid, K).at);
-  if (res) {
-    const In* rr = res + row * K;
-    Pack<In, E> r[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) r[j] = load_pack<In, E>(rr + RowVec<E>(j * tpr + tid, K).at);
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-#pragma unroll
-      for (int e = 0; e < E; ++e) h[j].v[e] = elem_of<In>(elem_f32(h[j].v[e]) + elem_f32(r[j].v[e]));
-  }
-  float ss = 0.f;
-  U am = 0;
+  const In* xr = res ? res + row * K : x;            // no residual: x again, and not used
+  Pack<In, E> h[N], r[N];
+  Gamma<GT, E> g[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const RowVec<E> rv(j * tpr + tid, K);
-    Pack<GT, E> g;
-    if (gamma) g = load_pack<GT, E>(gamma + rv.at);
+    const int at = Vec(j * tpr + tid, K).at;
+    h[j] = load_pack<In, E>(x + at);
+    r[j] = load_pack<In, E>(xr + at);
+    if (KEEP) g[j].load(gamma + at);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  float ss = 0.f;
+  RowMax<WIDE> am{};
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const Vec rv(j * tpr + tid, K);
+    if (res) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) h[j].v[e] = elem_of<In>(elem_f32(h[j].v[e]) + elem_f32(r[j].v[e]));
+    }
+    drop_foreign<In, E, RAGGED>(h[j], rv);
+    if (o.H) store_vec<In, E, RAGGED>((In*)o.H + row * K, rv, h[j]);
+    if (!KEEP) g[j].load(gamma + rv.at);
+    if (o.q) g[j].drop(rv);                          // its foreign elements need not be finite
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float f = e >= rv.skip ? elem_f32(h[j].v[e]) : 0.f;
+      const float f = elem_f32(h[j].v[e]);
       ss = __builtin_fmaf(f, f, ss);
       if (o.q) {
-        const U u = gamma ? (U)f * (U)elem_f32(g.v[e]) : (U)f;
-        am = max_of(am, e >= rv.skip ? finite_or_inf(u) : (U)0);
+        const float w = g[j](e), p = f * w;
+        am.add(p, WIDE ? __builtin_fmaf(f, w, -p) : 0.f);
       }
     }
-    if (o.H) store_vec<In, E>((In*)o.H + row * K, rv, h[j]);
   }
   ss = wave_sum(ss);
-  if (o.q) am = wave_max(am);
+  if (o.q) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) am.join(am.other(m));
+  }
   if constexpr (!WAVE) {
     __shared__ float sums[16];
-    __shared__ U maxs[16];
+    __shared__ RowMax<WIDE> maxs[16];
     if (lane == 0) {
       sums[wave] = ss;
       maxs[wave] = am;
@@ -137,11 +190,11 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
     am = maxs[0];
     for (int w = 1; w < tpr / 64; ++w) {
       ss += sums[w];
-      am = max_of(am, maxs[w]);
+      am.join(maxs[w]);
     }
   }
   const float rstd = o.norm ? 1.0f / sqrtf(ss / (float)K + eps) : 1.0f;
-  const RowCodes<U> codes(am);
+  const RowCodes<WIDE> codes(am);
   if (tid == 0) {
     if (o.rstd) o.rstd[row] = rstd;
     if (o.q) o.qs[row] = codes.scale() * rstd;
@@ -149,36 +202,65 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
   if (!o.Y && !o.q) return;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const RowVec<E> rv(j * tpr + tid, K);
-    Pack<GT, E> g;
-    if (gamma) g = load_pack<GT, E>(gamma + rv.at);
+    const Vec rv(j * tpr + tid, K);
+    forget<In, E>(h[j]);
+    if (!KEEP) g[j].load(gamma + rv.at);
     if (o.Y) {
       Pack<In, E> y;
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        y.v[e] = elem_of<In>(elem_f32(h[j].v[e]) * rstd * (gamma ? elem_f32(g.v[e]) : 1.f));
-      store_vec<In, E>((In*)o.Y + row * K, rv, y);
+      for (int e = 0; e < E; ++e) y.v[e] = elem_of<In>(elem_f32(h[j].v[e]) * rstd * g[j](e));
+      store_vec<In, E, RAGGED>((In*)o.Y + row * K, rv, y);
     }
-    if (o.q) {
+    if constexpr (!std::is_same<In, float>::value) {
+      if (!o.q) continue;
       Pack<int8_t, E> c;
+      auto exact = [&](int e) { return (double)elem_f32(h[j].v[e]) * (double)g[j](e); };
+      bool slow = true;
+      if constexpr (E % 4 == 0) {
+        slow = codes.bad || codes.tiny;
+        if (!slow) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const U f = (U)elem_f32(h[j].v[e]);
-        c.v[e] = (int8_t)codes.code(gamma ? f * (U)elem_f32(g.v[e]) : f);
+          for (int w = 0; w < E / 4; ++w) {
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = elem_f32(h[j].v[4 * w + i]) * g[j](4 * w + i);
+            const uint32_t b = codes.four(p, [&](int i) { return exact(4 * w + i); });
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c.v[4 * w + i] = (int8_t)(b >> (8 * i));
+          }
+        }
       }
-      store_vec<int8_t, E>(o.q + row * K, rv, c);
+      if (slow) {
+#pragma unroll 1
+        for (int e = 0; e < E; ++e) {
+          // (an indexed element would put the vectors in memory: pick it by compares)
+          double u = 0.0;
+#pragma unroll
+          for (int i = 0; i < E; ++i) u = i == e ? exact(i) : u;
+          const int8_t k = (int8_t)codes.code(u);
+#pragma unroll
+          for (int i = 0; i < E; ++i) c.v[i] = i == e ? k : c.v[i];
+        }
+      }
+      store_vec<int8_t, E, RAGGED>(o.q + row * K, rv, c);
     }
   }
+}
+
+template <typename GT>
+__device__ __forceinline__ float gamma_at(const GT* gamma, int64_t k) {
+  if constexpr (kHasGamma<GT>) return elem_f32(gamma[k]);
+  return 1.f;
 }
 
 // Rows too long for registers: two walks over the row.  The second reads h back
 // from H where it was written (X or the residual may be H itself).
 template <typename In, typename GT>
-__global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* res, const GT* __restrict__ gamma,
-                                                        int64_t K, float eps, NormOut o) {
-  typedef Prod<In, GT> U;
+__global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* res, const GT* gamma, int64_t K,
+                                                        float eps, NormOut o) {
+  constexpr bool WIDE = kWide<In, GT>;
   __shared__ float sums[16];
-  __shared__ U maxs[16];
+  __shared__ RowMax<WIDE> maxs[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = blockIdx.x, base = row * K;
   In* H = (In*)o.H;
@@ -186,16 +268,17 @@ __global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* r
     return res ? elem_of<In>(elem_f32(X[base + k]) + elem_f32(res[base + k])) : X[base + k];
   };
   float ss = 0.f;
-  U am = 0;
+  RowMax<WIDE> am{};
   for (int64_t k = threadIdx.x; k < K; k += 1024) {
     const In h = sum_at(k);
-    const float f = elem_f32(h);
+    const float f = elem_f32(h), w = gamma_at(gamma, k), p = f * w;
     ss = __builtin_fmaf(f, f, ss);
-    if (o.q) am = max_of(am, finite_or_inf(gamma ? (U)f * (U)elem_f32(gamma[k]) : (U)f));
+    am.add(p, WIDE ? __builtin_fmaf(f, w, -p) : 0.f);
     if (H) H[base + k] = h;
   }
   ss = wave_sum(ss);
-  am = wave_max(am);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) am.join(am.other(m));
   if (lane == 0) {
     sums[wave] = ss;
     maxs[wave] = am;
@@ -205,10 +288,10 @@ __global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* r
   am = maxs[0];
   for (int w = 1; w < 16; ++w) {
     ss += sums[w];
-    am = max_of(am, maxs[w]);
+    am.join(maxs[w]);
   }
   const float rstd = o.norm ? 1.0f / sqrtf(ss / (float)K + eps) : 1.0f;
-  const RowCodes<U> codes(am);
+  const RowCodes<WIDE> codes(am);
   if (threadIdx.x == 0) {
     if (o.rstd) o.rstd[row] = rstd;
     if (o.q) o.qs[row] = codes.scale() * rstd;
@@ -216,22 +299,19 @@ __global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* r
   if (!o.Y && !o.q) return;
   for (int64_t k = threadIdx.x; k < K; k += 1024) {   // each element by the thread that made it
     const float f = elem_f32(H ? H[base + k] : sum_at(k));
-    const float g = gamma ? elem_f32(gamma[k]) : 1.f;
-    if (o.q) o.q[base + k] = (int8_t)codes.code((U)f * (U)g);
+    const float g = gamma_at(gamma, k);
+    if (o.q) o.q[base + k] = (int8_t)codes.code((double)f * (double)g);
     if (o.Y) ((In*)o.Y)[base + k] = elem_of<In>(f * rstd * g);
   }
 }
 
-template <typename In, typename GT, int E, int N>
-void rms_block(const In* X, const In* res, const GT* gamma, int64_t T, int64_t K, float eps, const NormOut& o,
-               hipStream_t s) {
-  const int threads = (int)(cdiv(cdiv(cdiv(K, E), N), 64) * 64);
-  rms_row_kernel<In, GT, E, N, false><<<(unsigned)T, threads, 0, s>>>(X, res, gamma, T, (int)K, eps, o);
-}
-template <typename In, typename GT, int E, int N>
-void rms_wave(const In* X, const In* res, const GT* gamma, int64_t T, int64_t K, float eps, const NormOut& o,
+template <typename In, typename GT, int E, int N, bool WAVE>
+void rms_rows(const In* X, const In* res, const GT* gamma, int64_t T, int64_t K, float eps, const NormOut& o,
               hipStream_t s) {
-  rms_row_kernel<In, GT, E, N, true><<<(unsigned)cdiv(T, 4), 256, 0, s>>>(X, res, gamma, T, (int)K, eps, o);
+  const int threads = WAVE ? 256 : (int)(cdiv(cdiv(cdiv(K, E), N), 64) * 64);
+  const unsigned blocks = (unsigned)(WAVE ? cdiv(T, 4) : T);
+  if (K % E == 0) rms_row_kernel<In, GT, E, N, WAVE, false><<<blocks, threads, 0, s>>>(X, res, gamma, T, (int)K, eps, o);
+  else rms_row_kernel<In, GT, E, N, WAVE, true><<<blocks, threads, 0, s>>>(X, res, gamma, T, (int)K, eps, o);
 }
 
 template <typename In, typename GT>
@@ -241,23 +321,21 @@ hipError_t rms_launch(const void* X_, const void* res_, const void* gamma_, int6
   const In *X = (const In*)X_, *res = (const In*)res_;
   const GT* gamma = (const GT*)gamma_;
   const int64_t v = cdiv(K, E);
-  if (K < E) rms_wave<In, GT, 1, 1>(X, res, gamma, T, K, eps, o, s);
-  else if (v <= 64) rms_wave<In, GT, E, 1>(X, res, gamma, T, K, eps, o, s);
-  else if (v <= 128) rms_wave<In, GT, E, 2>(X, res, gamma, T, K, eps, o, s);
-  else if (v <= 256) rms_wave<In, GT, E, 4>(X, res, gamma, T, K, eps, o, s);
-  else if (v <= 512) rms_block<In, GT, E, 1>(X, res, gamma, T, K, eps, o, s);
-  else if (v <= 1024) rms_block<In, GT, E, 2>(X, res, gamma, T, K, eps, o, s);
-  else if (v <= 1536) rms_block<In, GT, E, 3>(X, res, gamma, T, K, eps, o, s);
-  else if (v <= 2048) rms_block<In, GT, E, 4>(X, res, gamma, T, K, eps, o, s);
-  else if (v <= 8192) rms_block<In, GT, E, 8>(X, res, gamma, T, K, eps, o, s);
+  if (K < E) rms_row_kernel<In, GT, 1, 1, true, false><<<(unsigned)cdiv(T, 4), 256, 0, s>>>(X, res, gamma, T, (int)K, eps, o);
+  else if (v <= 64) rms_rows<In, GT, E, 1, true>(X, res, gamma, T, K, eps, o, s);
+  else if (v <= 128) rms_rows<In, GT, E, 2, true>(X, res, gamma, T, K, eps, o, s);
+  else if (v <= 256) rms_rows<In, GT, E, 4, true>(X, res, gamma, T, K, eps, o, s);
+  else if (v <= 1024) rms_rows<In, GT, E, 2, false>(X, res, gamma, T, K, eps, o, s);
+  else if (v <= 3072) rms_rows<In, GT, E, 3, false>(X, res, gamma, T, K, eps, o, s);
+  else if (v <= 8192) rms_rows<In, GT, E, 8, false>(X, res, gamma, T, K, eps, o, s);
   else rms_long_kernel<In, GT><<<(unsigned)T, 1024, 0, s>>>(X, res, gamma, K, eps, o);
   return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- gradient
 
-constexpr int kBwdWaveBlocks = 512, kBwdBlocks = 768;   // partial rows of dgamma, at most
-constexpr int64_t kBwdMaxVecs = 4096;                   // vectors of a row kept in registers (512 threads x 8)
+constexpr int kBwdBlocks = 512;                         // partial rows of dgamma, at most
+constexpr int64_t kBwdMaxVecs = 4096;                   // vectors of a row kept in registers (1024 threads x 4)
 
 // Groups of tokens with a partial row of dgamma each, a function of the sizes
 // alone (the workspace's size); fewer for rows past 2^25 / kBwdBlocks columns,
@@ -268,88 +346,110 @@ int64_t bwd_groups(int64_t T, int64_t K) {
   return T < most ? T : most;
 }
 
-template <typename In, typename GT, int E, int N, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 512) void rms_bwd_kernel(const In* dY, const In* __restrict__ H,
-                                                                   const float* __restrict__ rstd,
-                                                                   const GT* __restrict__ gamma, const In* dH,
-                                                                   int64_t T, int K, In* dX, float* __restrict__ part) {
+// A block (WAVE: each of its four waves) takes every gridDim-th row and keeps its
+// columns, so dgamma's partial sums stay in registers.  The next row's loads are
+// issued before this row's sum is taken.
+template <typename In, typename GT, int E, int N, bool WAVE, bool RAGGED>
+__global__ __launch_bounds__(WAVE ? 256 : N == 4 ? 1024 : 512, N <= 2 || N == 4 ? 4 : 3) void rms_bwd_kernel(const In* dY, const In* __restrict__ H,
+                                                                   const float* __restrict__ rstd, const GT* gamma,
+                                                                   const In* dH, int64_t T, int K, In* dX,
+                                                                   float* __restrict__ part) {
+  typedef RowVec<E, RAGGED> Vec;
+  constexpr bool AHEAD = N < 4;                       // four vectors a thread: the registers hold one row, no gamma
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tid = WAVE ? lane : (int)threadIdx.x, tpr = WAVE ? 64 : (int)blockDim.x;
   const int64_t first = WAVE ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
   const int64_t step = WAVE ? (int64_t)gridDim.x * 4 : (int64_t)gridDim.x;
   const float inv_k = 1.0f / (float)K;
+  const In* dHr = dH ? dH : dY;                       // no dH: dY again, and not used
   float dg[N][E];
+  Gamma<GT, E> g[N];
 #pragma unroll
-  for (int j = 0; j < N; ++j)
+  for (int j = 0; j < N; ++j) {
+    if (AHEAD) g[j].load(gamma + Vec(j * tpr + tid, K).at);
 #pragma unroll
     for (int e = 0; e < E; ++e) dg[j][e] = 0.f;
-  __shared__ float sums[2][8];
-  int slot = 0;
-  for (int64_t row = first; row < T; row += step) {
-    const int64_t base = row * K;
+  }
+  struct Row {
     Pack<In, E> dy[N], h[N], r[N];
+    float rs;
+  };
+  auto load = [&](Row& w, int64_t row) {
+    const int64_t base = row * K;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const RowVec<E> rv(j * tpr + tid, K);
-      dy[j] = load_pack<In, E>(dY + base + rv.at);
-      h[j] = load_pack<In, E>(H + base + rv.at);
-      if (dH) r[j] = load_pack<In, E>(dH + base + rv.at);
+      const int at = Vec(j * tpr + tid, K).at;
+      w.dy[j] = load_pack<In, E>(dY + base + at);
+      w.h[j] = load_pack<In, E>(H + base + at);
+      w.r[j] = load_pack<In, E>(dHr + base + at);
     }
-    const float rs = rstd[row];
+    w.rs = rstd[row];
+  };
+  __shared__ float sums[2][16];
+  int slot = 0;
+  Row now, next;
+  if (first < T) load(now, first);
+  for (int64_t row = first; row < T; row += step) {
+    const int64_t base = row * K;
+    if (AHEAD) load(next, row + step < T ? row + step : row);
+    __builtin_amdgcn_sched_barrier(0);
+    const float rs = now.rs;
     float c = 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const RowVec<E> rv(j * tpr + tid, K);
-      Pack<GT, E> g;
-      if (gamma) g = load_pack<GT, E>(gamma + rv.at);
+      const Vec rv(j * tpr + tid, K);
+      if (!AHEAD) g[j].load(gamma + rv.at);
+      drop_foreign<In, E, RAGGED>(now.dy[j], rv);
+      drop_foreign<In, E, RAGGED>(now.h[j], rv);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float d = e >= rv.skip ? elem_f32(dy[j].v[e]) : 0.f;
-        const float xh = e >= rv.skip ? elem_f32(h[j].v[e]) * rs : 0.f;
-        const float p = d * xh;
+        const float p = elem_f32(now.dy[j].v[e]) * (elem_f32(now.h[j].v[e]) * rs);
         dg[j][e] += p;
-        c = __builtin_fmaf(p, gamma ? elem_f32(g.v[e]) : 1.f, c);
+        // (a foreign element's gamma need not be finite)
+        c = __builtin_fmaf(p, rv.mine(e) ? g[j](e) : 0.f, c);
       }
     }
-    if (!dX) continue;
-    c = wave_sum(c);
-    if constexpr (!WAVE) {
-      // two slots in turn: a row's sums are read before the slot is written again
-      if (lane == 0) sums[slot][wave] = c;
-      __syncthreads();
-      c = sums[slot][0];
-      for (int w = 1; w < tpr / 64; ++w) c += sums[slot][w];
-      slot ^= 1;
-    }
-    c *= inv_k;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const RowVec<E> rv(j * tpr + tid, K);
-      Pack<GT, E> g;
-      if (gamma) g = load_pack<GT, E>(gamma + rv.at);
-      Pack<In, E> out;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float a = elem_f32(dy[j].v[e]) * (gamma ? elem_f32(g.v[e]) : 1.f);
-        const float xh = elem_f32(h[j].v[e]) * rs;
-        float d = rs * (a - xh * c);
-        if (dH) d += elem_f32(r[j].v[e]);
-        out.v[e] = elem_of<In>(d);
+    if (dX) {
+      c = wave_sum(c);
+      if constexpr (!WAVE) {
+        // two slots in turn: a row's sums are read before the slot is written again
+        if (lane == 0) sums[slot][wave] = c;
+        __syncthreads();
+        c = sums[slot][0];
+        for (int w = 1; w < tpr / 64; ++w) c += sums[slot][w];
+        slot ^= 1;
       }
-      store_vec<In, E>(dX + base, rv, out);
+      c *= inv_k;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const Vec rv(j * tpr + tid, K);
+        if (!AHEAD) g[j].load(gamma + rv.at);
+        forget<In, E>(now.dy[j]);
+        forget<In, E>(now.h[j]);
+        Pack<In, E> out;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float a = elem_f32(now.dy[j].v[e]) * g[j](e), xh = elem_f32(now.h[j].v[e]) * rs;
+          const float d = rs * (a - xh * c);
+          out.v[e] = elem_of<In>(dH ? d + elem_f32(now.r[j].v[e]) : d);
+        }
+        store_vec<In, E, RAGGED>(dX + base, rv, out);
+      }
     }
+    if (AHEAD) now = next;
+    else if (row + step < T) load(now, row + step);
   }
   if (!part) return;
   float* dst = part + (int64_t)blockIdx.x * K;
+  auto put = [&](int j, const float (&v)[E]) {
+    const Vec rv(j * tpr + tid, K);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (rv.mine(e)) dst[rv.at + e] = v[e];
+  };
   if constexpr (!WAVE) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const RowVec<E> rv(j * tpr + tid, K);
-      if (!rv.live) continue;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (e >= rv.skip) dst[rv.at + e] = dg[j][e];
-    }
+    for (int j = 0; j < N; ++j) put(j, dg[j]);
   } else {
     // the four waves' sums, added in wave order
     __shared__ float all[N * E * 64];
@@ -360,20 +460,14 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void rms_bwd_kernel(const In* dY,
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const int at = (j * E + e) * 64 + lane;
-            all[at] = w == 0 ? dg[j][e] : all[at] + dg[j][e];
+            all[at] = dg[j][e] = w == 0 ? dg[j][e] : all[at] + dg[j][e];
           }
       }
       __syncthreads();
     }
-    if (wave == 0) {
+    if (wave == 3) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const RowVec<E> rv(j * 64 + lane, K);
-        if (!rv.live) continue;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (e >= rv.skip) dst[rv.at + e] = all[(j * E + e) * 64 + lane];
-      }
+      for (int j = 0; j < N; ++j) put(j, dg[j]);
     }
   }
 }
@@ -394,16 +488,15 @@ __global__ __launch_bounds__(256) void rms_dgamma_long_kernel(const In* __restri
 
 template <typename In, typename GT>
 __global__ __launch_bounds__(1024) void rms_dx_long_kernel(const In* dY, const In* __restrict__ H,
-                                                           const float* __restrict__ rstd,
-                                                           const GT* __restrict__ gamma, const In* dH, int64_t K,
-                                                           In* dX) {
+                                                           const float* __restrict__ rstd, const GT* gamma,
+                                                           const In* dH, int64_t K, In* dX) {
   __shared__ float sums[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = blockIdx.x, base = row * K;
   const float rs = rstd[row];
   float c = 0.f;
   for (int64_t k = threadIdx.x; k < K; k += 1024)
-    c += elem_f32(dY[base + k]) * (gamma ? elem_f32(gamma[k]) : 1.f) * (elem_f32(H[base + k]) * rs);
+    c += elem_f32(dY[base + k]) * gamma_at(gamma, k) * (elem_f32(H[base + k]) * rs);
   c = wave_sum(c);
   if (lane == 0) sums[wave] = c;
   __syncthreads();
@@ -411,7 +504,7 @@ __global__ __launch_bounds__(1024) void rms_dx_long_kernel(const In* dY, const I
   for (int w = 1; w < 16; ++w) c += sums[w];
   c /= (float)K;
   for (int64_t k = threadIdx.x; k < K; k += 1024) {
-    const float a = elem_f32(dY[base + k]) * (gamma ? elem_f32(gamma[k]) : 1.f);
+    const float a = elem_f32(dY[base + k]) * gamma_at(gamma, k);
     float d = rs * (a - elem_f32(H[base + k]) * rs * c);
     if (dH) d += elem_f32(dH[base + k]);
     dX[base + k] = elem_of<In>(d);
@@ -445,24 +538,22 @@ __global__ __launch_bounds__(1024) void rms_dgamma_reduce_kernel(const float* __
   }
 }
 
-template <typename In, typename GT, int E, int N>
-int64_t bwd_block(const In* dY, const In* H, const float* rstd, const GT* gamma, const In* dH, int64_t T, int64_t K,
-                  In* dX, float* part, hipStream_t s) {
-  const int threads = (int)(cdiv(cdiv(cdiv(K, E), N), 64) * 64);
-  const int64_t groups = bwd_groups(T, K);
-  rms_bwd_kernel<In, GT, E, N, false><<<(unsigned)groups, threads, 0, s>>>(dY, H, rstd, gamma, dH, T, (int)K, dX,
-                                                                            part);
-  return groups;
-}
-template <typename In, typename GT, int E, int N>
-int64_t bwd_wave(const In* dY, const In* H, const float* rstd, const GT* gamma, const In* dH, int64_t T, int64_t K,
+template <typename In, typename GT, int E, int N, bool WAVE>
+int64_t bwd_rows(const In* dY, const In* H, const float* rstd, const GT* gamma, const In* dH, int64_t T, int64_t K,
                  In* dX, float* part, hipStream_t s) {
-  const int64_t need = cdiv(T, 4), groups = need < kBwdWaveBlocks ? need : kBwdWaveBlocks;
-  rms_bwd_kernel<In, GT, E, N, true><<<(unsigned)groups, 256, 0, s>>>(dY, H, rstd, gamma, dH, T, (int)K, dX, part);
+  const int threads = WAVE ? 256 : (int)(cdiv(cdiv(cdiv(K, E), N), 64) * 64);
+  const int64_t groups = bwd_groups(WAVE ? cdiv(T, 4) : T, K);
+  if (K % E == 0)
+    rms_bwd_kernel<In, GT, E, N, WAVE, false><<<(unsigned)groups, threads, 0, s>>>(dY, H, rstd, gamma, dH, T, (int)K,
+                                                                                   dX, part);
+  else
+    rms_bwd_kernel<In, GT, E, N, WAVE, true><<<(unsigned)groups, threads, 0, s>>>(dY, H, rstd, gamma, dH, T, (int)K,
+                                                                                  dX, part);
   return groups;
 }
 
-template <typename In, typename GT>
+// DG: dgamma's type (gamma's, which may not be there)
+template <typename In, typename GT, typename DG>
 hipError_t bwd_launch(const void* dY_, const void* H_, const float* rstd, const void* gamma_, const void* dH_,
                       int64_t T, int64_t K, void* dX_, void* dgamma, int accumulate, float* part, hipStream_t s) {
   constexpr int E = vec_elems<In>();
@@ -473,14 +564,15 @@ hipError_t bwd_launch(const void* dY_, const void* H_, const float* rstd, const 
   int64_t groups = 0;
   const int64_t v = cdiv(K, E);
   if (T == 0) {
-  } else if (K < E) groups = bwd_wave<In, GT, 1, 1>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
-  else if (v <= 64) groups = bwd_wave<In, GT, E, 1>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
-  else if (v <= 128) groups = bwd_wave<In, GT, E, 2>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
-  else if (v <= 256) groups = bwd_block<In, GT, E, 1>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
-  else if (v <= 768) groups = bwd_block<In, GT, E, 2>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
-  else if (v <= 1536) groups = bwd_block<In, GT, E, 3>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
-  else if (v <= 2048) groups = bwd_block<In, GT, E, 4>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
-  else if (v <= kBwdMaxVecs) groups = bwd_block<In, GT, E, 8>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
+  } else if (K < E) {
+    groups = bwd_groups(cdiv(T, 4), K);
+    rms_bwd_kernel<In, GT, 1, 1, true, false><<<(unsigned)groups, 256, 0, s>>>(dY, H, rstd, gamma, dH, T, (int)K,
+                                                                                     dX, part);
+  } else if (v <= 64) groups = bwd_rows<In, GT, E, 1, true>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
+  else if (v <= 128) groups = bwd_rows<In, GT, E, 2, true>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
+  else if (v <= 512) groups = bwd_rows<In, GT, E, 1, false>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
+  else if (v <= 1536) groups = bwd_rows<In, GT, E, 3, false>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
+  else if (v <= kBwdMaxVecs) groups = bwd_rows<In, GT, E, 4, false>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
   else {
     groups = bwd_groups(T, K);
     if (dgamma)
@@ -490,8 +582,26 @@ hipError_t bwd_launch(const void* dY_, const void* H_, const float* rstd, const 
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dgamma) return e;
-  rms_dgamma_reduce_kernel<GT><<<(unsigned)cdiv(K, 64), 1024, 0, s>>>(part, (int)groups, K, accumulate, (GT*)dgamma);
+  rms_dgamma_reduce_kernel<DG><<<(unsigned)cdiv(K, 64), 1024, 0, s>>>(part, (int)groups, K, accumulate, (DG*)dgamma);
   return hipGetLastError();
+}
+
+template <typename In>
+hipError_t rms_any(const void* X, const void* res, bool wide, const void* gamma, int64_t T, int64_t K, float eps,
+                   const NormOut& o, hipStream_t s) {
+  if (!gamma) return rms_launch<In, Ones>(X, res, gamma, T, K, eps, o, s);
+  return wide ? rms_launch<In, float>(X, res, gamma, T, K, eps, o, s)
+              : rms_launch<In, In>(X, res, gamma, T, K, eps, o, s);
+}
+
+template <typename In>
+hipError_t bwd_any(const void* dY, const void* H, const float* rstd, bool wide, const void* gamma, const void* dH,
+                   int64_t T, int64_t K, void* dX, void* dgamma, int accumulate, float* part, hipStream_t s) {
+  if (!gamma)
+    return wide ? bwd_launch<In, Ones, float>(dY, H, rstd, gamma, dH, T, K, dX, dgamma, accumulate, part, s)
+                : bwd_launch<In, Ones, In>(dY, H, rstd, gamma, dH, T, K, dX, dgamma, accumulate, part, s);
+  return wide ? bwd_launch<In, float, float>(dY, H, rstd, gamma, dH, T, K, dX, dgamma, accumulate, part, s)
+              : bwd_launch<In, In, In>(dY, H, rstd, gamma, dH, T, K, dX, dgamma, accumulate, part, s);
 }
 
 }  // namespace
@@ -500,21 +610,18 @@ hipError_t launch_rmsnorm(Dt dt, const void* X, const void* res, Dt gamma_dt, co
                           float eps, void* H, void* Y, int8_t* q, float* qs, float* rstd, hipStream_t s) {
   if (T == 0 || K == 0) return hipSuccess;
   const NormOut o{H, Y, q, qs, rstd, true};
-  const bool wide = gamma && gamma_dt == Dt::F32;
-  if (dt == Dt::F32) return rms_launch<float, float>(X, res, gamma, T, K, eps, o, s);
-  if (dt == Dt::F16)
-    return wide ? rms_launch<_Float16, float>(X, res, gamma, T, K, eps, o, s)
-                : rms_launch<_Float16, _Float16>(X, res, gamma, T, K, eps, o, s);
-  return wide ? rms_launch<uint16_t, float>(X, res, gamma, T, K, eps, o, s)
-              : rms_launch<uint16_t, uint16_t>(X, res, gamma, T, K, eps, o, s);
+  const bool wide = gamma_dt == Dt::F32;
+  if (dt == Dt::F32) return rms_any<float>(X, res, wide, gamma, T, K, eps, o, s);
+  if (dt == Dt::F16) return rms_any<_Float16>(X, res, wide, gamma, T, K, eps, o, s);
+  return rms_any<uint16_t>(X, res, wide, gamma, T, K, eps, o, s);
 }
 
 hipError_t launch_quantize_rows_i8(Dt dt, const void* X, int64_t T, int64_t K, int8_t* q, float* scale,
                                    hipStream_t s) {
   if (T == 0 || K == 0) return hipSuccess;
   const NormOut o{nullptr, nullptr, q, scale, nullptr, false};
-  return dt == Dt::F16 ? rms_launch<_Float16, _Float16>(X, nullptr, nullptr, T, K, 0.f, o, s)
-                       : rms_launch<uint16_t, uint16_t>(X, nullptr, nullptr, T, K, 0.f, o, s);
+  return dt == Dt::F16 ? rms_any<_Float16>(X, nullptr, false, nullptr, T, K, 0.f, o, s)
+                       : rms_any<uint16_t>(X, nullptr, false, nullptr, T, K, 0.f, o, s);
 }
 
 int64_t rmsnorm_bwd_workspace_bytes(int64_t T, int64_t K) { return bwd_groups(T, K) * K * 4; }
@@ -525,12 +632,9 @@ hipError_t launch_rmsnorm_bwd(Dt dt, const void* dY, const void* H, const float*
   if (K == 0) return hipSuccess;
   float* part = (float*)workspace;
   const bool wide = gamma_dt == Dt::F32;          // dgamma's type too, so also without a gamma
-  if (dt == Dt::F32) return bwd_launch<float, float>(dY, H, rstd, gamma, dH, T, K, dX, dgamma, accumulate, part, s);
-  if (dt == Dt::F16)
-    return wide ? bwd_launch<_Float16, float>(dY, H, rstd, gamma, dH, T, K, dX, dgamma, accumulate, part, s)
-                : bwd_launch<_Float16, _Float16>(dY, H, rstd, gamma, dH, T, K, dX, dgamma, accumulate, part, s);
-  return wide ? bwd_launch<uint16_t, float>(dY, H, rstd, gamma, dH, T, K, dX, dgamma, accumulate, part, s)
-              : bwd_launch<uint16_t, uint16_t>(dY, H, rstd, gamma, dH, T, K, dX, dgamma, accumulate, part, s);
+  if (dt == Dt::F32) return bwd_any<float>(dY, H, rstd, wide, gamma, dH, T, K, dX, dgamma, accumulate, part, s);
+  if (dt == Dt::F16) return bwd_any<_Float16>(dY, H, rstd, wide, gamma, dH, T, K, dX, dgamma, accumulate, part, s);
+  return bwd_any<uint16_t>(dY, H, rstd, wide, gamma, dH, T, K, dX, dgamma, accumulate, part, s);
 }
 
 }  // namespace slope

@@ -30,67 +30,108 @@ template <> __device__ __forceinline__ uint16_t elem_of<uint16_t>(float f) { ret
 template <> __device__ __forceinline__ _Float16 elem_of<_Float16>(float f) { return (_Float16)f; }
 template <> __device__ __forceinline__ float elem_of<float>(float f) { return f; }
 
-// |u| for a row's maximum, with NaN taken as infinity (fmax would drop it).
-__device__ __forceinline__ float finite_or_inf(float u) {
-  const float a = __builtin_fabsf(u);
-  return a < __builtin_inff() ? a : __builtin_inff();
-}
-__device__ __forceinline__ double finite_or_inf(double u) {
-  const double a = __builtin_fabs(u);
-  return a < __builtin_inf() ? a : __builtin_inf();
-}
-__device__ __forceinline__ float max_of(float a, float b) { return a > b ? a : b; }
-__device__ __forceinline__ double max_of(double a, double b) { return a > b ? a : b; }
+// ---------------------------------------------------------------- codes of a row
+// code = the integer nearest to 127 u / amax, ties to even; amax = max |u| of the
+// row, u = h g the exact product of two stored values.  u travels as an fp32
+// pair: p = fp32(h g) and what the rounding left, e = h g - p (zero where g has
+// 16 bits too: the product then fits).
 
-// Codes of a row whose largest |u| is `amax` (U = float where every u is exact
-// in fp32, double where a 16-bit value meets an fp32 gamma).
-//
-// code = the integer nearest to 127 u / amax, ties to even.  The quotient comes
-// from one fp32 reciprocal and is within 2^-16 of the true one (|q| <= 127: two
-// roundings of 2^-24 each), so its rounding is decided unless it lies within
-// 1e-4 of a border k + 1/2; there the sign of 254 u - (2k + 1) amax decides,
-// which is exact in double (at most 43 significant bits in either product).
-// About one value in 5000 takes that branch.
-template <typename U> struct RowCodes;
-
-__device__ __forceinline__ float border_code(double u, double amax, float q, float k) {
-  const double twice = 2.0 * (double)k + (q > k ? 1.0 : -1.0);   // twice the border next to q
-  const double d = 254.0 * u - twice * amax;
-  const int lo = (int)(0.5 * (twice - 1.0));                     // the codes on its two sides: lo, lo + 1
-  return (float)(d > 0.0 ? lo + 1 : d < 0.0 ? lo : lo + (lo & 1));
-}
-
-template <> struct RowCodes<float> {
-  float amax, lift, inv;
-  bool bad;
-  __device__ __forceinline__ explicit RowCodes(float a) : amax(a) {
-    bad = !(a < __builtin_inff());
-    // a power of two that keeps the reciprocal of a tiny amax finite
-    lift = a < 0x1p-60f ? 0x1p60f : 1.0f;
-    inv = (a > 0.0f && !bad) ? 127.0f / (a * lift) : 0.0f;
+// Largest |u| of the values seen so far: the bits of its p, and its e with p's
+// sign taken off.  Magnitude bits order like magnitudes, with infinity and NaN on
+// top, so a row without a finite maximum shows in `hi`.
+template <bool WIDE> struct RowMax;
+template <> struct RowMax<false> {
+  uint32_t hi;                                       // start from {} (zero)
+  __device__ __forceinline__ void add(float p, float) {
+    const uint32_t b = __float_as_uint(p) & 0x7FFFFFFFu;
+    hi = b > hi ? b : hi;
   }
-  __device__ __forceinline__ float scale() const { return bad ? __builtin_nanf("") : amax / 127.0f; }
-  __device__ __forceinline__ int code(float u) const {
-    const float q = (u * lift) * inv;
-    float k = __builtin_rintf(q);
-    if (__builtin_fabsf(q - k) > 0.4999f) k = border_code((double)u, (double)amax, q, k);
-    return bad ? 0 : (int)k;
+  __device__ __forceinline__ void join(const RowMax& o) { hi = o.hi > hi ? o.hi : hi; }
+  __device__ __forceinline__ RowMax other(int mask) const {
+    RowMax o;
+    o.hi = (uint32_t)__shfl_xor((int)hi, mask);
+    return o;
   }
+  __device__ __forceinline__ double exact() const { return (double)__uint_as_float(hi); }
+};
+template <> struct RowMax<true> {
+  uint32_t hi;                                       // start from {} (zero)
+  float lo;
+  __device__ __forceinline__ void take(uint32_t b, float r) {
+    const bool up = b > hi || (b == hi && r > lo);
+    hi = up ? b : hi;
+    lo = up ? r : lo;
+  }
+  __device__ __forceinline__ void add(float p, float e) {
+    const uint32_t b = __float_as_uint(p);
+    take(b & 0x7FFFFFFFu, __uint_as_float(__float_as_uint(e) ^ (b & 0x80000000u)));
+  }
+  __device__ __forceinline__ void join(const RowMax& o) { take(o.hi, o.lo); }
+  __device__ __forceinline__ RowMax other(int mask) const {
+    RowMax o;
+    o.hi = (uint32_t)__shfl_xor((int)hi, mask);
+    o.lo = __shfl_xor(lo, mask);
+    return o;
+  }
+  __device__ __forceinline__ double exact() const { return (double)__uint_as_float(hi) + (double)lo; }
 };
 
-template <> struct RowCodes<double> {
-  double amax, inv;
-  bool bad;
-  __device__ __forceinline__ explicit RowCodes(double a) : amax(a) {
-    bad = !(a < __builtin_inf());
-    inv = (a > 0.0 && !bad) ? 127.0 / a : 0.0;
+constexpr float kCodeMagic = 12582912.0f;             // 1.5 * 2^23: adding it rounds to an integer, ties to even
+
+// The quotient from one fp32 reciprocal, q = p * (127 / hi), is within 2^-14 of
+// the true one (|q| <= 127; p, hi, the division and the product each round by
+// 2^-24 at most), so its rounding is decided unless it lies within 1e-4 of a
+// border k + 1/2.  There the sign of 254 u - (2k + 1) amax decides, which is
+// exact in double (products of at most 43 bits).  About one value in 5000 takes
+// that branch.  Rows whose amax is below 2^-100, where products leave fp32's
+// normal range, go by double throughout.
+template <bool WIDE>
+struct RowCodes {
+  RowMax<WIDE> top;
+  float inv;
+  bool bad, tiny;
+  __device__ __forceinline__ explicit RowCodes(const RowMax<WIDE>& m) : top(m) {
+    bad = m.hi >= 0x7F800000u;
+    tiny = m.hi < 0x0D800000u;                       // 2^-100
+    inv = bad || tiny ? 0.f : 127.0f / __uint_as_float(m.hi);
   }
-  __device__ __forceinline__ float scale() const { return bad ? __builtin_nanf("") : (float)amax / 127.0f; }
+  __device__ __forceinline__ float scale() const {
+    return bad ? __builtin_nanf("") : __uint_as_float(top.hi) / 127.0f;
+  }
+  // the code beside the border next to q (k = q rounded)
+  __device__ __forceinline__ float at_border(double u, float q, float k) const {
+    const double twice = 2.0 * (double)k + (q > k ? 1.0 : -1.0), d = 254.0 * u - twice * top.exact();
+    const int lo = (int)(0.5 * (twice - 1.0));        // the codes on its two sides: lo, lo + 1
+    return (float)(d > 0.0 ? lo + 1 : d < 0.0 ? lo : lo + (lo & 1));
+  }
+  // one value, any row
   __device__ __forceinline__ int code(double u) const {
-    const float q = (float)(u * inv);
-    float k = __builtin_rintf(q);
-    if (__builtin_fabsf(q - k) > 0.4999f) k = border_code(u, amax, q, k);
-    return bad ? 0 : (int)k;
+    if (bad || top.hi == 0u) return 0;
+    const double q = 127.0 * u / top.exact();
+    const float k = (float)__builtin_rint(q);
+    return (int)(__builtin_fabs(q - k) > 0.4999 ? at_border(u, (float)q, k) : k);
+  }
+  // The four codes of p[0..3], one a byte (an ordinary row).  u(i) gives the exact
+  // product of value i.
+  template <typename F>
+  __device__ __forceinline__ uint32_t four(const float (&p)[4], F&& u) const {
+    float t[4], far = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float q = p[i] * inv;
+      t[i] = q + kCodeMagic;
+      far = __builtin_fmaxf(far, __builtin_fabsf(q - (t[i] - kCodeMagic)));
+    }
+    if (far > 0.4999f) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float q = p[i] * inv, k = t[i] - kCodeMagic;
+        if (__builtin_fabsf(q - k) > 0.4999f) t[i] = at_border(u(i), q, k) + kCodeMagic;
+      }
+    }
+    // the low bytes of t are the codes in two's complement
+    return __builtin_amdgcn_perm(__float_as_uint(t[1]), __float_as_uint(t[0]), 0x0C0C0400u) |
+           __builtin_amdgcn_perm(__float_as_uint(t[3]), __float_as_uint(t[2]), 0x04000C0Cu);
   }
 };
 
