@@ -350,7 +350,7 @@ int64_t bwd_groups(int64_t T, int64_t K) {
 // columns, so dgamma's partial sums stay in registers.  The next row's loads are
 // issued before this row's sum is taken.
 template <typename In, typename GT, int E, int N, bool WAVE, bool RAGGED>
-__global__ __launch_bounds__(WAVE ? 256 : N == 4 ? 1024 : 512, N <= 2 || N == 4 ? 4 : 3) void rms_bwd_kernel(const In* dY, const In* __restrict__ H,
+__global__ __launch_bounds__(WAVE ? 256 : N == 4 ? 1024 : 512, N == 4 ? 4 : 2) void rms_bwd_kernel(const In* dY, const In* __restrict__ H,
                                                                    const float* __restrict__ rstd, const GT* gamma,
                                                                    const In* dH, int64_t T, int K, In* dX,
                                                                    float* __restrict__ part) {
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(WAVE ? 256 : N == 4 ? 1024 : 512, N <= 2 || N == 4 
       const int at = Vec(j * tpr + tid, K).at;
       w.dy[j] = load_pack<In, E>(dY + base + at);
       w.h[j] = load_pack<In, E>(H + base + at);
-      w.r[j] = load_pack<In, E>(dHr + base + at);
+      if (AHEAD) w.r[j] = load_pack<In, E>(dHr + base + at);
     }
     w.rs = rstd[row];
   };
@@ -423,7 +423,10 @@ __global__ __launch_bounds__(WAVE ? 256 : N == 4 ? 1024 : 512, N <= 2 || N == 4 
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const Vec rv(j * tpr + tid, K);
-        if (!AHEAD) g[j].load(gamma + rv.at);
+        if (!AHEAD) {
+          now.r[j] = load_pack<In, E>(dHr + base + rv.at);
+          g[j].load(gamma + rv.at);
+        }
         forget<In, E>(now.dy[j]);
         forget<In, E>(now.h[j]);
         Pack<In, E> out;
@@ -511,29 +514,30 @@ __global__ __launch_bounds__(1024) void rms_dx_long_kernel(const In* dY, const I
   }
 }
 
-// dgamma[k] = sum over the groups, in a fixed order: 16 waves take a sixteenth
-// of the rows each for the block's 64 columns, and the 16 sums are added in
-// wave order.
+// dgamma[k] = sum over the groups, in a fixed order: 32 columns a block, 32 threads
+// a column with a thirty-second of the rows each (sixteen loads in flight), their
+// sums added in order.
 template <typename GT>
 __global__ __launch_bounds__(1024) void rms_dgamma_reduce_kernel(const float* __restrict__ part, int groups,
                                                                  int64_t K, int accumulate, GT* __restrict__ out) {
-  __shared__ float sums[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t k = (int64_t)blockIdx.x * 64 + lane, kc = k < K ? k : K - 1;
-  const int per = (groups + 15) / 16, g0 = wave * per, g1 = g0 + per < groups ? g0 + per : groups;
+  __shared__ float sums[32][33];
+  const int c = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t k = (int64_t)blockIdx.x * 32 + c, kc = k < K ? k : K - 1;
+  const int per = (groups + 31) / 32, g0 = y * per, g1 = g0 + per < groups ? g0 + per : groups;
   float s = 0.f;
-  for (int g = g0; g < g1; g += 8) {
-    float v[8];
+  for (int g = g0; g < g1; g += 16) {
+    float v[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = part[(int64_t)(g + i < g1 ? g + i : g) * K + kc];
+    for (int i = 0; i < 16; ++i) v[i] = part[(int64_t)(g + i < g1 ? g + i : g) * K + kc];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += g + i < g1 ? v[i] : 0.f;
+    for (int i = 0; i < 16; ++i) s += g + i < g1 ? v[i] : 0.f;
   }
-  sums[wave][lane] = s;
+  sums[y][c] = s;
   __syncthreads();
-  if (wave == 0 && k < K) {
+  if (y == 0 && k < K) {
     float d = accumulate ? elem_f32(out[k]) : 0.f;
-    for (int w = 0; w < 16; ++w) d += sums[w][lane];
+#pragma unroll
+    for (int w = 0; w < 32; ++w) d += sums[w][c];
     out[k] = elem_of<GT>(d);
   }
 }
@@ -542,7 +546,11 @@ template <typename In, typename GT, int E, int N, bool WAVE>
 int64_t bwd_rows(const In* dY, const In* H, const float* rstd, const GT* gamma, const In* dH, int64_t T, int64_t K,
                  In* dX, float* part, hipStream_t s) {
   const int threads = WAVE ? 256 : (int)(cdiv(cdiv(cdiv(K, E), N), 64) * 64);
-  const int64_t groups = bwd_groups(WAVE ? cdiv(T, 4) : T, K);
+  // a block of three or four vectors a thread leaves no room for a second one on
+  // its compute unit: one round of 256 blocks (8192 x 9216: 120.5 us against 128.9
+  // with 512).  Narrower rows take 512 (4096 x 2304: 20.4 us against 25.5).
+  int64_t groups = bwd_groups(WAVE ? cdiv(T, 4) : T, K);
+  if (N >= 3 && groups > 256) groups = 256;
   if (K % E == 0)
     rms_bwd_kernel<In, GT, E, N, WAVE, false><<<(unsigned)groups, threads, 0, s>>>(dY, H, rstd, gamma, dH, T, (int)K,
                                                                                    dX, part);
@@ -582,7 +590,7 @@ hipError_t bwd_launch(const void* dY_, const void* H_, const float* rstd, const 
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dgamma) return e;
-  rms_dgamma_reduce_kernel<DG><<<(unsigned)cdiv(K, 64), 1024, 0, s>>>(part, (int)groups, K, accumulate, (DG*)dgamma);
+  rms_dgamma_reduce_kernel<DG><<<(unsigned)cdiv(K, 32), 1024, 0, s>>>(part, (int)groups, K, accumulate, (DG*)dgamma);
   return hipGetLastError();
 }
 
