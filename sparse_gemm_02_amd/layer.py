@@ -1,6 +1,7 @@
-"""Training-side wrappers over the C ABI: a 2:4 sparse linear layer with an
-optional low-rank adapter, its autograd function, and AdamW on its compressed
-values.
+"""Module wrappers over the C ABI: a 2:4 sparse linear layer with an optional
+low-rank adapter, its autograd function, AdamW on its compressed values; the
+RMS norm with the residual's addition, its autograd function; and the linear
+layer on 8-bit integer codes, for inference.
 
 Orchestration only: every arithmetic step runs in libslope.so through the
 binding in this package (the forward product with the fused adapter term, the
@@ -26,15 +27,19 @@ and N multiples of 16 (the packed operand format).
 """
 from __future__ import annotations
 
+from typing import NamedTuple
+
 import torch
 
-from . import (slope_adamw, slope_adamw_double_prune_packed, slope_double_prune_packed, slope_lowrank_grads_packed,
-               slope_lowrank_grads_workspace_bytes, slope_lowrank_workspace_bytes, slope_masked_wgrad_packed,
-               slope_pack_sparse, slope_pack_tokens, slope_packed_sparse_bytes, slope_packed_tokens_bytes,
-               slope_prune_compress24, slope_spmm_bwd_dx_packed, slope_spmm_bwd_dx_packed_tokens,
-               slope_spmm_fwd_packed, slope_wgrad_split_workspace_bytes)
+from . import (I8_DECODE_MAX_TOKENS, slope_adamw, slope_adamw_double_prune_packed, slope_double_prune_packed,
+               slope_lowrank_add, slope_lowrank_grads_packed, slope_lowrank_grads_workspace_bytes,
+               slope_lowrank_workspace_bytes, slope_masked_wgrad_packed, slope_pack_sparse, slope_pack_sparse_i8,
+               slope_pack_tokens, slope_packed_sparse_bytes, slope_packed_sparse_i8_bytes, slope_packed_tokens_bytes,
+               slope_prune_compress24, slope_quantize_rows_i8, slope_rmsnorm, slope_rmsnorm_bwd,
+               slope_rmsnorm_bwd_workspace_bytes, slope_spmm_bwd_dx_packed, slope_spmm_bwd_dx_packed_tokens,
+               slope_spmm_fwd_packed, slope_spmm_i8_decode, slope_spmm_i8_packed, slope_wgrad_split_workspace_bytes)
 
-__all__ = ["SparseLinear", "SparseAdamW", "training_state_bytes"]
+__all__ = ["SparseLinear", "SparseAdamW", "training_state_bytes", "ResidualRMSNorm", "Int8Rows", "Int8SparseLinear"]
 
 
 def _bytes(n, device):
@@ -236,3 +241,147 @@ def training_state_bytes(layer: SparseLinear, optimizer: SparseAdamW | None = No
     packed = canonical + nb(layer.packed_s)
     return {"canonical": canonical, "with_packed_operands": packed, "dense_adamw": dense,
             "canonical_ratio": canonical / dense, "with_packed_ratio": packed / dense}
+
+
+class Int8Rows(NamedTuple):
+    """Activations as 8-bit integer codes: q [..., K] int8 and one float32 scale
+    for each row of K, scale [...]; the values are q * scale."""
+    q: torch.Tensor
+    scale: torch.Tensor
+
+
+class _ResidualRMSNormFn(torch.autograd.Function):
+    """(y, h) of x and residual [..., K]; without a residual h is x itself and y
+    alone is returned.  The rows are flattened in here: with reshapes outside, the
+    one gradient of x and residual would reach the two leaves as two views of one
+    tensor, and accumulating into one .grad would change the other."""
+
+    @staticmethod
+    def forward(ctx, x, residual, gamma, eps):
+        K = x.shape[-1]
+        rows = lambda t: t.reshape(-1, K).contiguous()
+        x2 = rows(x)
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        rstd = torch.empty(x2.shape[0], dtype=torch.float32, device=x.device)
+        if residual is None:
+            h, h2 = None, x2
+            slope_rmsnorm(x2, gamma, eps, Y=y.view(x2.shape), rstd=rstd)
+        else:
+            h = torch.empty_like(y)
+            h2 = h.view(x2.shape)
+            slope_rmsnorm(x2, gamma, eps, residual=rows(residual), H=h2, Y=y.view(x2.shape), rstd=rstd)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(h2 if h is None else h, rstd, gamma)
+        return y if h is None else (y, h)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, rstd, gamma = ctx.saved_tensors
+        need_x, need_r, need_g = ctx.needs_input_grad[:3]
+        if dy is None:                               # only h was used
+            return dh if need_x else None, dh if need_r else None, None, None
+        rows = lambda t: t.reshape(-1, gamma.shape[0]).contiguous()
+        dx = dgamma = ws = None
+        if need_x or need_r:
+            dx = torch.empty(dy.shape, dtype=h.dtype, device=h.device)
+        if need_g:
+            dgamma = torch.empty_like(gamma)
+            ws = _bytes(slope_rmsnorm_bwd_workspace_bytes(rstd.shape[0], gamma.shape[0]), h.device)
+        if dx is not None or need_g:
+            slope_rmsnorm_bwd(rows(dy), rows(h), rstd, gamma, dX=None if dx is None else dx.view(-1, gamma.shape[0]),
+                              dgamma=dgamma, workspace=ws, dH=None if dh is None or dx is None else rows(dh))
+        return dx if need_x else None, dx if need_r else None, dgamma, None
+
+
+class ResidualRMSNorm(torch.nn.Module):
+    """Root-mean-square norm over the last dimension with the residual's addition:
+
+        h = x + residual,   y = h / sqrt(mean(h^2) + eps) * weight
+
+    for bf16, fp16 or fp32 x; weight in x's format or fp32.  `norm(x)` returns y,
+    `norm(x, residual)` returns (y, h); both are differentiable in x, residual and
+    weight.  `norm.codes(...)` (inference) returns y as 8-bit integer codes with a
+    scale for each row, the input of Int8SparseLinear."""
+
+    def __init__(self, features: int, eps: float = 1e-5, dtype=torch.float32, device="cuda"):
+        super().__init__()
+        self.features, self.eps = features, eps
+        self.weight = torch.nn.Parameter(torch.ones(features, dtype=dtype, device=device))
+
+    def _check(self, x, residual):
+        if x.shape[-1] != self.features:
+            raise ValueError(f"input must have {self.features} columns")
+        if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+            raise ValueError("residual must have the input's shape and format")
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
+        self._check(x, residual)
+        return _ResidualRMSNormFn.apply(x, residual, self.weight, self.eps)
+
+    @torch.no_grad()
+    def codes(self, x: torch.Tensor, residual: torch.Tensor | None = None, output: bool = False):
+        """(codes, h), or (codes, h, y) with output=True, in one pass over x; h is
+        x itself without a residual.  bf16 or fp16 x."""
+        self._check(x, residual)
+        x2 = x.reshape(-1, self.features).contiguous()
+        r2 = None if residual is None else residual.reshape(-1, self.features).contiguous()
+        q = torch.empty(x2.shape, dtype=torch.int8, device=x.device)
+        scale = torch.empty(x2.shape[0], dtype=torch.float32, device=x.device)
+        h = x2 if r2 is None else torch.empty_like(x2)
+        y = torch.empty_like(x2) if output else None
+        slope_rmsnorm(x2, self.weight, self.eps, residual=r2, H=None if r2 is None else h, Y=y, q=q, q_scale=scale)
+        rows = Int8Rows(q.view(x.shape), scale.view(x.shape[:-1]))
+        return (rows, h.view(x.shape), y.view(x.shape)) if output else (rows, h.view(x.shape))
+
+
+class Int8SparseLinear(torch.nn.Module):
+    """Inference form of a SparseLinear on 8-bit integer codes:
+
+        y = (q . W_q^T) * scale_row * w_scale (+ (x . L) . R)
+
+    The weight's codes and scales (one for each output) are made once, from the
+    layer's current values; the 16-bit weight is not kept.  `lin(x)` quantizes
+    the rows of a bf16 or fp16 x itself; `lin(rows)` takes an Int8Rows, and then,
+    if the layer has an adapter, the 16-bit values as well: `lin(rows, x)`."""
+
+    def __init__(self, layer: SparseLinear):
+        super().__init__()
+        N, K, dev = layer.out_features, layer.in_features, layer.values.device
+        self.in_features, self.out_features, self.rank = K, N, layer.rank
+        self.dtype = layer.values.dtype
+        self.register_buffer("packed", _bytes(slope_packed_sparse_i8_bytes(N, K), dev))
+        self.register_buffer("w_scale", torch.empty(N, dtype=torch.float32, device=dev))
+        with torch.no_grad():
+            slope_pack_sparse_i8(layer.values, layer.meta, N, K, self.w_scale, self.packed)
+            self.register_buffer("L", layer.L.detach().clone() if layer.rank else None)
+            self.register_buffer("R", layer.R.detach().clone() if layer.rank else None)
+
+    @torch.no_grad()
+    def forward(self, rows: Int8Rows | torch.Tensor, x: torch.Tensor | None = None) -> torch.Tensor:
+        K, N = self.in_features, self.out_features
+        if not isinstance(rows, Int8Rows):
+            x = rows
+        if x is not None and (x.shape[-1] != K or x.dtype != self.dtype):
+            raise ValueError("input must have in_features columns and the layer's format")
+        if self.rank and x is None:
+            raise ValueError("the adapter needs the 16-bit input next to its codes")
+        x2 = None if x is None else x.reshape(-1, K).contiguous()
+        if isinstance(rows, Int8Rows):
+            if rows.q.shape[-1] != K or rows.scale.shape != rows.q.shape[:-1] or (x is not None and x.shape != rows.q.shape):
+                raise ValueError("codes must have in_features columns, one scale a row, and the input's shape")
+            lead = rows.q.shape[:-1]
+            q, scale = rows.q.reshape(-1, K).contiguous(), rows.scale.reshape(-1).contiguous()
+        else:
+            lead = x.shape[:-1]
+            q = torch.empty(x2.shape, dtype=torch.int8, device=x2.device)
+            scale = torch.empty(x2.shape[0], dtype=torch.float32, device=x2.device)
+            slope_quantize_rows_i8(x2, q, scale)
+        T = q.shape[0]
+        y = torch.empty((T, N), dtype=self.dtype, device=q.device)
+        product = slope_spmm_i8_decode if T <= I8_DECODE_MAX_TOKENS else slope_spmm_i8_packed
+        product(q, scale, self.packed, self.w_scale, N, y)
+        if self.rank and T:
+            ws = _bytes(slope_lowrank_workspace_bytes(T, K, self.rank, N), q.device)
+            slope_lowrank_add(x2, self.L, self.R, ws, y)
+        return y.view(*lead, N)
