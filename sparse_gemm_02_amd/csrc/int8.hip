@@ -662,7 +662,8 @@ hipError_t spmm_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, 
   const int64_t tiles = cdiv(M, 128) * halves;
   const double small = tiles <= cus ? 0.42 : 0.35 + 0.0014 * (256.0 / cus) * tiles;
   const double direct = 0.13 + 0.0006 * (256.0 / cus) * (cdiv(M, 64) * cdiv(T, 64));
-  if (direct <= small && direct <= large) return decode_go<8, 2, 1, 1, 4, 2, O>(a);
+  // (a grid's second dimension ends at 65535)
+  if (direct <= small && direct <= large && cdiv(T, 64) <= 65535) return decode_go<8, 2, 1, 1, 4, 2, O>(a);
   if (small <= large) {
     static LdsLimit limit;
     auto kern = spmm_i8_kernel<SmallI8, O>;

@@ -145,6 +145,20 @@ def test_product_on_many_tiles(T, K, N):
     assert np.array_equal(c.run(S.slope_spmm_i8_packed, "bf16"), c.ref("bf16"))
 
 
+@pytest.mark.parametrize("T", [1 << 22, (1 << 22) - 64])
+def test_product_of_as_many_tokens_as_there_may_be(T):
+    K, N = 16, 4
+    c = Case(8, K, N, seed=3)
+    g = torch.Generator().manual_seed(1)
+    pick = torch.randint(0, 8, (T,), generator=g)
+    xq, xs = c.xq[pick].contiguous().cuda(), c.xs[pick].contiguous().cuda()
+    y = torch.zeros((T, N), dtype=torch.bfloat16, device="cuda")
+    S.slope_spmm_i8_packed(xq, xs, c.packed, c.ws, N, y)
+    ref = torch.from_numpy(c.ref("bf16")).bfloat16().cuda()
+    torch.cuda.synchronize()
+    assert bool((y == ref[pick.cuda()]).all())
+
+
 @pytest.mark.parametrize("T", [2, 80])
 def test_long_sums_stay_in_int32(T):
     """The widest reduction with codes at the ends of int8: sums next to 2^31."""
@@ -288,6 +302,27 @@ def test_graph_replays_equal_the_eager_calls():
         for T, b in bufs.items():
             for n in outs:
                 assert torch.equal(b[n], want[T][n]), (seed, T, n)
+
+
+def test_first_call_of_a_kernel_inside_a_capture():
+    """fp16 outputs on every kind of grid, captured before any eager call of them:
+    what a launch sets up once must not be a stream operation."""
+    shapes = [(40, 272, 260), (500, 272, 9216), (515, 656, 4100), (130, 272, 520)]
+    cases = [Case(*s, seed=5) for s in shapes]
+    args = [(c.xq.cuda(), c.xs.cuda(), c.packed, c.ws, c.N, torch.zeros((c.T, c.N), dtype=torch.float16, device="cuda"))
+            for c in cases]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for a in args:
+            S.slope_spmm_i8_packed(*a)
+    for _ in range(3):
+        for a in args:
+            a[-1].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for c, a in zip(cases, args):
+            assert np.array_equal(f64(a[-1]), c.ref("f16"))
 
 
 @pytest.mark.parametrize("T", [1, 16, 64, 512])
