@@ -221,40 +221,69 @@ struct TileI8 {
     for (int fm = 0; fm < G::FM; ++fm)
       acc[fm][ft] = __builtin_amdgcn_smfmac_i32_32x32x64_i8(f.a[fm], f.b[ft], acc[fm][ft], (int)x[fm][s], 0, 0);
   }
-  // The sums scaled and stored to Y[t][m].  The lane's scales are all loaded
-  // first, from clamped, valid places (a load behind a bounds test would be
-  // waited for by itself); M % 4 == 0: four rows are all inside or all outside.
+  // The sums scaled and stored to Y[t][m].  A lane holds four rows m of one token;
+  // stored as they are, every store would touch 32 lines with 16 bytes each (7 us
+  // a 256 x 256 tile).  So each wave turns 32 tokens at a time through its own
+  // piece of the ring (free by now), and stores whole lines.  The lane's scales
+  // are all loaded first, from clamped, valid places (a load behind a bounds test
+  // would be waited for by itself); M % 4 == 0.
   template <typename O>
   __device__ __forceinline__ void store(const i32x16 (&acc)[G::FM][G::FT], const float* __restrict__ x_scale,
                                         const float* __restrict__ w_scale, O* __restrict__ Y) const {
+    constexpr int ROW = G::WM * (int)sizeof(O) + 16;  // a token's rows, padded against bank conflicts
+    constexpr int PER = 16 / (int)sizeof(O), LANES = G::WM / PER, TOKENS = 64 / LANES;   // 16-byte pieces
+    static_assert(G::WAVES * 32 * ROW <= G::LDS_BYTES, "the ring holds every wave's piece");
+    wait_vmcnt<0>();                                 // no load into the ring is left
+    wait_lgkmcnt0();
+    barrier();
+    compiler_fence();
+    char* own = lds + wave * (32 * ROW);
     float st[G::FT];
     Pack<float, 4> sn[G::FM][4];
-    const int64_t tl = t0 + wt * G::WT + (lane & 31), ml = m0 + wm * G::WM + 4 * (lane >> 5);
+    const int64_t tw = t0 + wt * G::WT, mw = m0 + wm * G::WM;
+    const int h4 = 4 * (lane >> 5);
 #pragma unroll
-    for (int ft = 0; ft < G::FT; ++ft) st[ft] = x_scale[tl + ft * 32 < T ? tl + ft * 32 : T - 1];
+    for (int ft = 0; ft < G::FT; ++ft) {
+      const int64_t t = tw + ft * 32 + (lane & 31);
+      st[ft] = x_scale[t < T ? t : T - 1];
+    }
 #pragma unroll
     for (int fm = 0; fm < G::FM; ++fm)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t m = ml + fm * 32 + 8 * q;
+        const int64_t m = mw + fm * 32 + 8 * q + h4;
         sn[fm][q] = load_pack<float, 4>(w_scale + (m < M ? m : M - 4));
       }
+    const int64_t m = mw + (lane % LANES) * PER;
 #pragma unroll
     for (int ft = 0; ft < G::FT; ++ft) {
-      const int64_t t = tl + ft * 32;
-      if (t >= T) continue;
 #pragma unroll
-      for (int fm = 0; fm < G::FM; ++fm) {
+      for (int fm = 0; fm < G::FM; ++fm)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int64_t m = ml + fm * 32 + 8 * q;
-          if (m >= M) continue;
           float y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[i] = scaled(acc[fm][ft][4 * q + i], st[ft], sn[fm][q].v[i]);
-          store4<O>(Y + t * M + m, y);
+          store4<O>(reinterpret_cast<O*>(own + (lane & 31) * ROW) + fm * 32 + 8 * q + h4, y);
+        }
+      compiler_fence();                              // (a wave's LDS operations run in order)
+#pragma unroll
+      for (int j = 0; j < 32; j += TOKENS) {
+        const int row = j + lane / LANES;
+        const int64_t t = tw + ft * 32 + row;
+        const Pack<O, PER> y = *reinterpret_cast<const Pack<O, PER>*>(
+            __builtin_assume_aligned(own + row * ROW + (lane % LANES) * 16, 16));
+        if (t < T) {
+          O* p = Y + t * M + m;
+          if (m + PER <= M) {
+            store_pack<O, PER>(p, y);
+          } else if (m < M) {                        // 16-bit outputs, M % 8 == 4: the last four
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = y.v[i];
+          }
         }
       }
+      compiler_fence();
     }
   }
 };
@@ -313,7 +342,6 @@ __global__ __launch_bounds__(G::THREADS, G::BLOCKS* G::WAVES / 4) void spmm_i8_k
     cur = next;
     next = t.after(next);
   }
-  wait_vmcnt<0>();
   t.store(acc, x_scale, w_scale, Y);
 }
 
@@ -379,7 +407,6 @@ __device__ __forceinline__ void ping_pong_tile(char* lds, const int8_t* Xq, cons
       phase_end();
     }
   }
-  wait_vmcnt<0>();
   t.store(acc, x_scale, w_scale, Y);
 }
 
