@@ -534,17 +534,28 @@ I8_DECODE_MAX_TOKENS = 64   # SLOPE_I8_DECODE_MAX_TOKENS
 I8_MAX_COLS = 1 << 18       # SLOPE_I8_MAX_COLS
 
 
-# raw handle of a device's current stream (torch.cuda.current_stream builds a
-# Stream object first, 2 us of a 10 us call)
+# The calls of a few-token step are bound by the host, so the checks below are
+# written for the path where they pass: torch's own handles of the current stream
+# and device (its Python functions build a Stream object first: 2 us of a 10 us
+# call), one comparison chain a tensor, one dict look-up a dtype.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_CODES = {torch.float32: _F32, torch.bfloat16: _BF16, torch.float16: _F16}
+_i8, _f32t = torch.int8, torch.float32
+
+
+def _code(dtype):
+    c = _CODES.get(dtype)
+    return _dt(dtype) if c is None else c          # _dt raises
 
 
 def _rows(t, name):
     """(T, K) of a matrix with one token per row."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions [T, K], got shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have two dimensions [T, K], got shape {tuple(shape)}")
+    return shape
 
 
 def _place(index):
@@ -564,10 +575,6 @@ def _arg(t, name, shape, dtype, dev):
     raise ValueError(f"{name} is on {_place(t.get_device())}, not on {_place(dev)}")
 
 
-def _opt(t, name, shape, dtype, dev):
-    return None if t is None else _arg(t, name, shape, dtype, dev)
-
-
 def _buffer(t, name, dev):
     """(address, bytes) of a contiguous scratch or operand buffer on device `dev`."""
     if t is None:
@@ -576,7 +583,7 @@ def _buffer(t, name, dev):
         raise ValueError(f"{name} must be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {_place(t.get_device())}, not on {_place(dev)}")
-    return t.data_ptr() or 256, t.numel() * t.element_size()
+    return t.data_ptr() or 256, t.nbytes
 
 
 def _on_device(fn, dev, stream, *args):
@@ -585,7 +592,7 @@ def _on_device(fn, dev, stream, *args):
         raise ValueError("tensors must live in GPU memory")
     s = _raw_stream(dev) if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     f = getattr(_lib or library(), fn)
-    if dev == torch.cuda.current_device():
+    if dev == _device_now():
         st = f(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -601,10 +608,13 @@ def slope_rmsnorm(X, gamma, eps, residual=None, H=None, Y=None, q=None, q_scale=
     T, K = shape = _rows(X, "X")
     dt, d = X.dtype, X.get_device()
     gdt = dt if gamma is None else gamma.dtype
-    _on_device("slope_rmsnorm", d, stream, _dt(dt), _arg(X, "X", shape, dt, d), _opt(residual, "residual", shape, dt, d),
-               _dt(gdt), _opt(gamma, "gamma", (K,), gdt, d), T, K, eps, _opt(H, "H", shape, dt, d),
-               _opt(Y, "Y", shape, dt, d), _opt(q, "q", shape, torch.int8, d),
-               _opt(q_scale, "q_scale", (T,), torch.float32, d), _opt(rstd, "rstd", (T,), torch.float32, d))
+    _on_device("slope_rmsnorm", d, stream, _code(dt), _arg(X, "X", shape, dt, d),
+               None if residual is None else _arg(residual, "residual", shape, dt, d), _code(gdt),
+               None if gamma is None else _arg(gamma, "gamma", (K,), gdt, d), T, K, eps,
+               None if H is None else _arg(H, "H", shape, dt, d), None if Y is None else _arg(Y, "Y", shape, dt, d),
+               None if q is None else _arg(q, "q", shape, _i8, d),
+               None if q_scale is None else _arg(q_scale, "q_scale", (T,), _f32t, d),
+               None if rstd is None else _arg(rstd, "rstd", (T,), _f32t, d))
 
 
 def slope_rmsnorm_bwd_workspace_bytes(T: int, K: int) -> int:
@@ -622,18 +632,20 @@ def slope_rmsnorm_bwd(dY, H, rstd, gamma, dX=None, dgamma=None, workspace=None, 
     dt, d = dY.dtype, dY.get_device()
     gdt = gamma.dtype if gamma is not None else dgamma.dtype if dgamma is not None else dt
     wp, wb = _buffer(workspace, "workspace", d)
-    _on_device("slope_rmsnorm_bwd", d, stream, _dt(dt), _arg(dY, "dY", shape, dt, d), _arg(H, "H", shape, dt, d),
-               _arg(rstd, "rstd", (T,), torch.float32, d), _dt(gdt), _opt(gamma, "gamma", (K,), gdt, d),
-               _opt(dH, "dH", shape, dt, d), T, K, _opt(dX, "dX", shape, dt, d),
-               _opt(dgamma, "dgamma", (K,), gdt, d), int(bool(accumulate)), wp, wb)
+    _on_device("slope_rmsnorm_bwd", d, stream, _code(dt), _arg(dY, "dY", shape, dt, d), _arg(H, "H", shape, dt, d),
+               _arg(rstd, "rstd", (T,), _f32t, d), _code(gdt),
+               None if gamma is None else _arg(gamma, "gamma", (K,), gdt, d),
+               None if dH is None else _arg(dH, "dH", shape, dt, d), T, K,
+               None if dX is None else _arg(dX, "dX", shape, dt, d),
+               None if dgamma is None else _arg(dgamma, "dgamma", (K,), gdt, d), int(bool(accumulate)), wp, wb)
 
 
 def slope_quantize_rows_i8(X, q, scale, stream=None) -> None:
     """int8 codes q [T, K] and scales [T] of the rows of a bf16 or fp16 X [T, K]."""
     T, K = shape = _rows(X, "X")
     d = X.get_device()
-    _on_device("slope_quantize_rows_i8", d, stream, _dt(X), _arg(X, "X", shape, X.dtype, d), T, K,
-               _arg(q, "q", shape, torch.int8, d), _arg(scale, "scale", (T,), torch.float32, d))
+    _on_device("slope_quantize_rows_i8", d, stream, _code(X.dtype), _arg(X, "X", shape, X.dtype, d), T, K,
+               _arg(q, "q", shape, _i8, d), _arg(scale, "scale", (T,), _f32t, d))
 
 
 def slope_packed_sparse_i8_bytes(rows: int, cols: int) -> int:
@@ -646,19 +658,19 @@ def slope_pack_sparse_i8(values, meta, rows, cols, w_scale, packed, stream=None)
     """int8 tile chunks of a compressed 16-bit matrix, with its rows' scales in w_scale [rows]."""
     d = values.get_device()
     pp, pb = _buffer(packed, "packed", d)
-    _on_device("slope_pack_sparse_i8", d, stream, _dt(values),
+    _on_device("slope_pack_sparse_i8", d, stream, _code(values.dtype),
                _arg(values, "values", (rows, cols // 2), values.dtype, d),
                _arg(meta, "meta", (rows, (cols // 4 + 7) // 8), torch.int32, d), rows, cols,
-               _arg(w_scale, "w_scale", (rows,), torch.float32, d), pp, pb)
+               _arg(w_scale, "w_scale", (rows,), _f32t, d), pp, pb)
 
 
 def _spmm_i8(fn, Xq, x_scale, packed_w, w_scale, N, Y, stream):
     T, K = shape = _rows(Xq, "Xq")
     d = Xq.get_device()
     pp, pb = _buffer(packed_w, "packed_w", d)
-    _on_device(fn, d, stream, _dt(Y), _arg(Xq, "Xq", shape, torch.int8, d),
-               _arg(x_scale, "x_scale", (T,), torch.float32, d), T, K, pp, pb,
-               _arg(w_scale, "w_scale", (N,), torch.float32, d), N, _arg(Y, "Y", (T, N), Y.dtype, d))
+    odt = Y.dtype
+    _on_device(fn, d, stream, _code(odt), _arg(Xq, "Xq", shape, _i8, d), _arg(x_scale, "x_scale", (T,), _f32t, d), T, K,
+               pp, pb, _arg(w_scale, "w_scale", (N,), _f32t, d), N, _arg(Y, "Y", (T, N), odt, d))
 
 
 def slope_spmm_i8_packed(Xq, x_scale, packed_w, w_scale, N, Y, stream=None) -> None:

@@ -642,10 +642,12 @@ template <int R, int FM, int G, int D, int W, int WPS, typename O>
 hipError_t decode_go(const SpmmArgs<O>& a) {
   constexpr int FT = R > 4 ? 2 : 1;
   constexpr int LDS = W * (G * R * 1024 > FM * FT * 2048 ? G * R * 1024 : FM * FT * 2048);   // X rows; sums
-  static LdsLimit limit;
   auto kern = decode_i8_kernel<R, FM, G, D, W, WPS, O>;
-  const hipError_t e = limit.set((const void*)kern, LDS);
-  if (e != hipSuccess) return e;
+  if constexpr (LDS > 64 * 1024) {
+    static LdsLimit limit;
+    const hipError_t e = limit.set((const void*)kern, LDS);
+    if (e != hipSuccess) return e;
+  }
   kern<<<dim3((unsigned)cdiv(a.M, 32 * FM), (unsigned)cdiv(a.T, 8 * R)), 64 * W, LDS, a.s>>>(a.Xq, a.packed, a.M, a.T, a.K, a.xs, a.ws, a.Y);
   return hipGetLastError();
 }
@@ -668,6 +670,17 @@ hipError_t decode_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K
   return wide ? decode_go<8, 2, 1, 1, 4, 2, O>(a) : decode_go<8, 1, 1, 1, 8, 4, O>(a);
 }
 
+// device_compute_units, asked once for each device (1 us of a 5 us call).
+int64_t compute_units() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kDevices) return device_compute_units();
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) known[dev].store(n = (int)device_compute_units(), std::memory_order_relaxed);
+  return n;
+}
+
 // Any number of tokens.  Three kernels, chosen by their estimated time in units
 // of a stage (us for 128 k), fitted to sweeps of 65 .. 8192 tokens over 9216 ->
 // 9216 / 27648, 20480 -> 5120, 5120 -> 5120 / 15360 and 768 -> 2304:
@@ -676,14 +689,16 @@ hipError_t decode_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K
 //   small   128 x 128 tiles, two a compute unit: 0.42 up to one a unit, then
 //           0.35 + 0.0014 a tile
 //   direct  the few-token kernel over groups of 64 tokens: 0.13 + 0.0006 a block
-// Measured, us (large / small / direct): 9216 -> 9216 at 128 tokens 40 / 29.5 /
-// 24, 256: 41 / 31 / 37, 512: 42 / 49 / 62, 1000: 65 / 79 / 111, 8192: 380 / 491 /
-// 895; 20480 -> 5120 at 256: 79 / 58 / 51, 512: 80 / 59 / 78, 1000: 85 / 103 / 130.
+// Measured, us (large / small / direct), before the tiles were stored by whole
+// lines, which took 3 to 9% off the first two alike: 9216 -> 9216 at 128 tokens 40
+// / 29.5 / 24, 256: 41 / 31 / 37, 512: 42 / 49 / 62, 1000: 65 / 79 / 111, 8192: 380
+// / 491 / 895; 20480 -> 5120 at 256: 79 / 58 / 51, 512: 80 / 59 / 78, 1000: 85 /
+// 103 / 130.
 template <typename O>
 hipError_t spmm_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, const void* packed, const float* ws,
                        int64_t M, void* Y, hipStream_t s) {
   const SpmmArgs<O> a{Xq, (const char*)packed, (int)M, (int)T, (int)K, xs, ws, (O*)Y, s};
-  const int64_t cus = device_compute_units(), rows = cdiv(M, 256), cols = cdiv(T, 256), halves = cdiv(T, 128);
+  const int64_t cus = compute_units(), rows = cdiv(M, 256), cols = cdiv(T, 256), halves = cdiv(T, 128);
   const int64_t rows_full = full_width_rows(rows, cols, halves, cus);
   const double large = 0.010 * (100 * cdiv(rows_full * cols, cus) + 65 * cdiv((rows - rows_full) * halves, cus));
   const int64_t tiles = cdiv(M, 128) * halves;
