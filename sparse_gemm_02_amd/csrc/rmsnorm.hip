@@ -334,6 +334,7 @@ hipError_t rms_launch(const void* X_, const void* res_, const void* gamma_, int6
 
 // ---------------------------------------------------------------- gradient
 
+constexpr int kBwdWaves = 8;                            // waves of a block whose waves take a row each
 constexpr int kBwdBlocks = 512;                         // partial rows of dgamma, at most
 constexpr int64_t kBwdMaxVecs = 4096;                   // vectors of a row kept in registers (1024 threads x 4)
 
@@ -346,11 +347,11 @@ int64_t bwd_groups(int64_t T, int64_t K) {
   return T < most ? T : most;
 }
 
-// A block (WAVE: each of its four waves) takes every gridDim-th row and keeps its
+// A block (WAVE: each of its eight waves) takes every gridDim-th row and keeps its
 // columns, so dgamma's partial sums stay in registers.  The next row's loads are
 // issued before this row's sum is taken.
 template <typename In, typename GT, int E, int N, bool WAVE, bool RAGGED>
-__global__ __launch_bounds__(WAVE ? 256 : N == 4 ? 1024 : 512, N == 4 ? 4 : 2) void rms_bwd_kernel(const In* dY, const In* __restrict__ H,
+__global__ __launch_bounds__(N == 4 ? 1024 : 512, N == 4 ? 4 : 2) void rms_bwd_kernel(const In* dY, const In* __restrict__ H,
                                                                    const float* __restrict__ rstd, const GT* gamma,
                                                                    const In* dH, int64_t T, int K, In* dX,
                                                                    float* __restrict__ part) {
@@ -358,8 +359,8 @@ __global__ __launch_bounds__(WAVE ? 256 : N == 4 ? 1024 : 512, N == 4 ? 4 : 2) v
   constexpr bool AHEAD = N < 4;                       // four vectors a thread: the registers hold one row, no gamma
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tid = WAVE ? lane : (int)threadIdx.x, tpr = WAVE ? 64 : (int)blockDim.x;
-  const int64_t first = WAVE ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
-  const int64_t step = WAVE ? (int64_t)gridDim.x * 4 : (int64_t)gridDim.x;
+  const int64_t first = WAVE ? (int64_t)blockIdx.x * kBwdWaves + wave : (int64_t)blockIdx.x;
+  const int64_t step = WAVE ? (int64_t)gridDim.x * kBwdWaves : (int64_t)gridDim.x;
   const float inv_k = 1.0f / (float)K;
   const In* dHr = dH ? dH : dY;                       // no dH: dY again, and not used
   float dg[N][E];
@@ -444,33 +445,30 @@ __global__ __launch_bounds__(WAVE ? 256 : N == 4 ? 1024 : 512, N == 4 ? 4 : 2) v
   }
   if (!part) return;
   float* dst = part + (int64_t)blockIdx.x * K;
-  auto put = [&](int j, const float (&v)[E]) {
-    const Vec rv(j * tpr + tid, K);
+  if constexpr (WAVE) {
+    // the waves' sums side by side in LDS, added in wave order
+    __shared__ float all[kBwdWaves][N * E * 64];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (rv.mine(e)) dst[rv.at + e] = v[e];
-  };
-  if constexpr (!WAVE) {
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-    for (int j = 0; j < N; ++j) put(j, dg[j]);
-  } else {
-    // the four waves' sums, added in wave order
-    __shared__ float all[N * E * 64];
-    for (int w = 0; w < 4; ++w) {
-      if (wave == w) {
+      for (int e = 0; e < E; ++e) all[wave][(j * E + e) * 64 + lane] = dg[j][e];
+    __syncthreads();
+    for (int at = threadIdx.x; at < N * E * 64; at += 64 * kBwdWaves) {
+      const Vec rv((at / (64 * E)) * 64 + at % 64, K);
+      const int e = at / 64 % E;
+      if (!rv.mine(e)) continue;
+      float s = all[0][at];
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int at = (j * E + e) * 64 + lane;
-            all[at] = dg[j][e] = w == 0 ? dg[j][e] : all[at] + dg[j][e];
-          }
-      }
-      __syncthreads();
+      for (int w = 1; w < kBwdWaves; ++w) s += all[w][at];
+      dst[rv.at + e] = s;
     }
-    if (wave == 3) {
+  } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) put(j, dg[j]);
+    for (int j = 0; j < N; ++j) {
+      const Vec rv(j * tpr + tid, K);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (rv.mine(e)) dst[rv.at + e] = dg[j][e];
     }
   }
 }
@@ -545,12 +543,13 @@ __global__ __launch_bounds__(1024) void rms_dgamma_reduce_kernel(const float* __
 template <typename In, typename GT, int E, int N, bool WAVE>
 int64_t bwd_rows(const In* dY, const In* H, const float* rstd, const GT* gamma, const In* dH, int64_t T, int64_t K,
                  In* dX, float* part, hipStream_t s) {
-  const int threads = WAVE ? 256 : (int)(cdiv(cdiv(cdiv(K, E), N), 64) * 64);
+  const int threads = WAVE ? 64 * kBwdWaves : (int)(cdiv(cdiv(cdiv(K, E), N), 64) * 64);
   // a block of three or four vectors a thread leaves no room for a second one on
   // its compute unit: one round of 256 blocks (8192 x 9216: 120.5 us against 128.9
   // with 512).  Narrower rows take 512 (4096 x 2304: 20.4 us against 25.5).
-  int64_t groups = bwd_groups(WAVE ? cdiv(T, 4) : T, K);
-  if (N >= 3 && groups > 256) groups = 256;
+  // Rows of one wave: 256 blocks of eight waves.
+  int64_t groups = bwd_groups(WAVE ? cdiv(T, kBwdWaves) : T, K);
+  if ((WAVE || N >= 3) && groups > 256) groups = 256;
   if (K % E == 0)
     rms_bwd_kernel<In, GT, E, N, WAVE, false><<<(unsigned)groups, threads, 0, s>>>(dY, H, rstd, gamma, dH, T, (int)K,
                                                                                    dX, part);
@@ -573,8 +572,8 @@ hipError_t bwd_launch(const void* dY_, const void* H_, const float* rstd, const 
   const int64_t v = cdiv(K, E);
   if (T == 0) {
   } else if (K < E) {
-    groups = bwd_groups(cdiv(T, 4), K);
-    rms_bwd_kernel<In, GT, 1, 1, true, false><<<(unsigned)groups, 256, 0, s>>>(dY, H, rstd, gamma, dH, T, (int)K,
+    groups = bwd_groups(cdiv(T, kBwdWaves), K);
+    rms_bwd_kernel<In, GT, 1, 1, true, false><<<(unsigned)groups, 64 * kBwdWaves, 0, s>>>(dY, H, rstd, gamma, dH, T, (int)K,
                                                                                      dX, part);
   } else if (v <= 64) groups = bwd_rows<In, GT, E, 1, true>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
   else if (v <= 128) groups = bwd_rows<In, GT, E, 2, true>(dY, H, rstd, gamma, dH, T, K, dX, part, s);
