@@ -43,15 +43,15 @@ __global__ __launch_bounds__(256) void pack_i8_kernel(const In* __restrict__ val
   const int64_t half = K / 2, wpr = (K / 4 + 7) / 8;
   const In* v = vals + (live ? row : 0) * half;
   const uint32_t* m = meta + (live ? row : 0) * wpr;
-  RowMax<false> am{};
+  uint32_t am = 0u;
   for (int64_t c = 8 * k; c < half; c += 64) {
     const Pack<In, 8> p = load_pack<In, 8>(v + c);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) am.add(elem_f32(p.v[e]), 0.f);
+    for (int e = 0; e < 8; ++e) am = max_bits(am, mag_bits(elem_f32(p.v[e])));
   }
 #pragma unroll
-  for (int x = 4; x >= 1; x >>= 1) am.join(am.other(x));
-  const RowCodes<false> codes(am);
+  for (int x = 4; x >= 1; x >>= 1) am = max_bits(am, (uint32_t)__shfl_xor((int)am, x));
+  const RowCodes codes(am, 0.f);
   if (live && k == 0) scale[row] = codes.scale();
   for (int64_t s = 0; s < stages; ++s) {
     char* chunk = out + (tile * stages + s) * kChunkBytes;

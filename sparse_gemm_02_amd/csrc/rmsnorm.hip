@@ -33,6 +33,17 @@ __device__ __forceinline__ float wave_sum(float v) {
   for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
   return v;
 }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v = max_bits(v, (uint32_t)__shfl_xor((int)v, m));
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, m));
+  return v;
+}
+
 // The vectors of a row of K >= E elements: vector i holds elements E i .. E i +
 // E - 1; the last one, when K is not a multiple of E (RAGGED), is moved back to
 // end at K, and its first `skip` elements belong to the vector before it.  A
@@ -139,19 +150,19 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
   if (WAVE && row >= T) return;
   const int tid = WAVE ? lane : (int)threadIdx.x, tpr = WAVE ? 64 : (int)blockDim.x;
   const In* x = X + row * K;
-  const In* xr = res ? res + row * K : x;            // no residual: x again, and not used
+  const In* xr = res ? res + row * K : x;            // no residual: the row's first vector, and not used
   Pack<In, E> h[N], r[N];
   Gamma<GT, E> g[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     const int at = Vec(j * tpr + tid, K).at;
     h[j] = load_pack<In, E>(x + at);
-    r[j] = load_pack<In, E>(xr + at);
+    r[j] = load_pack<In, E>(xr + (res ? at : 0));
     if (KEEP) g[j].load(gamma + at);
   }
   __builtin_amdgcn_sched_barrier(0);
   float ss = 0.f;
-  RowMax<WIDE> am{};
+  uint32_t mine = 0u;                                // largest |h g| (as fp32) of this thread
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     const Vec rv(j * tpr + tid, K);
@@ -167,34 +178,58 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
     for (int e = 0; e < E; ++e) {
       const float f = elem_f32(h[j].v[e]);
       ss = __builtin_fmaf(f, f, ss);
-      if (o.q) {
-        const float w = g[j](e), p = f * w;
-        am.add(p, WIDE ? __builtin_fmaf(f, w, -p) : 0.f);
-      }
+      if (o.q) mine = max_bits(mine, mag_bits(f * g[j](e)));
     }
   }
   ss = wave_sum(ss);
-  if (o.q) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) am.join(am.other(m));
-  }
+  uint32_t hi = o.q ? wave_max(mine) : 0u;
   if constexpr (!WAVE) {
     __shared__ float sums[16];
-    __shared__ RowMax<WIDE> maxs[16];
+    __shared__ uint32_t maxs[16];
     if (lane == 0) {
       sums[wave] = ss;
-      maxs[wave] = am;
+      maxs[wave] = hi;
     }
     __syncthreads();
     ss = sums[0];
-    am = maxs[0];
+    hi = maxs[0];
     for (int w = 1; w < tpr / 64; ++w) {
       ss += sums[w];
-      am.join(maxs[w]);
+      hi = max_bits(hi, maxs[w]);
+    }
+  }
+  float lo = 0.f;
+  if constexpr (WIDE) {
+    // of the values that share the row's largest p (one, as a rule), the largest
+    // left-over: looked for by the threads that have such a value.  Carried along
+    // with every maximum it cost a fifth of the kernel's arithmetic.
+    if (o.q) {
+      float r = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < N; ++j) forget<In, E>(h[j]);
+      if (mine == hi) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          if (!KEEP) g[j].load(gamma + Vec(j * tpr + tid, K).at);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float f = elem_f32(h[j].v[e]), w = g[j](e), p = f * w;
+            if (mag_bits(p) == hi) r = __builtin_fmaxf(r, left_over(f, w, p));
+          }
+        }
+      }
+      lo = wave_max(r);
+      if constexpr (!WAVE) {
+        __shared__ float rests[16];
+        if (lane == 0) rests[wave] = lo;
+        __syncthreads();
+        lo = rests[0];
+        for (int w = 1; w < tpr / 64; ++w) lo = __builtin_fmaxf(lo, rests[w]);
+      }
     }
   }
   const float rstd = o.norm ? 1.0f / sqrtf(ss / (float)K + eps) : 1.0f;
-  const RowCodes<WIDE> codes(am);
+  const RowCodes codes(hi, lo);
   if (tid == 0) {
     if (o.rstd) o.rstd[row] = rstd;
     if (o.q) o.qs[row] = codes.scale() * rstd;
@@ -258,9 +293,8 @@ __device__ __forceinline__ float gamma_at(const GT* gamma, int64_t k) {
 template <typename In, typename GT>
 __global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* res, const GT* gamma, int64_t K,
                                                         float eps, NormOut o) {
-  constexpr bool WIDE = kWide<In, GT>;
-  __shared__ float sums[16];
-  __shared__ RowMax<WIDE> maxs[16];
+  __shared__ float sums[16], rests[16];
+  __shared__ uint32_t maxs[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = blockIdx.x, base = row * K;
   In* H = (In*)o.H;
@@ -268,30 +302,44 @@ __global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* r
     return res ? elem_of<In>(elem_f32(X[base + k]) + elem_f32(res[base + k])) : X[base + k];
   };
   float ss = 0.f;
-  RowMax<WIDE> am{};
+  uint32_t mine = 0u;
   for (int64_t k = threadIdx.x; k < K; k += 1024) {
     const In h = sum_at(k);
-    const float f = elem_f32(h), w = gamma_at(gamma, k), p = f * w;
+    const float f = elem_f32(h);
     ss = __builtin_fmaf(f, f, ss);
-    am.add(p, WIDE ? __builtin_fmaf(f, w, -p) : 0.f);
+    mine = max_bits(mine, mag_bits(f * gamma_at(gamma, k)));
     if (H) H[base + k] = h;
   }
   ss = wave_sum(ss);
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) am.join(am.other(m));
+  uint32_t hi = wave_max(mine);
   if (lane == 0) {
     sums[wave] = ss;
-    maxs[wave] = am;
+    maxs[wave] = hi;
   }
   __syncthreads();
   ss = sums[0];
-  am = maxs[0];
+  hi = maxs[0];
   for (int w = 1; w < 16; ++w) {
     ss += sums[w];
-    am.join(maxs[w]);
+    hi = max_bits(hi, maxs[w]);
+  }
+  float lo = 0.f;
+  if constexpr (kWide<In, GT>) {
+    float r = -__builtin_inff();
+    if (mine == hi) {
+      for (int64_t k = threadIdx.x; k < K; k += 1024) {
+        const float f = elem_f32(H ? H[base + k] : sum_at(k)), w = gamma_at(gamma, k), p = f * w;
+        if (mag_bits(p) == hi) r = __builtin_fmaxf(r, left_over(f, w, p));
+      }
+    }
+    r = wave_max(r);
+    if (lane == 0) rests[wave] = r;
+    __syncthreads();
+    lo = rests[0];
+    for (int w = 1; w < 16; ++w) lo = __builtin_fmaxf(lo, rests[w]);
   }
   const float rstd = o.norm ? 1.0f / sqrtf(ss / (float)K + eps) : 1.0f;
-  const RowCodes<WIDE> codes(am);
+  const RowCodes codes(hi, lo);
   if (threadIdx.x == 0) {
     if (o.rstd) o.rstd[row] = rstd;
     if (o.q) o.qs[row] = codes.scale() * rstd;
@@ -362,7 +410,7 @@ __global__ __launch_bounds__(N == 4 ? 1024 : 512, N == 4 ? 4 : 2) void rms_bwd_k
   const int64_t first = WAVE ? (int64_t)blockIdx.x * kBwdWaves + wave : (int64_t)blockIdx.x;
   const int64_t step = WAVE ? (int64_t)gridDim.x * kBwdWaves : (int64_t)gridDim.x;
   const float inv_k = 1.0f / (float)K;
-  const In* dHr = dH ? dH : dY;                       // no dH: dY again, and not used
+  const In* dHr = dH ? dH : dY;                       // no dH: dY's first vector, and not used
   float dg[N][E];
   Gamma<GT, E> g[N];
 #pragma unroll
@@ -382,7 +430,7 @@ __global__ __launch_bounds__(N == 4 ? 1024 : 512, N == 4 ? 4 : 2) void rms_bwd_k
       const int at = Vec(j * tpr + tid, K).at;
       w.dy[j] = load_pack<In, E>(dY + base + at);
       w.h[j] = load_pack<In, E>(H + base + at);
-      if (AHEAD) w.r[j] = load_pack<In, E>(dHr + base + at);
+      if (AHEAD) w.r[j] = load_pack<In, E>(dHr + (dH ? base + at : 0));
     }
     w.rs = rstd[row];
   };
@@ -425,7 +473,7 @@ __global__ __launch_bounds__(N == 4 ? 1024 : 512, N == 4 ? 4 : 2) void rms_bwd_k
       for (int j = 0; j < N; ++j) {
         const Vec rv(j * tpr + tid, K);
         if (!AHEAD) {
-          now.r[j] = load_pack<In, E>(dHr + base + rv.at);
+          now.r[j] = load_pack<In, E>(dHr + (dH ? base + rv.at : 0));
           g[j].load(gamma + rv.at);
         }
         forget<In, E>(now.dy[j]);

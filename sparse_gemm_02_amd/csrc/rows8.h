@@ -32,52 +32,24 @@ template <> __device__ __forceinline__ float elem_of<float>(float f) { return f;
 
 // ---------------------------------------------------------------- codes of a row
 // code = the integer nearest to 127 u / amax, ties to even; amax = max |u| of the
-// row, u = h g the exact product of two stored values.  u travels as an fp32
-// pair: p = fp32(h g) and what the rounding left, e = h g - p (zero where g has
-// 16 bits too: the product then fits).
+// row, u = h g the exact product of two stored values.  u is seen as p = fp32(h g)
+// and what the rounding left, h g - p (zero where g has 16 bits too: the product
+// then fits).
 
-// Largest |u| of the values seen so far: the bits of its p, and its e with p's
-// sign taken off.  Magnitude bits order like magnitudes, with infinity and NaN on
-// top, so a row without a finite maximum shows in `hi`.
-template <bool WIDE> struct RowMax;
-template <> struct RowMax<false> {
-  uint32_t hi;                                       // start from {} (zero)
-  __device__ __forceinline__ void add(float p, float) {
-    const uint32_t b = __float_as_uint(p) & 0x7FFFFFFFu;
-    hi = b > hi ? b : hi;
-  }
-  __device__ __forceinline__ void join(const RowMax& o) { hi = o.hi > hi ? o.hi : hi; }
-  __device__ __forceinline__ RowMax other(int mask) const {
-    RowMax o;
-    o.hi = (uint32_t)__shfl_xor((int)hi, mask);
-    return o;
-  }
-  __device__ __forceinline__ double exact() const { return (double)__uint_as_float(hi); }
-};
-template <> struct RowMax<true> {
-  uint32_t hi;                                       // start from {} (zero)
-  float lo;
-  __device__ __forceinline__ void take(uint32_t b, float r) {
-    const bool up = b > hi || (b == hi && r > lo);
-    hi = up ? b : hi;
-    lo = up ? r : lo;
-  }
-  __device__ __forceinline__ void add(float p, float e) {
-    const uint32_t b = __float_as_uint(p);
-    take(b & 0x7FFFFFFFu, __uint_as_float(__float_as_uint(e) ^ (b & 0x80000000u)));
-  }
-  __device__ __forceinline__ void join(const RowMax& o) { take(o.hi, o.lo); }
-  __device__ __forceinline__ RowMax other(int mask) const {
-    RowMax o;
-    o.hi = (uint32_t)__shfl_xor((int)hi, mask);
-    o.lo = __shfl_xor(lo, mask);
-    return o;
-  }
-  __device__ __forceinline__ double exact() const { return (double)__uint_as_float(hi) + (double)lo; }
-};
+// Bits of |p|: they order like magnitudes, with infinity and NaN on top, so a row
+// without a finite maximum shows in the largest.
+__device__ __forceinline__ uint32_t mag_bits(float p) { return __float_as_uint(p) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// |f w| - |p| for p = fp32(f w), exact
+__device__ __forceinline__ float left_over(float f, float w, float p) {
+  return __builtin_copysignf(1.0f, p) * __builtin_fmaf(f, w, -p);
+}
 
 constexpr float kCodeMagic = 12582912.0f;             // 1.5 * 2^23: adding it rounds to an integer, ties to even
 
+// Codes of a row whose largest |p| has the bits `hi`, and of whose values with that
+// p the largest left-over is `lo`: amax = hi + lo.
+//
 // The quotient from one fp32 reciprocal, q = p * (127 / hi), is within 2^-14 of
 // the true one (|q| <= 127; p, hi, the division and the product each round by
 // 2^-24 at most), so its rounding is decided unless it lies within 1e-4 of a
@@ -85,29 +57,27 @@ constexpr float kCodeMagic = 12582912.0f;             // 1.5 * 2^23: adding it r
 // exact in double (products of at most 43 bits).  About one value in 5000 takes
 // that branch.  Rows whose amax is below 2^-100, where products leave fp32's
 // normal range, go by double throughout.
-template <bool WIDE>
 struct RowCodes {
-  RowMax<WIDE> top;
-  float inv;
+  uint32_t hi;
+  float lo, inv;
   bool bad, tiny;
-  __device__ __forceinline__ explicit RowCodes(const RowMax<WIDE>& m) : top(m) {
-    bad = m.hi >= 0x7F800000u;
-    tiny = m.hi < 0x0D800000u;                       // 2^-100
-    inv = bad || tiny ? 0.f : 127.0f / __uint_as_float(m.hi);
+  __device__ __forceinline__ RowCodes(uint32_t hi_, float lo_) : hi(hi_), lo(lo_) {
+    bad = hi >= 0x7F800000u;
+    tiny = hi < 0x0D800000u;                         // 2^-100
+    inv = bad || tiny ? 0.f : 127.0f / __uint_as_float(hi);
   }
-  __device__ __forceinline__ float scale() const {
-    return bad ? __builtin_nanf("") : __uint_as_float(top.hi) / 127.0f;
-  }
+  __device__ __forceinline__ float scale() const { return bad ? __builtin_nanf("") : __uint_as_float(hi) / 127.0f; }
+  __device__ __forceinline__ double amax() const { return (double)__uint_as_float(hi) + (double)lo; }
   // the code beside the border next to q (k = q rounded)
   __device__ __forceinline__ float at_border(double u, float q, float k) const {
-    const double twice = 2.0 * (double)k + (q > k ? 1.0 : -1.0), d = 254.0 * u - twice * top.exact();
-    const int lo = (int)(0.5 * (twice - 1.0));        // the codes on its two sides: lo, lo + 1
-    return (float)(d > 0.0 ? lo + 1 : d < 0.0 ? lo : lo + (lo & 1));
+    const double twice = 2.0 * (double)k + (q > k ? 1.0 : -1.0), d = 254.0 * u - twice * amax();
+    const int below = (int)(0.5 * (twice - 1.0));     // the codes on its two sides: below, below + 1
+    return (float)(d > 0.0 ? below + 1 : d < 0.0 ? below : below + (below & 1));
   }
   // one value, any row
   __device__ __forceinline__ int code(double u) const {
-    if (bad || top.hi == 0u) return 0;
-    const double q = 127.0 * u / top.exact();
+    if (bad || hi == 0u) return 0;
+    const double q = 127.0 * u / amax();
     const float k = (float)__builtin_rint(q);
     return (int)(__builtin_fabs(q - k) > 0.4999 ? at_border(u, (float)q, k) : k);
   }
