@@ -15,8 +15,9 @@
  * The quotient is decided exactly, not in rounded arithmetic, so the codes are
  * a function of the row's values alone (no order of a sum enters, also after
  * the norm below, where rstd is common to a whole row and cancels).  A row of
- * zeros has codes 0 and scale 0.  A row that holds an infinity or a NaN has
- * codes 0 and scale NaN, so everything computed from it is NaN.  (The pages
+ * zeros has codes 0 and scale 0.  A row that holds an infinity, a NaN or a
+ * product past float32's range has codes 0 and scale NaN, so everything computed
+ * from it is NaN.  (The pages
  * that slope.h names give no 8-bit format; slope_quantize_e4m3's reading has
  * one scale for a whole tensor.)
  */
@@ -41,8 +42,7 @@ extern "C" {
  *   rstd = 1 / sqrt(mean_k h^2 + eps)
  *   y    = h * rstd * gamma      (float32, rounded to dt once)
  *   q, q_scale = the 8-bit integer reading of the row u = h * gamma, the
- *          products taken exactly (in float32 for a 16-bit gamma), the scale
- *          amax / 127 * rstd
+ *          products taken exactly, the scale amax / 127 * rstd
  * h is used as rounded, so a gradient or a later call that starts from H sees
  * the same numbers.  Sums are float32.
  *   X, residual_or_null  [T, K] dt

@@ -51,8 +51,8 @@ __global__ __launch_bounds__(256) void pack_i8_kernel(const In* __restrict__ val
   }
 #pragma unroll
   for (int x = 4; x >= 1; x >>= 1) am = max_bits(am, (uint32_t)__shfl_xor((int)am, x));
-  const RowCodes codes(am, 0.f);
-  if (live && k == 0) scale[row] = codes.scale();
+  const RowCodes codes(am, (double)__uint_as_float(am));
+  if (live && k == 0) scale[row] = codes.scale(1.0f);
   for (int64_t s = 0; s < stages; ++s) {
     char* chunk = out + (tile * stages + s) * kChunkBytes;
     const int64_t c0 = s * 64 + 8 * k, word = 4 * s + (k & 3);

@@ -43,6 +43,19 @@ __device__ __forceinline__ float wave_max(float v) {
   for (int m = 32; m >= 1; m >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, m));
   return v;
 }
+__device__ __forceinline__ double wave_max(double v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v = __builtin_fmax(v, __shfl_xor(v, m));
+  return v;
+}
+
+// A value that all lanes share, in scalar registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+__device__ __forceinline__ float uniform(float v) { return __uint_as_float(uniform(__float_as_uint(v))); }
+__device__ __forceinline__ double uniform(double v) {
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{uniform(w[0]), uniform(w[1])});
+}
 
 // The vectors of a row of K >= E elements: vector i holds elements E i .. E i +
 // E - 1; the last one, when K is not a multiple of E (RAGGED), is moved back to
@@ -126,6 +139,9 @@ struct Gamma<Ones, E> {
 // (fp32 rows have no codes.)
 template <typename In, typename GT>
 constexpr bool kWide = std::is_same<GT, float>::value && !std::is_same<In, float>::value;
+// Products that may leave fp32's range below (fp16 values times fp16 ones do not).
+template <typename In, typename GT>
+constexpr bool kMayVanish = kWide<In, GT> || (std::is_same<In, uint16_t>::value && kHasGamma<GT>);
 
 struct NormOut {
   void *H, *Y;
@@ -198,6 +214,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
       hi = max_bits(hi, maxs[w]);
     }
   }
+  hi = uniform(hi);
   float lo = 0.f;
   if constexpr (WIDE) {
     // of the values that share the row's largest p (one, as a rule), the largest
@@ -228,11 +245,33 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
       }
     }
   }
-  const float rstd = o.norm ? 1.0f / sqrtf(ss / (float)K + eps) : 1.0f;
-  const RowCodes codes(hi, lo);
+  double amax = (double)__uint_as_float(hi) + (double)lo;
+  if constexpr (kMayVanish<In, GT>) {
+    if (o.q && tiny_bits(hi)) {                      // the same for the whole row
+      double m = 0.0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        forget<In, E>(h[j]);
+        if (!KEEP) g[j].load(gamma + Vec(j * tpr + tid, K).at);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          m = __builtin_fmax(m, __builtin_fabs((double)elem_f32(h[j].v[e]) * (double)g[j](e)));
+      }
+      amax = wave_max(m);
+      if constexpr (!WAVE) {
+        __shared__ double tops[16];
+        if (lane == 0) tops[wave] = amax;
+        __syncthreads();
+        amax = tops[0];
+        for (int w = 1; w < tpr / 64; ++w) amax = __builtin_fmax(amax, tops[w]);
+      }
+    }
+  }
+  const float rstd = uniform(o.norm ? 1.0f / sqrtf(ss / (float)K + eps) : 1.0f);
+  const RowCodes codes(hi, uniform(amax));
   if (tid == 0) {
     if (o.rstd) o.rstd[row] = rstd;
-    if (o.q) o.qs[row] = codes.scale() * rstd;
+    if (o.q) o.qs[row] = codes.scale(rstd);
   }
   if (!o.Y && !o.q) return;
 #pragma unroll
@@ -295,6 +334,7 @@ __global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* r
                                                         float eps, NormOut o) {
   __shared__ float sums[16], rests[16];
   __shared__ uint32_t maxs[16];
+  __shared__ double tops[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = blockIdx.x, base = row * K;
   In* H = (In*)o.H;
@@ -338,11 +378,24 @@ __global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* r
     lo = rests[0];
     for (int w = 1; w < 16; ++w) lo = __builtin_fmaxf(lo, rests[w]);
   }
+  double amax = (double)__uint_as_float(hi) + (double)lo;
+  if constexpr (kMayVanish<In, GT>) {
+    if (o.q && tiny_bits(hi)) {                      // the same for the whole row
+      double m = 0.0;
+      for (int64_t k = threadIdx.x; k < K; k += 1024)
+        m = __builtin_fmax(m, __builtin_fabs((double)elem_f32(H ? H[base + k] : sum_at(k)) * (double)gamma_at(gamma, k)));
+      m = wave_max(m);
+      if (lane == 0) tops[wave] = m;
+      __syncthreads();
+      amax = tops[0];
+      for (int w = 1; w < 16; ++w) amax = __builtin_fmax(amax, tops[w]);
+    }
+  }
   const float rstd = o.norm ? 1.0f / sqrtf(ss / (float)K + eps) : 1.0f;
-  const RowCodes codes(hi, lo);
+  const RowCodes codes(hi, amax);
   if (threadIdx.x == 0) {
     if (o.rstd) o.rstd[row] = rstd;
-    if (o.q) o.qs[row] = codes.scale() * rstd;
+    if (o.q) o.qs[row] = codes.scale(rstd);
   }
   if (!o.Y && !o.q) return;
   for (int64_t k = threadIdx.x; k < K; k += 1024) {   // each element by the thread that made it
@@ -641,12 +694,23 @@ hipError_t bwd_launch(const void* dY_, const void* H_, const float* rstd, const 
   return hipGetLastError();
 }
 
+// Rows of one launch: a grid ends below 2^32 threads, a row takes 1024 at most.
+constexpr int64_t kLaunchRows = int64_t(1) << 21;
+
 template <typename In>
-hipError_t rms_any(const void* X, const void* res, bool wide, const void* gamma, int64_t T, int64_t K, float eps,
-                   const NormOut& o, hipStream_t s) {
-  if (!gamma) return rms_launch<In, Ones>(X, res, gamma, T, K, eps, o, s);
-  return wide ? rms_launch<In, float>(X, res, gamma, T, K, eps, o, s)
-              : rms_launch<In, In>(X, res, gamma, T, K, eps, o, s);
+hipError_t rms_any(const void* X_, const void* res_, bool wide, const void* gamma, int64_t T, int64_t K, float eps,
+                   const NormOut& all, hipStream_t s) {
+  for (int64_t t = 0; t < T; t += kLaunchRows) {
+    const int64_t n = T - t < kLaunchRows ? T - t : kLaunchRows, at = t * K;
+    const In *X = (const In*)X_ + at, *res = res_ ? (const In*)res_ + at : nullptr;
+    const NormOut o{all.H ? (In*)all.H + at : nullptr, all.Y ? (In*)all.Y + at : nullptr, all.q ? all.q + at : nullptr,
+                    all.q ? all.qs + t : nullptr, all.rstd ? all.rstd + t : nullptr, all.norm};
+    const hipError_t e = !gamma ? rms_launch<In, Ones>(X, res, gamma, n, K, eps, o, s)
+                         : wide ? rms_launch<In, float>(X, res, gamma, n, K, eps, o, s)
+                                : rms_launch<In, In>(X, res, gamma, n, K, eps, o, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename In>

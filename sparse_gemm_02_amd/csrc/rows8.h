@@ -47,37 +47,47 @@ __device__ __forceinline__ float left_over(float f, float w, float p) {
 
 constexpr float kCodeMagic = 12582912.0f;             // 1.5 * 2^23: adding it rounds to an integer, ties to even
 
-// Codes of a row whose largest |p| has the bits `hi`, and of whose values with that
-// p the largest left-over is `lo`: amax = hi + lo.
+// Below it a row's products leave fp32's normal range, and p may have lost bits that
+// no left-over shows.
+constexpr uint32_t kTinyBits = 0x0D800000u;           // 2^-100
+__device__ __forceinline__ bool tiny_bits(uint32_t hi) { return hi < kTinyBits; }
+
+// Codes of a row whose largest |p| has the bits `hi` and whose largest |u| is amax:
+// hi and the largest left-over of the values with that p, or, in a row of tiny_bits,
+// the largest of the products themselves.
 //
 // The quotient from one fp32 reciprocal, q = p * (127 / hi), is within 2^-14 of
 // the true one (|q| <= 127; p, hi, the division and the product each round by
 // 2^-24 at most), so its rounding is decided unless it lies within 1e-4 of a
 // border k + 1/2.  There the sign of 254 u - (2k + 1) amax decides, which is
 // exact in double (products of at most 43 bits).  About one value in 5000 takes
-// that branch.  Rows whose amax is below 2^-100, where products leave fp32's
-// normal range, go by double throughout.
+// that branch.  Rows of tiny_bits go by double throughout.
 struct RowCodes {
+  double amax;
   uint32_t hi;
-  float lo, inv;
+  float inv;
   bool bad, tiny;
-  __device__ __forceinline__ RowCodes(uint32_t hi_, float lo_) : hi(hi_), lo(lo_) {
+  __device__ __forceinline__ RowCodes(uint32_t hi_, double amax_) : amax(amax_), hi(hi_) {
     bad = hi >= 0x7F800000u;
-    tiny = hi < 0x0D800000u;                         // 2^-100
+    tiny = tiny_bits(hi);
     inv = bad || tiny ? 0.f : 127.0f / __uint_as_float(hi);
   }
-  __device__ __forceinline__ float scale() const { return bad ? __builtin_nanf("") : __uint_as_float(hi) / 127.0f; }
-  __device__ __forceinline__ double amax() const { return (double)__uint_as_float(hi) + (double)lo; }
+  // (a tiny row's own scale may be far below fp32's normal range where the product
+  // with the norm's factor is not: one rounding of both)
+  __device__ __forceinline__ float scale(float rstd) const {
+    if (bad) return __builtin_nanf("");
+    return tiny ? (float)(amax / 127.0 * (double)rstd) : __uint_as_float(hi) / 127.0f * rstd;
+  }
   // the code beside the border next to q (k = q rounded)
   __device__ __forceinline__ float at_border(double u, float q, float k) const {
-    const double twice = 2.0 * (double)k + (q > k ? 1.0 : -1.0), d = 254.0 * u - twice * amax();
+    const double twice = 2.0 * (double)k + (q > k ? 1.0 : -1.0), d = 254.0 * u - twice * amax;
     const int below = (int)(0.5 * (twice - 1.0));     // the codes on its two sides: below, below + 1
     return (float)(d > 0.0 ? below + 1 : d < 0.0 ? below : below + (below & 1));
   }
   // one value, any row
   __device__ __forceinline__ int code(double u) const {
-    if (bad || hi == 0u) return 0;
-    const double q = 127.0 * u / amax();
+    if (bad || amax == 0.0) return 0;
+    const double q = 127.0 * u / amax;
     const float k = (float)__builtin_rint(q);
     return (int)(__builtin_fabs(q - k) > 0.4999 ? at_border(u, (float)q, k) : k);
   }

@@ -209,6 +209,58 @@ def test_codes_next_to_borders(gdt):
     check_norm(x, None, gamma, "bf16", y=False, h=False, rstd=False)
 
 
+@pytest.mark.parametrize("K", [5, 24, 1001, 5120, 20000, 70000])
+@pytest.mark.parametrize("dt,gdt,sizes", [("bf16", "bf16", (-48, -52, -64, -72, -80, -100)),
+                                          ("bf16", "f32", (-48, -55, -64, -72, -80)), ("f16", "f32", (-7, -12))])
+def test_codes_of_vanishing_products(K, dt, gdt, sizes):
+    """Rows whose products h gamma lie around and below fp32's smallest numbers,
+    where h and gamma themselves do not.  A scale is one rounding of amax / 127
+    rstd (half a step, or half of fp32's smallest number), and rstd's error."""
+    g = torch.Generator().manual_seed(K)
+    x = torch.stack([torch.randn(K, generator=g) * 2.0 ** s for s in sizes]).to(DT[dt]).cuda()
+    gamma = (1 + 0.2 * torch.randn(K, generator=g)) * 2.0 ** (-126 if dt == "f16" else -62)
+    gamma = gamma.to(DT[gdt]).cuda()
+    q, sc = torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(len(sizes), device="cuda")
+    S.slope_rmsnorm(x, gamma, EPS, q=q, q_scale=sc)
+    torch.cuda.synchronize()
+    qr, amax = oracle.row_codes_i8(f64(x) * f64(gamma))
+    assert np.array_equal(f64(q), qr.astype(np.float64))
+    want = amax / 127 * oracle.rmsnorm(f64(x), None, EPS)[1]
+    close(f64(sc), want, 2.0 ** -17 * want + TINY["f32"])
+
+
+def test_codes_of_products_past_float32():
+    """A finite product that fp32 does not hold is an infinity to the row."""
+    x = torch.full((2, 64), 2.0 ** 80, dtype=torch.bfloat16, device="cuda")
+    x[1] = 1.0
+    gamma = torch.full((64,), 2.0 ** 80, dtype=torch.bfloat16, device="cuda")
+    q, sc = torch.full((2, 64), 5, dtype=torch.int8, device="cuda"), torch.empty(2, device="cuda")
+    S.slope_rmsnorm(x, gamma, EPS, q=q, q_scale=sc)
+    torch.cuda.synchronize()
+    assert torch.isnan(sc[0]) and not q[0].any() and bool((q[1] == 127).all()) and torch.isfinite(sc[1])
+
+
+def test_norm_of_as_many_rows_as_there_may_be():
+    """More rows than one grid takes: the last rows as they are by themselves."""
+    T, K = 1 << 22, 24
+    x = rand(6, 4096, K).repeat(T // 4096, 1)
+    x[-4096:] = rand(7, 4096, K)
+    gamma = rand(8, K, mean=1.0, sigma=0.2)
+
+    def run(v, res):
+        H, Y, q = torch.empty_like(v), torch.empty_like(v), torch.empty(v.shape, dtype=torch.int8, device="cuda")
+        sc, rstd = torch.empty(len(v), device="cuda"), torch.empty(len(v), device="cuda")
+        S.slope_rmsnorm(v, gamma, EPS, residual=res, H=H, Y=Y, q=q, q_scale=sc, rstd=rstd)
+        return H, Y, q, sc, rstd
+    all_rows, last = run(x, x), run(x[-4096:], x[-4096:])
+    first = run(x[:4096], x[:4096])
+    torch.cuda.synchronize()
+    for a, l, f in zip(all_rows, last, first):
+        assert torch.equal(a[-4096:], l)
+        for at in (0, T // 2 - 4096, T // 2):
+            assert torch.equal(a[at:at + 4096], f)
+
+
 def test_quantizer_takes_unaligned_code_rows():
     x = rand(4, 3, 48)
     buf = torch.zeros(3 * 48 + 5, dtype=torch.int8, device="cuda")
