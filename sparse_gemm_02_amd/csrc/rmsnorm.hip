@@ -27,21 +27,45 @@ namespace {
 // Elements per 16-byte access of a format.
 template <typename In> constexpr int vec_elems() { return 16 / (int)sizeof(In); }
 
-// Sum of v over the 64 lanes, the same in every lane (fixed order).
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
-  return v;
+// Sums and maxima over lanes: the same in every lane, in a fixed order.  Lanes
+// change values by cross-lane moves in the vector unit (a shuffle through LDS takes
+// some 100 cycles for each of its six steps; one row of 9216: 4.9 us with them,
+// 4.2 so).
+template <int CTRL, typename V>
+__device__ __forceinline__ V lane_move(V v) {
+  return __builtin_bit_cast(V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = max_bits(v, (uint32_t)__shfl_xor((int)v, m));
-  return v;
+struct Add {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_fmaxf(a, b); }
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return max_bits(a, b); }
+};
+// over each sixteen lanes
+template <class Op, typename V>
+__device__ __forceinline__ V fold16(V v) {
+  v = Op()(v, lane_move<0xB1>(v));                   // neighbours
+  v = Op()(v, lane_move<0x4E>(v));                   // pairs of four
+  v = Op()(v, lane_move<0x141>(v));                  // eight lanes mirrored
+  return Op()(v, lane_move<0x140>(v));               // sixteen lanes mirrored
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, m));
-  return v;
+// over the wave
+template <class Op, typename V>
+__device__ __forceinline__ V fold(V v) {
+  v = fold16<Op>(v);
+  const uint32_t a = __builtin_bit_cast(uint32_t, v);
+  const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  v = Op()(__builtin_bit_cast(V, (uint32_t)x[0]), __builtin_bit_cast(V, (uint32_t)x[1]));
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return Op()(__builtin_bit_cast(V, (uint32_t)y[0]), __builtin_bit_cast(V, (uint32_t)y[1]));
+}
+// over the values that a block's waves (at most 16) have put into `part`
+template <class Op, typename V>
+__device__ __forceinline__ V fold_waves(const V* part, int waves, V none) {
+  const int w = threadIdx.x & 15;
+  return fold16<Op>(w < waves ? part[w] : none);
 }
 __device__ __forceinline__ double wave_max(double v) {
 #pragma unroll
@@ -153,7 +177,7 @@ struct NormOut {
 // One row per block (WAVE: per wave, four rows a block), N vectors a thread.  All
 // of the row's loads are issued before the first use: written as the formula
 // reads, with loads under `if (residual)`, the compiler waited for each vector
-// before it asked for the next (one row of 9216: 6.2 us against 4.0).
+// before it asked for the next (one row of 9216: 6.4 us against 4.9).
 template <typename In, typename GT, int E, int N, bool WAVE, bool RAGGED>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X, const In* res, const GT* gamma,
                                                                     int64_t T, int K, float eps, NormOut o) {
@@ -161,6 +185,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
   constexpr bool WIDE = kWide<In, GT>;
   // gamma stays in registers between its two uses unless they would spill
   constexpr bool KEEP = N < 8;
+  constexpr bool CODES = !std::is_same<In, float>::value;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
   if (WAVE && row >= T) return;
@@ -178,7 +203,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
   }
   __builtin_amdgcn_sched_barrier(0);
   float ss = 0.f;
-  uint32_t mine = 0u;                                // largest |h g| (as fp32) of this thread
+  float top = 0.f;                                   // largest |h g| (as fp32) of this thread, and its bits
+  uint32_t mine = 0u;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     const Vec rv(j * tpr + tid, K);
@@ -189,16 +215,20 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
     drop_foreign<In, E, RAGGED>(h[j], rv);
     if (o.H) store_vec<In, E, RAGGED>((In*)o.H + row * K, rv, h[j]);
     if (!KEEP) g[j].load(gamma + rv.at);
-    if (o.q) g[j].drop(rv);                          // its foreign elements need not be finite
+    if (CODES) g[j].drop(rv);                       // its foreign elements need not be finite
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float f = elem_f32(h[j].v[e]);
       ss = __builtin_fmaf(f, f, ss);
-      if (o.q) mine = max_bits(mine, mag_bits(f * g[j](e)));
+      // (with the second form for eight vectors the compiler spills a hundred
+      // registers: 2048 x 32768 214 us against 107)
+      if (o.q && !KEEP) mine = max_bits(mine, mag_bits(f * g[j](e)));
+      else if (CODES && KEEP) top = max_mag(top, f * g[j](e));
     }
   }
-  ss = wave_sum(ss);
-  uint32_t hi = o.q ? wave_max(mine) : 0u;
+  if (KEEP) mine = mag_bits(top);
+  ss = fold<Add>(ss);
+  uint32_t hi = o.q ? fold<Max>(mine) : 0u;
   if constexpr (!WAVE) {
     __shared__ float sums[16];
     __shared__ uint32_t maxs[16];
@@ -207,12 +237,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
       maxs[wave] = hi;
     }
     __syncthreads();
-    ss = sums[0];
-    hi = maxs[0];
-    for (int w = 1; w < tpr / 64; ++w) {
-      ss += sums[w];
-      hi = max_bits(hi, maxs[w]);
-    }
+    ss = fold_waves<Add>(sums, tpr / 64, 0.f);
+    hi = fold_waves<Max>(maxs, tpr / 64, 0u);
   }
   hi = uniform(hi);
   float lo = 0.f;
@@ -235,13 +261,12 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
           }
         }
       }
-      lo = wave_max(r);
+      lo = fold<Max>(r);
       if constexpr (!WAVE) {
         __shared__ float rests[16];
         if (lane == 0) rests[wave] = lo;
         __syncthreads();
-        lo = rests[0];
-        for (int w = 1; w < tpr / 64; ++w) lo = __builtin_fmaxf(lo, rests[w]);
+        lo = fold_waves<Max>(rests, tpr / 64, -__builtin_inff());
       }
     }
   }
@@ -350,19 +375,15 @@ __global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* r
     mine = max_bits(mine, mag_bits(f * gamma_at(gamma, k)));
     if (H) H[base + k] = h;
   }
-  ss = wave_sum(ss);
-  uint32_t hi = wave_max(mine);
+  ss = fold<Add>(ss);
+  uint32_t hi = fold<Max>(mine);
   if (lane == 0) {
     sums[wave] = ss;
     maxs[wave] = hi;
   }
   __syncthreads();
-  ss = sums[0];
-  hi = maxs[0];
-  for (int w = 1; w < 16; ++w) {
-    ss += sums[w];
-    hi = max_bits(hi, maxs[w]);
-  }
+  ss = fold_waves<Add>(sums, 16, 0.f);
+  hi = fold_waves<Max>(maxs, 16, 0u);
   float lo = 0.f;
   if constexpr (kWide<In, GT>) {
     float r = -__builtin_inff();
@@ -372,11 +393,10 @@ __global__ __launch_bounds__(1024) void rms_long_kernel(const In* X, const In* r
         if (mag_bits(p) == hi) r = __builtin_fmaxf(r, left_over(f, w, p));
       }
     }
-    r = wave_max(r);
+    r = fold<Max>(r);
     if (lane == 0) rests[wave] = r;
     __syncthreads();
-    lo = rests[0];
-    for (int w = 1; w < 16; ++w) lo = __builtin_fmaxf(lo, rests[w]);
+    lo = fold_waves<Max>(rests, 16, -__builtin_inff());
   }
   double amax = (double)__uint_as_float(hi) + (double)lo;
   if constexpr (kMayVanish<In, GT>) {
@@ -512,13 +532,17 @@ __global__ __launch_bounds__(N == 4 ? 1024 : 512, N == 4 ? 4 : 2) void rms_bwd_k
       }
     }
     if (dX) {
-      c = wave_sum(c);
+      c = fold<Add>(c);
       if constexpr (!WAVE) {
         // two slots in turn: a row's sums are read before the slot is written again
         if (lane == 0) sums[slot][wave] = c;
         __syncthreads();
-        c = sums[slot][0];
-        for (int w = 1; w < tpr / 64; ++w) c += sums[slot][w];
+        if constexpr (AHEAD) {
+          c = fold_waves<Add>(sums[slot], tpr / 64, 0.f);
+        } else {                                     // (fewer registers spilled: 512 x 20480 36 us against 43)
+          c = sums[slot][0];
+          for (int w = 1; w < tpr / 64; ++w) c += sums[slot][w];
+        }
         slot ^= 1;
       }
       c *= inv_k;
@@ -599,11 +623,10 @@ __global__ __launch_bounds__(1024) void rms_dx_long_kernel(const In* dY, const I
   float c = 0.f;
   for (int64_t k = threadIdx.x; k < K; k += 1024)
     c += elem_f32(dY[base + k]) * gamma_at(gamma, k) * (elem_f32(H[base + k]) * rs);
-  c = wave_sum(c);
+  c = fold<Add>(c);
   if (lane == 0) sums[wave] = c;
   __syncthreads();
-  c = sums[0];
-  for (int w = 1; w < 16; ++w) c += sums[w];
+  c = fold_waves<Add>(sums, 16, 0.f);
   c /= (float)K;
   for (int64_t k = threadIdx.x; k < K; k += 1024) {
     const float a = elem_f32(dY[base + k]) * gamma_at(gamma, k);

@@ -36,6 +36,10 @@ template <> __device__ __forceinline__ float elem_of<float>(float f) { return f;
 // and what the rounding left, h g - p (zero where g has 16 bits too: the product
 // then fits).
 
+// The larger of a and |p|; a NaN stays (one instruction takes two values of p).
+__device__ __forceinline__ float max_mag(float a, float p) {
+  return __builtin_elementwise_maximum(a, __builtin_fabsf(p));
+}
 // Bits of |p|: they order like magnitudes, with infinity and NaN on top, so a row
 // without a finite maximum shows in the largest.
 __device__ __forceinline__ uint32_t mag_bits(float p) { return __float_as_uint(p) & 0x7FFFFFFFu; }
@@ -45,6 +49,7 @@ __device__ __forceinline__ float left_over(float f, float w, float p) {
   return __builtin_copysignf(1.0f, p) * __builtin_fmaf(f, w, -p);
 }
 
+constexpr float kUnsure = 0.49995f;                    // from an integer: the rounding may go either way
 constexpr float kCodeMagic = 12582912.0f;             // 1.5 * 2^23: adding it rounds to an integer, ties to even
 
 // Below it a row's products leave fp32's normal range, and p may have lost bits that
@@ -56,11 +61,11 @@ __device__ __forceinline__ bool tiny_bits(uint32_t hi) { return hi < kTinyBits; 
 // hi and the largest left-over of the values with that p, or, in a row of tiny_bits,
 // the largest of the products themselves.
 //
-// The quotient from one fp32 reciprocal, q = p * (127 / hi), is within 2^-14 of
+// The quotient from one fp32 reciprocal, q = p * (127 / hi), is within 4e-5 of
 // the true one (|q| <= 127; p, hi, the division and the product each round by
-// 2^-24 at most), so its rounding is decided unless it lies within 1e-4 of a
-// border k + 1/2.  There the sign of 254 u - (2k + 1) amax decides, which is
-// exact in double (products of at most 43 bits).  About one value in 5000 takes
+// 2^-24 of it at most: 3.1e-5), so its rounding is decided unless it lies within
+// 5e-5 of a border k + 1/2.  There the sign of 254 u - (2k + 1) amax decides, which is
+// exact in double (products of at most 43 bits).  About one value in 10000 takes
 // that branch.  Rows of tiny_bits go by double throughout.
 struct RowCodes {
   double amax;
@@ -102,11 +107,11 @@ struct RowCodes {
       t[i] = q + kCodeMagic;
       far = __builtin_fmaxf(far, __builtin_fabsf(q - (t[i] - kCodeMagic)));
     }
-    if (far > 0.4999f) {
+    if (far > kUnsure) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float q = p[i] * inv, k = t[i] - kCodeMagic;
-        if (__builtin_fabsf(q - k) > 0.4999f) t[i] = at_border(u(i), q, k) + kCodeMagic;
+        if (__builtin_fabsf(q - k) > kUnsure) t[i] = at_border(u(i), q, k) + kCodeMagic;
       }
     }
     // the low bytes of t are the codes in two's complement
