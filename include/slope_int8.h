@@ -58,7 +58,7 @@ extern "C" {
  * their element type's alignment.  Any K >= 1; K = 0 or T = 0 does nothing.
  * Errors: SLOPE_ERR_UNSUPPORTED for codes of an F32 X or another gamma_dt;
  * SLOPE_ERR_INVALID_ARG for a missing output, one of q and q_scale alone, an
- * eps outside its range, or H and Y the same. */
+ * eps outside its range, H and Y the same, or q_scale and rstd the same. */
 slope_status slope_rmsnorm(slope_dtype dt, const void* X, const void* residual_or_null, slope_dtype gamma_dt,
                            const void* gamma_or_null, int64_t T, int64_t K, double eps, void* H_or_null,
                            void* Y_or_null, int8_t* q_or_null, float* q_scale_or_null, float* rstd_or_null,
@@ -77,14 +77,15 @@ slope_status slope_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t K, int64_t* by
  *   rstd    [T] float32 as the forward wrote it
  *   gamma_or_null [K] gamma_dt (dt or F32), NULL = all ones
  *   dH_or_null    [T, K] dt: the gradient that reaches h by other ways
- *   dX_or_null    [T, K] dt output; may be dY or dH themselves
+ *   dX_or_null    [T, K] dt output; may be dY or dH themselves, not H
  *   dgamma_or_null [K] gamma_dt output; accumulate != 0 adds to its contents
  *   workspace     of slope_rmsnorm_bwd_workspace_bytes(T, K) bytes, scratch;
  *                 only used (and only checked) with dgamma
  * At least one output.  float32 arithmetic, sums over tokens in a fixed order,
  * one rounding of each output.  T = 0 gives dgamma = 0 (or leaves it, with
  * accumulate).  Errors: SLOPE_ERR_UNSUPPORTED for another gamma_dt,
- * SLOPE_ERR_WORKSPACE for a short or missing workspace. */
+ * SLOPE_ERR_WORKSPACE for a short or missing workspace, SLOPE_ERR_INVALID_ARG
+ * for a missing output or dX and H the same. */
 slope_status slope_rmsnorm_bwd(slope_dtype dt, const void* dY, const void* H, const float* rstd, slope_dtype gamma_dt,
                                const void* gamma_or_null, const void* dH_or_null, int64_t T, int64_t K,
                                void* dX_or_null, void* dgamma_or_null, int accumulate, void* workspace_or_null,

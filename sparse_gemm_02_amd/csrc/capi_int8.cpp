@@ -23,6 +23,9 @@ slope_status ptr(const void* p, bool required, unsigned align = 16) {
   return (reinterpret_cast<uintptr_t>(p) & (align - 1)) ? SLOPE_ERR_ALIGN : SLOPE_OK;
 }
 
+// Two arguments that share memory (empty ones may have one address).
+bool same(const void* a, const void* b, int64_t elements) { return a && a == b && elements > 0; }
+
 #define SLOPE_TRY(x)                       \
   do {                                     \
     slope_status _st = (x);                \
@@ -66,7 +69,7 @@ slope_status slope_rmsnorm(slope_dtype dt, const void* X, const void* residual_o
   SLOPE_TRY(ptr(rstd_or_null, false, 4));
   if (!H_or_null && !Y_or_null && !q_or_null && !rstd_or_null) return SLOPE_ERR_INVALID_ARG;
   if ((q_or_null == nullptr) != (q_scale_or_null == nullptr)) return SLOPE_ERR_INVALID_ARG;
-  if (H_or_null && H_or_null == Y_or_null) return SLOPE_ERR_INVALID_ARG;
+  if (same(H_or_null, Y_or_null, T * K) || same(q_scale_or_null, rstd_or_null, T)) return SLOPE_ERR_INVALID_ARG;
   if (!(eps >= (double)FLT_MIN && eps <= (double)FLT_MAX)) return SLOPE_ERR_INVALID_ARG;
   if (q_or_null && dt == SLOPE_F32) return SLOPE_ERR_UNSUPPORTED;   // codes come from 16-bit values
   if (!in_range(T) || !in_range(K)) return SLOPE_ERR_UNSUPPORTED;
@@ -97,6 +100,7 @@ slope_status slope_rmsnorm_bwd(slope_dtype dt, const void* dY, const void* H, co
   SLOPE_TRY(ptr(dgamma_or_null, false));
   SLOPE_TRY(ptr(workspace_or_null, false));
   if (!dX_or_null && !dgamma_or_null) return SLOPE_ERR_INVALID_ARG;
+  if (same(dX_or_null, H, T * K)) return SLOPE_ERR_INVALID_ARG;   // (dY or dH in place, H not)
   if (!in_range(T) || !in_range(K)) return SLOPE_ERR_UNSUPPORTED;
   const int64_t need = dgamma_or_null ? slope::rmsnorm_bwd_workspace_bytes(T, K) : 0;
   if (need > 0 && (!workspace_or_null || workspace_bytes < need)) return SLOPE_ERR_WORKSPACE;

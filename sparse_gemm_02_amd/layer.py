@@ -302,7 +302,11 @@ class ResidualRMSNorm(torch.nn.Module):
     for bf16, fp16 or fp32 x; weight in x's format or fp32.  `norm(x)` returns y,
     `norm(x, residual)` returns (y, h); both are differentiable in x, residual and
     weight.  `norm.codes(...)` (inference) returns y as 8-bit integer codes with a
-    scale for each row, the input of Int8SparseLinear."""
+    scale for each row, the input of Int8SparseLinear.
+
+    A step captured into a HIP graph is run once before on a side stream, and no
+    output of an eager call that still holds its autograd graph may be alive then:
+    its gradient accumulators belong to the eager stream."""
 
     def __init__(self, features: int, eps: float = 1e-5, dtype=torch.float32, device="cuda"):
         super().__init__()

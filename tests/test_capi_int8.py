@@ -58,6 +58,7 @@ def test_rmsnorm_refusals(lib):
     assert n(Y=None) == -1                                          # no output at all
     assert n(q=FAKE) == -1 and n(qs=FAKE) == -1                     # codes without scales, scales without codes
     assert n(H=FAKE, Y=FAKE) == -1                                  # h and y in one buffer
+    assert n(q=FAKE, qs=FAKE, rstd=FAKE) == -1                      # scales and rstd in one buffer
     for eps in (0.0, -1e-5, float("nan"), float("inf"), 1e-40, 1e39):
         assert n(eps=eps) == -1, eps
     assert n(X=FAKE + 2) == -3 and n(res=FAKE + 8) == -3 and n(gamma=FAKE + 4) == -3 and n(H=FAKE + 8) == -3
@@ -67,7 +68,7 @@ def test_rmsnorm_refusals(lib):
     assert n(T=(1 << 22) + 1) == -6 and n(K=(1 << 22) + 1) == -6
 
 
-def _bwd(lib, dt=BF16, dY=FAKE, H=FAKE, rstd=FAKE, gdt=BF16, gamma=FAKE, dH=None, T=4, K=64, dX=FAKE, dg=FAKE,
+def _bwd(lib, dt=BF16, dY=FAKE, H=FAKE, rstd=FAKE, gdt=BF16, gamma=FAKE, dH=None, T=4, K=64, dX=2 * FAKE, dg=FAKE,
          ws=FAKE, wb=BIG):
     return lib.slope_rmsnorm_bwd(dt, dY, H, rstd, gdt, gamma, dH, T, K, dX, dg, 0, ws, wb, None)
 
@@ -82,6 +83,7 @@ def test_rmsnorm_bwd_refusals(lib):
     assert b(rstd=FAKE + 2) == -3
     need = S.slope_rmsnorm_bwd_workspace_bytes(4, 64)
     assert b(wb=need - 1) == -4 and b(ws=None, wb=0) == -4
+    assert b(dX=FAKE) == -1                                         # dX over H
 
 
 def test_quantize_and_pack_refusals(lib):

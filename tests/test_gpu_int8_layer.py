@@ -215,3 +215,52 @@ def test_refusals():
         q8(Int8Rows(rows.q, rows.scale[:2]), x)
     with pytest.raises(ValueError, match="codes"):
         q8(rows, rand(1, 3, 64))
+
+
+def test_batches_without_rows():
+    """Every call on [0, K]: outputs without rows, gradients of zeros."""
+    norm = ResidualRMSNorm(256, dtype=torch.bfloat16)
+    x = rand(1, 0, 3, 256).requires_grad_()
+    r = rand(2, 0, 3, 256).requires_grad_()
+    for args in ((x,), (x, r)):
+        out = norm(*args)
+        y, h = out if len(args) == 2 else (out, x)
+        (y.sum() + h.sum()).backward()
+    torch.cuda.synchronize()
+    assert y.shape == h.shape == (0, 3, 256) and x.grad.shape == r.grad.shape == x.shape
+    assert norm.weight.grad is not None and not norm.weight.grad.any()
+    rows, h, y = norm.codes(x, r, output=True)
+    assert rows.q.shape == x.shape and rows.scale.shape == (0, 3) and h.shape == y.shape == x.shape
+    lin = Int8SparseLinear(SparseLinear(rand(3, 128, 256, sigma=0.02)))
+    assert lin(rows).shape == (0, 3, 128) and lin(x.detach()).shape == (0, 3, 128)
+
+
+def test_captured_forward_and_backward():
+    """norm's y, h and all three gradients in a captured graph, replayed on changed
+    inputs: equal to the eager calls, bit for bit."""
+    norm = ResidualRMSNorm(1024, dtype=torch.bfloat16)
+    static = [rand(i, 96, 1024).requires_grad_(i < 2) for i in range(4)]      # x, residual, dy, dh
+
+    def step():
+        y, h = norm(static[0], static[1])
+        return y.detach(), h.detach(), *torch.autograd.grad((y, h), (static[0], static[1], norm.weight), static[2:])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(3):
+        with torch.no_grad():
+            for j, t in enumerate(static):
+                t.copy_(rand(10 * i + j, 96, 1024))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), i
+        torch.cuda.synchronize()
