@@ -103,7 +103,7 @@ __device__ __forceinline__ void store4(O* p, const float (&y)[4]) {
 
 // ---------------------------------------------------------------- the GEMM
 // Transposed output tiles Out^T = W_q . Xq^T of BM x BT, stages of 128 dense k in
-// a ring of three LDS slots filled by buffer-to-LDS loads of 16 bytes a lane.
+// a ring of LDS slots (three or four) filled by buffer-to-LDS loads of 16 bytes a lane.
 // LDS granules: A row r c ^ ((r>>2)&3), B row r c ^ ((r^(r>>3))&7), so that
 // fragment reads are free of bank conflicts (the metadata's reads use half of the
 // banks; laid out over all of them they changed no time).  MFMA step s of a stage takes
@@ -114,11 +114,11 @@ __device__ __forceinline__ void store4(O* p, const float (&y)[4]) {
 // with offsets, ring slots and bounds computed anew each stage the same schedule
 // took 436 us for 8192 x 9216 x 9216, against 389 (and 374 since tiles are stored
 // by whole lines).
-template <int BM_, int BT_, int WGM_, int WGT_, int BLOCKS_>
+template <int BM_, int BT_, int WGM_, int WGT_, int BLOCKS_, int NST_ = 3>
 struct GeoI8 {
   static constexpr int BM = BM_, BT = BT_, WGM = WGM_, WGT = WGT_, WAVES = WGM * WGT, THREADS = 64 * WAVES;
   static constexpr int WM = BM / WGM, WT = BT / WGT, FM = WM / 32, FT = WT / 32;
-  static constexpr int KS = kChunkCols, NST = 3;
+  static constexpr int KS = kChunkCols, NST = NST_;   // slots of the ring
   static constexpr int BLOCKS = BLOCKS_;             // blocks a compute unit holds
   static constexpr int A_BYTES = BM * 64, B_BYTES = BT * 128, META_BYTES = BM * 16;
   static constexpr int SLOT = A_BYTES + B_BYTES + META_BYTES, LDS_BYTES = NST * SLOT;
@@ -200,10 +200,10 @@ struct TileI8 {
 #pragma unroll
     for (int j = 0; j < G::B_DMA; ++j) b_src[j] += G::KS;
   }
-  // until this wave's share of all but its newest stage is in LDS
+  // until this wave's share of all but its newest NST - 2 stages is in LDS
   __device__ __forceinline__ void wait_older() const {
-    if (wave < G::META_WAVES) wait_vmcnt<G::A_DMA + G::B_DMA + 1>();
-    else wait_vmcnt<G::A_DMA + G::B_DMA>();
+    if (wave < G::META_WAVES) wait_vmcnt<(G::NST - 2) * (G::A_DMA + G::B_DMA + 1)>();
+    else wait_vmcnt<(G::NST - 2) * (G::A_DMA + G::B_DMA)>();
   }
   __device__ __forceinline__ void read_meta(u32x2 (&x)[G::FM], int slot) const {
 #pragma unroll
@@ -300,7 +300,7 @@ __device__ __forceinline__ void clear_acc(i32x16 (&acc)[G::FM][G::FT]) {
     for (int ft = 0; ft < G::FT; ++ft) acc[fm][ft] = i32x16{};
 }
 
-// Small tiles, several blocks a compute unit: each step's fragments are read
+// Small tiles, one or several blocks a compute unit: each step's fragments are read
 // ahead of the step before, one barrier a stage, the slot refilled among the
 // second step's MFMAs; while one block waits, another multiplies.
 template <class G, typename O>
@@ -313,15 +313,15 @@ __global__ __launch_bounds__(G::THREADS, G::BLOCKS* G::WAVES / 4) void spmm_i8_k
   TileI8<G> t(lds, Xq, packed, M, T, Kred, tm, tt);
   i32x16 acc[G::FM][G::FT];
   clear_acc<G>(acc);
-  t.issue(0);
-  t.issue(G::SLOT);
+#pragma unroll
+  for (int i = 0; i < G::NST - 1; ++i) t.issue(i * G::SLOT);
   t.wait_older();
   barrier();
   compiler_fence();
   FragsI8<G> f0, f1;
   u32x2 x0[G::FM], x1[G::FM];
-  int cur = 0, next = G::SLOT, refill = 2 * G::SLOT;
-  t.issue(refill);
+  int cur = 0, next = G::SLOT;
+  t.issue((G::NST - 1) * G::SLOT);
   t.read_meta(x0, cur);
   t.read(f0, cur, 0);
   for (int s = 0; s < t.stages; ++s) {
@@ -426,6 +426,7 @@ __device__ __forceinline__ void ping_pong_tile(char* lds, const int8_t* Xq, cons
 typedef GeoI8<256, 256, 2, 4, 1> FullI8;
 typedef GeoI8<256, 128, 4, 2, 1> HalfI8;
 typedef GeoI8<128, 128, 2, 2, 2> SmallI8;
+typedef GeoI8<128, 64, 4, 1, 1, 4> NarrowI8;
 
 // The first rows_full row tiles in 256 x 256 tiles, the others in 256 x 128
 // (full_width_rows: a grid that would end in a partly filled round of blocks
@@ -695,19 +696,39 @@ int64_t compute_units() {
   return n;
 }
 
-// Any number of tokens.  Three kernels, chosen by their estimated time in units
+template <class G, typename O>
+hipError_t tiles_go(const SpmmArgs<O>& a) {
+  static LdsLimit limit;
+  auto kern = spmm_i8_kernel<G, O>;
+  const hipError_t e = limit.set((const void*)kern, G::LDS_BYTES);
+  if (e != hipSuccess) return e;
+  kern<<<(unsigned)(cdiv(a.M, G::BM) * cdiv(a.T, G::BT)), G::THREADS, G::LDS_BYTES, a.s>>>(a.Xq, a.packed, a.M, a.T, a.K,
+                                                                                        a.xs, a.ws, a.Y);
+  return hipGetLastError();
+}
+
+// Any number of tokens.  Four kernels, chosen by their estimated time in units
 // of a stage (us for 128 k), fitted to sweeps of 65 .. 8192 tokens over 9216 ->
-// 9216 / 27648, 20480 -> 5120, 5120 -> 5120 / 15360 and 768 -> 2304:
+// 9216 / 27648, 20480 -> 5120, 5120 -> 5120 / 15360, 4096 -> 1024 and 768 -> 2304:
 //   large   0.010 a unit of full_width_rows' cost (100 a round of full tiles, 65
 //           of half tiles)
 //   small   128 x 128 tiles, two a compute unit: 0.42 up to one a unit, then
 //           0.35 + 0.0014 a tile
-//   direct  the few-token kernel over groups of 64 tokens: 0.13 + 0.0006 a block
+//   narrow  128 x 64 tiles, at most one a compute unit: 0.25.  A compute unit takes
+//           in some 80 GB/s by LDS-DMA however deep the ring is (four slots here;
+//           three 43 us, six 40, eight 41 for 20480 -> 5120 at 256 tokens), so
+//           where one round of smaller tiles is enough, less to load is faster.
+//   direct  the few-token kernel over groups of 64 tokens, 64 rows a block: 0.13 +
+//           0.0006 a block; up to 128 such blocks 32 rows (4096 -> 1024 at 512
+//           tokens 7.2 us against 8.9; 5120 -> 5120 at 65, 160 blocks, 12.5
+//           against 11.5)
 // Measured, us (large / small / direct), before the tiles were stored by whole
 // lines, which took 3 to 9% off the first two alike: 9216 -> 9216 at 128 tokens 40
 // / 29.5 / 24, 256: 41 / 31 / 37, 512: 42 / 49 / 62, 1000: 65 / 79 / 111, 8192: 380
 // / 491 / 895; 20480 -> 5120 at 256: 79 / 58 / 51, 512: 80 / 59 / 78, 1000: 85 /
-// 103 / 130.
+// 103 / 130.  Narrow against the best of these: 9216 -> 9216 at 128 tokens 19.9 /
+// 24.1, 20480 -> 5120 at 128: 38.6 / 32.1, at 256: 39.1 / 50.7, 5120 -> 5120 at
+// 256: 13.1 / 15.9.
 template <typename O>
 hipError_t spmm_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, const void* packed, const float* ws,
                        int64_t M, void* Y, hipStream_t s) {
@@ -717,24 +738,21 @@ hipError_t spmm_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, 
   const double large = 0.010 * (100 * cdiv(rows_full * cols, cus) + 65 * cdiv((rows - rows_full) * halves, cus));
   const int64_t tiles = cdiv(M, 128) * halves;
   const double small = tiles <= cus ? 0.42 : 0.35 + 0.0014 * (256.0 / cus) * tiles;
-  const double direct = 0.13 + 0.0006 * (256.0 / cus) * (cdiv(M, 64) * cdiv(T, 64));
+  const double narrow = cdiv(M, 128) * cdiv(T, 64) <= cus ? 0.25 : small;
+  const int64_t blocks = cdiv(M, 64) * cdiv(T, 64);
+  const double direct = 0.13 + 0.0006 * (256.0 / cus) * blocks;
   // (a grid's second dimension ends at 65535)
-  if (direct <= small && direct <= large && cdiv(T, 64) <= 65535) return decode_go<8, 2, 1, 1, 4, 2, O>(a);
-  if (small <= large) {
-    static LdsLimit limit;
-    auto kern = spmm_i8_kernel<SmallI8, O>;
-    const hipError_t e = limit.set((const void*)kern, SmallI8::LDS_BYTES);
-    if (e != hipSuccess) return e;
-    kern<<<(unsigned)tiles, SmallI8::THREADS, SmallI8::LDS_BYTES, s>>>(a.Xq, a.packed, a.M, a.T, a.K, xs, ws, a.Y);
-    return hipGetLastError();
-  }
+  if (direct <= narrow && direct <= small && direct <= large && cdiv(T, 64) <= 65535)
+    return blocks <= 128 ? decode_go<8, 1, 1, 1, 8, 4, O>(a) : decode_go<8, 2, 1, 1, 4, 2, O>(a);
+  if (narrow < small && narrow <= large) return tiles_go<NarrowI8, O>(a);
+  if (small <= large) return tiles_go<SmallI8, O>(a);
   static LdsLimit limit;
   auto kern = spmm_i8_large_kernel<O>;
   const hipError_t e = limit.set((const void*)kern, FullI8::LDS_BYTES);
   if (e != hipSuccess) return e;
-  const int64_t blocks = rows_full * cols + (rows - rows_full) * halves;
-  kern<<<(unsigned)blocks, FullI8::THREADS, FullI8::LDS_BYTES, s>>>(a.Xq, a.packed, a.M, a.T, a.K, (int)rows_full, xs,
-                                                                    ws, a.Y);
+  const int64_t all = rows_full * cols + (rows - rows_full) * halves;
+  kern<<<(unsigned)all, FullI8::THREADS, FullI8::LDS_BYTES, s>>>(a.Xq, a.packed, a.M, a.T, a.K, (int)rows_full, xs, ws,
+                                                                 a.Y);
   return hipGetLastError();
 }
 

@@ -128,7 +128,7 @@ def test_few_token_product(T, K, N, out):
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("T,K,N", [(65, 768, 768), (256, 256, 256), (257, 272, 260), (511, 1040, 1028), (1000, 768, 2304),
-                                   (300, 16, 8), (70, 128, 4), (513, 400, 1540)])
+                                   (300, 16, 8), (70, 128, 4), (513, 400, 1540), (300, 400, 2308), (130, 272, 9220)])
 def test_product(T, K, N, out):
     say(f"[i8 product] T={T} K={K} N={N} {out}")
     c = Case(T, K, N, seed=T * 3 + K, dt="f16")
@@ -136,9 +136,11 @@ def test_product(T, K, N, out):
 
 
 # grids of every kind: full tiles with a last rows of half tiles, half tiles
-# alone, full tiles alone, small tiles; ragged in all three sizes
+# alone, full tiles alone, small and narrow tiles (one stage to more than a ring's);
+# ragged in all three sizes
 @pytest.mark.parametrize("T,K,N", [(4100, 144, 4612), (500, 272, 9216), (1000, 400, 9220), (515, 656, 4100),
-                                   (2050, 128, 9220), (1000, 16, 2304)])
+                                   (2050, 128, 9220), (1000, 16, 2304), (200, 16, 5124), (65, 400, 16384),
+                                   (253, 656, 7004), (256, 2320, 5120)])
 def test_product_on_many_tiles(T, K, N):
     say(f"[i8 product] T={T} K={K} N={N}")
     c = Case(T, K, N, seed=T + N)
@@ -307,7 +309,7 @@ def test_graph_replays_equal_the_eager_calls():
 def test_first_call_of_a_kernel_inside_a_capture():
     """fp16 outputs on every kind of grid, captured before any eager call of them:
     what a launch sets up once must not be a stream operation."""
-    shapes = [(40, 272, 260), (500, 272, 9216), (515, 656, 4100), (130, 272, 520)]
+    shapes = [(40, 272, 260), (500, 272, 9216), (515, 656, 4100), (130, 272, 520), (300, 272, 2308), (130, 272, 9220)]
     cases = [Case(*s, seed=5) for s in shapes]
     args = [(c.xq.cuda(), c.xs.cuda(), c.packed, c.ws, c.N, torch.zeros((c.T, c.N), dtype=torch.float16, device="cuda"))
             for c in cases]
