@@ -427,6 +427,7 @@ typedef GeoI8<256, 256, 2, 4, 1> FullI8;
 typedef GeoI8<256, 128, 4, 2, 1> HalfI8;
 typedef GeoI8<128, 128, 2, 2, 2> SmallI8;
 typedef GeoI8<128, 64, 4, 1, 1, 4> NarrowI8;
+typedef GeoI8<64, 64, 2, 2, 1, 4> LeastI8;
 
 // The first rows_full row tiles in 256 x 256 tiles, the others in 256 x 128
 // (full_width_rows: a grid that would end in a partly filled round of blocks
@@ -475,7 +476,8 @@ struct SpmmArgs {
 // Measured (bf16 out; floor: the weight at a copy's 5.13 TB/s): 9216 -> 27648 at
 // 1 / 16 / 64 tokens 31.2 / 34.1 / 44.9 us (floor 31.0), 9216 -> 9216 11.1 /
 // 11.8 / 16.4 (10.3), 5120 -> 15360 10.4 / 10.7 / 12.6 (9.6), 20480 -> 5120 12.6
-// / 14.4 / 23.2 (12.8), 36864 -> 9216 42.3 / 50.8 / 74.4 (41.4).  At one token
+// / 14.4 / 23.2 (12.8), 36864 -> 9216 42.3 / 50.8 / 74.4 (41.4); decode_launch
+// below gives some of them to the GEMM's tiles.  At one token
 // HBM bounds it; at 64 the L1s, through which every block draws all of X (two and
 // three sets in flight, 12 and 16 waves: the same or slower).
 template <int FM>
@@ -667,24 +669,6 @@ hipError_t decode_go(const SpmmArgs<O>& a) {
   return hipGetLastError();
 }
 
-// 64 rows a block where that leaves 128 blocks or more (9216 outputs, 9216 wide,
-// 32 tokens: 11.9 us against 16.4 with 32 rows): every block draws all of X, so
-// wider ones draw it less often.  Below, 64 rows would leave too many compute
-// units idle (5120 outputs, 20480 wide, 32 tokens: 20.4 us against 16.6).
-// Waves, stages and sets as measured best over the five shapes above: the
-// registers are kept to 128 (two blocks a compute unit) up to 32 tokens; at 64
-// the 64-row block needs more, and four waves beat eight (44.9 against 46.8 us).
-template <typename O>
-hipError_t decode_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, const void* packed, const float* ws,
-                         int64_t M, void* Y, hipStream_t s) {
-  const SpmmArgs<O> a{Xq, (const char*)packed, (int)M, (int)T, (int)K, xs, ws, (O*)Y, s};
-  const bool wide = M > 127 * 64;
-  if (T <= 8) return wide ? decode_go<1, 2, 1, 2, 8, 4, O>(a) : decode_go<1, 1, 2, 2, 8, 4, O>(a);
-  if (T <= 16) return wide ? decode_go<2, 2, 1, 2, 8, 4, O>(a) : decode_go<2, 1, 1, 2, 16, 4, O>(a);
-  if (T <= 32) return wide ? decode_go<4, 2, 1, 1, 8, 4, O>(a) : decode_go<4, 1, 1, 2, 8, 4, O>(a);
-  return wide ? decode_go<8, 2, 1, 1, 4, 2, O>(a) : decode_go<8, 1, 1, 1, 8, 4, O>(a);
-}
-
 // device_compute_units, asked once for each device (1 us of a 5 us call).
 int64_t compute_units() {
   constexpr int kDevices = 64;
@@ -707,17 +691,53 @@ hipError_t tiles_go(const SpmmArgs<O>& a) {
   return hipGetLastError();
 }
 
-// Any number of tokens.  Four kernels, chosen by their estimated time in units
+// Tiles of the GEMM's kind in one round: where BM rows a tile leave more than half
+// of the compute units one tile each, and none two, its deeper queue of weight
+// streams faster than the kernel above (us, tiles against it):
+//   9216 -> 27648 (216 tiles of 128): 1 token 29.9 / 30.8, 32: 30.3 / 36.7, 64: 33.3 / 44.8
+//   9216 -> 36864 (144 of 256):       1 token 39.4 / 42.4, 32: 43.2 / 50.6, 64: 48.3 / 64.0
+//   5120 -> 20480 (160 of 128):       1 token 11.4 / 14.3, 32: 12.3 / 16.6, 64: 13.3 / 19.1
+//   5120 -> 15360 (240 of 64):                             32: 11.1 / 11.0, 64: 11.2 / 12.9
+//   9216 -> 9216 (144 of 64):                              32: 16.7 / 11.8, 64: 16.8 / 17.8
+// (so 64 rows only from 33 tokens on).  With fewer tiles a compute unit's share
+// takes longer (20480 -> 5120, 80 tiles of 64, 64 tokens: 33.0 / 22.8).
+//
+// Otherwise 64 rows a block where that leaves 128 blocks or more (9216 outputs, 9216 wide,
+// 32 tokens: 11.9 us against 16.4 with 32 rows): every block draws all of X, so
+// wider ones draw it less often.  Below, 64 rows would leave too many compute
+// units idle (5120 outputs, 20480 wide, 32 tokens: 20.4 us against 16.6).
+// Waves, stages and sets as measured best over the five shapes above: the
+// registers are kept to 128 (two blocks a compute unit) up to 32 tokens; at 64
+// the 64-row block needs more, and four waves beat eight (44.9 against 46.8 us).
+template <typename O>
+hipError_t decode_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, const void* packed, const float* ws,
+                         int64_t M, void* Y, hipStream_t s) {
+  const SpmmArgs<O> a{Xq, (const char*)packed, (int)M, (int)T, (int)K, xs, ws, (O*)Y, s};
+  const int64_t cus = compute_units();
+  auto one_round = [&](int bm) { return 2 * cdiv(M, bm) > cus && cdiv(M, bm) <= cus; };
+  if (T > 32 && one_round(64)) return tiles_go<LeastI8, O>(a);
+  if (one_round(128)) return T <= 32 ? tiles_go<GeoI8<128, 32, 4, 1, 1, 4>, O>(a) : tiles_go<NarrowI8, O>(a);
+  if (one_round(256))
+    return T <= 32 ? tiles_go<GeoI8<256, 32, 4, 1, 1, 4>, O>(a) : tiles_go<GeoI8<256, 64, 4, 1, 1, 4>, O>(a);
+  const bool wide = M > 127 * 64;
+  if (T <= 8) return wide ? decode_go<1, 2, 1, 2, 8, 4, O>(a) : decode_go<1, 1, 2, 2, 8, 4, O>(a);
+  if (T <= 16) return wide ? decode_go<2, 2, 1, 2, 8, 4, O>(a) : decode_go<2, 1, 1, 2, 16, 4, O>(a);
+  if (T <= 32) return wide ? decode_go<4, 2, 1, 1, 8, 4, O>(a) : decode_go<4, 1, 1, 2, 8, 4, O>(a);
+  return wide ? decode_go<8, 2, 1, 1, 4, 2, O>(a) : decode_go<8, 1, 1, 1, 8, 4, O>(a);
+}
+
+// Any number of tokens.  Five kernels, chosen by their estimated time in units
 // of a stage (us for 128 k), fitted to sweeps of 65 .. 8192 tokens over 9216 ->
 // 9216 / 27648, 20480 -> 5120, 5120 -> 5120 / 15360, 4096 -> 1024 and 768 -> 2304:
 //   large   0.010 a unit of full_width_rows' cost (100 a round of full tiles, 65
 //           of half tiles)
 //   small   128 x 128 tiles, two a compute unit: 0.42 up to one a unit, then
 //           0.35 + 0.0014 a tile
-//   narrow  128 x 64 tiles, at most one a compute unit: 0.25.  A compute unit takes
-//           in some 80 GB/s by LDS-DMA however deep the ring is (four slots here;
-//           three 43 us, six 40, eight 41 for 20480 -> 5120 at 256 tokens), so
-//           where one round of smaller tiles is enough, less to load is faster.
+//   narrow  128 x 64 tiles, at most one a compute unit: 0.25, or 64 x 64: 0.215.
+//           A compute unit takes in some 70 GB/s by LDS-DMA however deep the ring
+//           (four slots here; three 43 us, six 40, eight 41 for 20480 -> 5120 at
+//           256 tokens) and however many waves (eight: 40), so where one round of
+//           smaller tiles is enough, less to load is faster.
 //   direct  the few-token kernel over groups of 64 tokens, 64 rows a block: 0.13 +
 //           0.0006 a block; up to 128 such blocks 32 rows (4096 -> 1024 at 512
 //           tokens 7.2 us against 8.9; 5120 -> 5120 at 65, 160 blocks, 12.5
@@ -727,24 +747,26 @@ hipError_t tiles_go(const SpmmArgs<O>& a) {
 // / 29.5 / 24, 256: 41 / 31 / 37, 512: 42 / 49 / 62, 1000: 65 / 79 / 111, 8192: 380
 // / 491 / 895; 20480 -> 5120 at 256: 79 / 58 / 51, 512: 80 / 59 / 78, 1000: 85 /
 // 103 / 130.  Narrow against the best of these: 9216 -> 9216 at 128 tokens 19.9 /
-// 24.1, 20480 -> 5120 at 128: 38.6 / 32.1, at 256: 39.1 / 50.7, 5120 -> 5120 at
-// 256: 13.1 / 15.9.
+// 24.1, 20480 -> 5120 at 128: 38.6 (64 x 64 33.1) / 32.1, at 192: 39.0 (33.7) / 46,
+// at 256: 39.1 / 50.7, 5120 -> 5120 at 256: 13.1 / 15.9.
 template <typename O>
 hipError_t spmm_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, const void* packed, const float* ws,
                        int64_t M, void* Y, hipStream_t s) {
+  if (T <= 64) return decode_launch<O>(Xq, xs, T, K, packed, ws, M, Y, s);
   const SpmmArgs<O> a{Xq, (const char*)packed, (int)M, (int)T, (int)K, xs, ws, (O*)Y, s};
   const int64_t cus = compute_units(), rows = cdiv(M, 256), cols = cdiv(T, 256), halves = cdiv(T, 128);
   const int64_t rows_full = full_width_rows(rows, cols, halves, cus);
   const double large = 0.010 * (100 * cdiv(rows_full * cols, cus) + 65 * cdiv((rows - rows_full) * halves, cus));
   const int64_t tiles = cdiv(M, 128) * halves;
   const double small = tiles <= cus ? 0.42 : 0.35 + 0.0014 * (256.0 / cus) * tiles;
-  const double narrow = cdiv(M, 128) * cdiv(T, 64) <= cus ? 0.25 : small;
   const int64_t blocks = cdiv(M, 64) * cdiv(T, 64);
+  const double narrow = blocks <= cus ? 0.215 : cdiv(M, 128) * cdiv(T, 64) <= cus ? 0.25 : small;
   const double direct = 0.13 + 0.0006 * (256.0 / cus) * blocks;
   // (a grid's second dimension ends at 65535)
   if (direct <= narrow && direct <= small && direct <= large && cdiv(T, 64) <= 65535)
     return blocks <= 128 ? decode_go<8, 1, 1, 1, 8, 4, O>(a) : decode_go<8, 2, 1, 1, 4, 2, O>(a);
-  if (narrow < small && narrow <= large) return tiles_go<NarrowI8, O>(a);
+  if (narrow < small && narrow <= large)
+    return blocks <= cus ? tiles_go<LeastI8, O>(a) : tiles_go<NarrowI8, O>(a);
   if (small <= large) return tiles_go<SmallI8, O>(a);
   static LdsLimit limit;
   auto kern = spmm_i8_large_kernel<O>;

@@ -117,7 +117,8 @@ class Case:
 
 @pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("T,K,N", [(1, 16, 4), (3, 48, 20), (17, 272, 300), (32, 128, 32), (33, 1040, 96), (64, 2064, 516),
-                                   (5, 5120, 1024), (61, 656, 260)])
+                                   (5, 5120, 1024), (61, 656, 260), (1, 272, 16900), (32, 1040, 17000), (33, 656, 17004),
+                                   (64, 16, 20480), (9, 400, 33000), (40, 272, 33004), (50, 784, 8300), (20, 272, 8300)])
 def test_few_token_product(T, K, N, out):
     say(f"[i8 decode] T={T} K={K} N={N} {out}")
     c = Case(T, K, N, seed=T + K)
@@ -128,7 +129,8 @@ def test_few_token_product(T, K, N, out):
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("T,K,N", [(65, 768, 768), (256, 256, 256), (257, 272, 260), (511, 1040, 1028), (1000, 768, 2304),
-                                   (300, 16, 8), (70, 128, 4), (513, 400, 1540), (300, 400, 2308), (130, 272, 9220)])
+                                   (300, 16, 8), (70, 128, 4), (513, 400, 1540), (300, 400, 2308), (130, 272, 9220),
+                                   (300, 16, 2500), (190, 656, 5060)])
 def test_product(T, K, N, out):
     say(f"[i8 product] T={T} K={K} N={N} {out}")
     c = Case(T, K, N, seed=T * 3 + K, dt="f16")
@@ -309,7 +311,8 @@ def test_graph_replays_equal_the_eager_calls():
 def test_first_call_of_a_kernel_inside_a_capture():
     """fp16 outputs on every kind of grid, captured before any eager call of them:
     what a launch sets up once must not be a stream operation."""
-    shapes = [(40, 272, 260), (500, 272, 9216), (515, 656, 4100), (130, 272, 520), (300, 272, 2308), (130, 272, 9220)]
+    shapes = [(40, 272, 260), (500, 272, 9216), (515, 656, 4100), (130, 272, 520), (150, 272, 2900), (300, 272, 2308),
+              (130, 272, 9220), (5, 272, 16900), (5, 272, 33000), (50, 272, 33000)]
     cases = [Case(*s, seed=5) for s in shapes]
     args = [(c.xq.cuda(), c.xs.cuda(), c.packed, c.ws, c.N, torch.zeros((c.T, c.N), dtype=torch.float16, device="cuda"))
             for c in cases]
