@@ -10,8 +10,9 @@
 // to the row and cancels), and the outputs are made from the registers.
 // Measured: 8192 x 9216 bf16 with residual and codes 97.5 us (5.4 TB/s; a plain
 // copy reaches 5.1), with y in place of the codes 106; 16384 x 1024 23 us; 1021 x
-// 5120 fp16 7.1 us and 2047 x 771 fp32 8.1 us, of which one row alone takes 4.2;
-// without a residual (8192 x 9216 fp16, 68 us, 3.3 TB/s) the arithmetic bounds it.
+// 5120 fp16 with an fp32 gamma 7.6 us and 2047 x 771 fp32 7.9 us, of which one row
+// alone takes 4.2; without a residual (8192 x 9216 fp16, 64 us, 3.5 TB/s) the
+// arithmetic bounds it.
 //
 // Gradient:  a = dy g,  xh = h rstd,  c = mean(a xh)
 //   dx = rstd (a - xh c) + dh,   dg = sum over tokens of dy xh
@@ -210,11 +211,12 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
   }
   __builtin_amdgcn_sched_barrier(0);
   float ss = 0.f;
-  float top = 0.f;                                   // largest |h g| (as fp32) of this thread, and its bits
-  uint32_t mine = 0u;
+  float top[N];                                      // largest |h g| (as fp32) of each vector
+  uint32_t mine = 0u;                                // bits of the thread's largest
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     const Vec rv(j * tpr + tid, K);
+    top[j] = 0.f;
     if (res) {
 #pragma unroll
       for (int e = 0; e < E; ++e) h[j].v[e] = elem_of<In>(elem_f32(h[j].v[e]) + elem_f32(r[j].v[e]));
@@ -230,10 +232,10 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
       // (with the second form for eight vectors the compiler spills a hundred
       // registers: 2048 x 32768 214 us against 107)
       if (o.q && !KEEP) mine = max_bits(mine, mag_bits(f * g[j](e)));
-      else if (CODES && KEEP) top = max_mag(top, f * g[j](e));
+      else if (CODES && KEEP) top[j] = max_mag(top[j], f * g[j](e));
     }
+    if (KEEP) mine = max_bits(mine, mag_bits(top[j]));
   }
-  if (KEEP) mine = mag_bits(top);
   ss = fold<Add>(ss);
   uint32_t hi = o.q ? fold<Max>(mine) : 0u;
   if constexpr (!WAVE) {
@@ -251,21 +253,20 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
   float lo = 0.f;
   if constexpr (WIDE) {
     // of the values that share the row's largest p (one, as a rule), the largest
-    // left-over: looked for by the threads that have such a value.  Carried along
-    // with every maximum it cost a fifth of the kernel's arithmetic.
+    // left-over: looked for where a vector has such a value (16384 x 1792 fp16 23.0
+    // us; in all of a thread's vectors 28.1; carried along with every maximum more).
     if (o.q) {
       float r = -__builtin_inff();
 #pragma unroll
       for (int j = 0; j < N; ++j) forget<In, E>(h[j]);
-      if (mine == hi) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          if (!KEEP) g[j].load(gamma + Vec(j * tpr + tid, K).at);
+      for (int j = 0; j < N; ++j) {
+        if ((KEEP ? mag_bits(top[j]) : mine) != hi) continue;
+        if (!KEEP) g[j].load(gamma + Vec(j * tpr + tid, K).at);
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float f = elem_f32(h[j].v[e]), w = g[j](e), p = f * w;
-            if (mag_bits(p) == hi) r = __builtin_fmaxf(r, left_over(f, w, p));
-          }
+        for (int e = 0; e < E; ++e) {
+          const float f = elem_f32(h[j].v[e]), w = g[j](e), p = f * w;
+          if (mag_bits(p) == hi) r = __builtin_fmaxf(r, left_over(f, w, p));
         }
       }
       lo = fold<Max>(r);
