@@ -426,6 +426,7 @@ __device__ __forceinline__ void ping_pong_tile(char* lds, const int8_t* Xq, cons
 typedef GeoI8<256, 256, 2, 4, 1> FullI8;
 typedef GeoI8<256, 128, 4, 2, 1> HalfI8;
 typedef GeoI8<128, 128, 2, 2, 2> SmallI8;
+typedef GeoI8<128, 128, 4, 2, 1, 4> SingleI8;
 typedef GeoI8<128, 64, 4, 1, 1, 4> NarrowI8;
 typedef GeoI8<64, 64, 2, 2, 1, 4> LeastI8;
 
@@ -731,8 +732,9 @@ hipError_t decode_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K
 // 9216 / 27648, 20480 -> 5120, 5120 -> 5120 / 15360, 4096 -> 1024 and 768 -> 2304:
 //   large   0.010 a unit of full_width_rows' cost (100 a round of full tiles, 65
 //           of half tiles)
-//   small   128 x 128 tiles, two a compute unit: 0.42 up to one a unit, then
-//           0.35 + 0.0014 a tile
+//   small   128 x 128 tiles: 0.42 up to one a compute unit (eight waves, four
+//           slots: 5120 -> 20480 at 128 tokens 17.1 us, as below 18.6), then 0.35 +
+//           0.0014 a tile (two a unit, four waves and three slots each)
 //   narrow  128 x 64 tiles, at most one a compute unit: 0.25, or 64 x 64: 0.215.
 //           A compute unit takes in some 70 GB/s by LDS-DMA however deep the ring
 //           (four slots here; three 43 us, six 40, eight 41 for 20480 -> 5120 at
@@ -767,7 +769,7 @@ hipError_t spmm_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, 
     return blocks <= 128 ? decode_go<8, 1, 1, 1, 8, 4, O>(a) : decode_go<8, 2, 1, 1, 4, 2, O>(a);
   if (narrow < small && narrow <= large)
     return blocks <= cus ? tiles_go<LeastI8, O>(a) : tiles_go<NarrowI8, O>(a);
-  if (small <= large) return tiles_go<SmallI8, O>(a);
+  if (small <= large) return tiles <= cus ? tiles_go<SingleI8, O>(a) : tiles_go<SmallI8, O>(a);
   static LdsLimit limit;
   auto kern = spmm_i8_large_kernel<O>;
   const hipError_t e = limit.set((const void*)kern, FullI8::LDS_BYTES);

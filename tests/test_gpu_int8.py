@@ -142,7 +142,7 @@ def test_product(T, K, N, out):
 # ragged in all three sizes
 @pytest.mark.parametrize("T,K,N", [(4100, 144, 4612), (500, 272, 9216), (1000, 400, 9220), (515, 656, 4100),
                                    (2050, 128, 9220), (1000, 16, 2304), (200, 16, 5124), (65, 400, 16384),
-                                   (253, 656, 7004), (256, 2320, 5120)])
+                                   (253, 656, 7004), (256, 2320, 5120), (33000, 48, 100)])
 def test_product_on_many_tiles(T, K, N):
     say(f"[i8 product] T={T} K={K} N={N}")
     c = Case(T, K, N, seed=T + N)
@@ -312,7 +312,7 @@ def test_first_call_of_a_kernel_inside_a_capture():
     """fp16 outputs on every kind of grid, captured before any eager call of them:
     what a launch sets up once must not be a stream operation."""
     shapes = [(40, 272, 260), (500, 272, 9216), (515, 656, 4100), (130, 272, 520), (150, 272, 2900), (300, 272, 2308),
-              (130, 272, 9220), (5, 272, 16900), (5, 272, 33000), (50, 272, 33000)]
+              (130, 272, 9220), (5, 272, 16900), (5, 272, 33000), (50, 272, 33000), (33000, 48, 100)]
     cases = [Case(*s, seed=5) for s in shapes]
     args = [(c.xq.cuda(), c.xs.cuda(), c.packed, c.ws, c.N, torch.zeros((c.T, c.N), dtype=torch.float16, device="cuda"))
             for c in cases]
