@@ -455,7 +455,7 @@ hipError_t rms_launch(const void* X_, const void* res_, const void* gamma_, int6
   else if (v <= 128) rms_rows<In, GT, E, 2, true>(X, res, gamma, T, K, eps, o, s);
   else if (v <= 256) rms_rows<In, GT, E, 4, true>(X, res, gamma, T, K, eps, o, s);
   else if (v <= 1024) rms_rows<In, GT, E, 2, false>(X, res, gamma, T, K, eps, o, s);
-  else if (v <= 3072) rms_rows<In, GT, E, 3, false>(X, res, gamma, T, K, eps, o, s);
+  else if (v <= 3 * 1024) rms_rows<In, GT, E, 3, false>(X, res, gamma, T, K, eps, o, s);
   else if (v <= 8192) rms_rows<In, GT, E, 8, false>(X, res, gamma, T, K, eps, o, s);
   else rms_long_kernel<In, GT><<<(unsigned)T, 1024, 0, s>>>(X, res, gamma, K, eps, o);
   return hipGetLastError();
