@@ -122,6 +122,12 @@ __device__ __forceinline__ void store_vec(V* row, const RowVec<E, RAGGED>& r, co
   }
 }
 
+template <typename V, int E, bool RAGGED, bool TWICE>
+__device__ __forceinline__ void put_vec(V* row, const RowVec<E, RAGGED>& r, const Pack<V, E>& x) {
+  if constexpr (!TWICE) store_vec<V, E, RAGGED>(row, r, x);
+  else if (r.skip < E) store_pack<V, E>(row + r.at, x);
+}
+
 // Zeros in place of a vector's elements that are not its own, so that no sum or
 // maximum sees them.
 template <typename V, int E, bool RAGGED>
@@ -194,6 +200,15 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
   // gamma stays in registers between its two uses unless they would spill
   constexpr bool KEEP = N < 8;
   constexpr bool CODES = !std::is_same<In, float>::value;
+  // The foreign elements of a row's last vector are the row's own too, loaded
+  // twice.  TWICE: they are worked on and stored twice, with the same values, and
+  // only the sum leaves them out (16384 x 1001 fp32 43.5 us; with zeros in their
+  // place and the others stored one by one 59).  With more values a thread the registers
+  // it takes cost more (2000 x 12301 bf16 55 us against 52).
+  constexpr bool TWICE = RAGGED && N * E <= 16;
+  // An h in place of an input is stored when every load of the row is complete:
+  // another thread may have yet to load an element that this one stores.
+  const bool late = TWICE && o.H && (o.H == (const void*)X || o.H == (const void*)res);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = WAVE ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
   if (WAVE && row >= T) return;
@@ -221,10 +236,15 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
 #pragma unroll
       for (int e = 0; e < E; ++e) h[j].v[e] = elem_of<In>(elem_f32(h[j].v[e]) + elem_f32(r[j].v[e]));
     }
-    drop_foreign<In, E, RAGGED>(h[j], rv);
-    if (o.H) store_vec<In, E, RAGGED>((In*)o.H + row * K, rv, h[j]);
+    if constexpr (TWICE) {
+      if (o.H && !late && rv.skip < E) store_pack<In, E>((In*)o.H + row * K + rv.at, h[j]);
+    } else {
+      drop_foreign<In, E, RAGGED>(h[j], rv);
+      if (o.H) store_vec<In, E, RAGGED>((In*)o.H + row * K, rv, h[j]);
+    }
     if (!KEEP) g[j].load(gamma + rv.at);
-    if (CODES) g[j].drop(rv);                       // its foreign elements need not be finite
+    if (!TWICE && CODES) g[j].drop(rv);              // its foreign elements need not be finite
+    const float before = ss;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float f = elem_f32(h[j].v[e]);
@@ -235,6 +255,14 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
       else if (CODES && KEEP) top[j] = max_mag(top[j], f * g[j](e));
     }
     if (KEEP) mine = max_bits(mine, mag_bits(top[j]));
+    if (TWICE && rv.skip != 0) {
+      ss = before;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float f = rv.mine(e) ? elem_f32(h[j].v[e]) : 0.f;
+        ss = __builtin_fmaf(f, f, ss);
+      }
+    }
   }
   ss = fold<Add>(ss);
   uint32_t hi = o.q ? fold<Max>(mine) : 0u;
@@ -306,6 +334,13 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
     if (o.rstd) o.rstd[row] = rstd;
     if (o.q) o.qs[row] = codes.scale(rstd);
   }
+  if (late) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const Vec rv(j * tpr + tid, K);
+      if (rv.skip < E) store_pack<In, E>((In*)o.H + row * K + rv.at, h[j]);
+    }
+  }
   if (!o.Y && !o.q) return;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
@@ -316,7 +351,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
       Pack<In, E> y;
 #pragma unroll
       for (int e = 0; e < E; ++e) y.v[e] = elem_of<In>(elem_f32(h[j].v[e]) * rstd * g[j](e));
-      store_vec<In, E, RAGGED>((In*)o.Y + row * K, rv, y);
+      put_vec<In, E, RAGGED, TWICE>((In*)o.Y + row * K, rv, y);
     }
     if constexpr (!std::is_same<In, float>::value) {
       if (!o.q) continue;
@@ -349,7 +384,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rms_row_kernel(const In* X,
           for (int i = 0; i < E; ++i) c.v[i] = i == e ? k : c.v[i];
         }
       }
-      store_vec<int8_t, E, RAGGED>(o.q + row * K, rv, c);
+      put_vec<int8_t, E, RAGGED, TWICE>(o.q + row * K, rv, c);
     }
   }
 }

@@ -139,10 +139,12 @@ def test_norm_without_gamma_or_residual():
     check_norm(rand(2, 7, 640, dt="f16"), rand(3, 7, 640, dt="f16"), None, "f16")
 
 
-@pytest.mark.parametrize("K", [40, 771, 9216, 70000])
+@pytest.mark.parametrize("K,dt", [(40, "bf16"), (771, "bf16"), (9216, "bf16"), (70000, "bf16"), (1445, "bf16"),
+                                  (2049, "bf16"), (5121, "bf16"), (8191, "bf16"), (12301, "bf16"), (30001, "bf16"),
+                                  (1001, "f32"), (4099, "f32"), (6001, "f32"), (12285, "f32")])
 @pytest.mark.parametrize("place", ["H=X", "H=res", "Y=X", "Y=res", "H=res,Y=X", "H=X,Y=res"])
-def test_norm_in_place(K, place):
-    x, res, g = rand(1, 4, K), rand(2, 4, K), rand(3, K, mean=1.0, sigma=0.1)
+def test_norm_in_place(K, dt, place):
+    x, res, g = rand(1, 300, K, dt=dt), rand(2, 300, K, dt=dt), rand(3, K, mean=1.0, sigma=0.1, dt=dt)
     hr, yr = torch.empty_like(x), torch.empty_like(x)
     S.slope_rmsnorm(x, g, EPS, residual=res, H=hr, Y=yr)
     where = dict(p.split("=") for p in place.split(","))
