@@ -10,7 +10,7 @@
 // to the row and cancels), and the outputs are made from the registers.
 // Measured: 8192 x 9216 bf16 with residual and codes 97.5 us (5.4 TB/s; a plain
 // copy reaches 5.1), with y in place of the codes 106; 16384 x 1024 23 us; 1021 x
-// 5120 fp16 with an fp32 gamma 7.6 us and 2047 x 771 fp32 7.9 us, of which one row
+// 5120 fp16 with an fp32 gamma 7.6 us and 2047 x 771 fp32 6.5 us, of which one row
 // alone takes 4.2; without a residual (8192 x 9216 fp16, 64 us, 3.5 TB/s) the
 // arithmetic bounds it.
 //
