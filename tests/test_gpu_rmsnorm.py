@@ -343,6 +343,13 @@ def test_bwd_accumulates_and_works_in_place(K):
     check_bwd(100, K, "bf16", None, with_dh=True, in_place="dh", accumulate=True)
 
 
+@pytest.mark.parametrize("in_place", ["dy", "dh"])
+@pytest.mark.parametrize("K,dt", [(301, "bf16"), (771, "bf16"), (2049, "f16"), (3333, "bf16"), (5121, "bf16"), (20481, "bf16"),
+                                  (201, "f32"), (1001, "f32"), (6001, "f32"), (12285, "f32")])
+def test_bwd_in_place_at_odd_widths(K, dt, in_place):
+    check_bwd(700, K, dt, "f32", with_dh=True, in_place=in_place)
+
+
 def test_bwd_one_output_at_a_time():
     T, K = 33, 1536
     h, dy, g = rand(1, T, K), rand(2, T, K), rand(3, K, mean=1.0, sigma=0.1, dt="f32")
