@@ -46,6 +46,14 @@ def _bytes(n, device):
     return torch.empty(max(16, n), dtype=torch.uint8, device=device)
 
 
+def _aligned(t):
+    """t contiguous and at a 16-byte address, which the library asks of its caller: a
+    copy if need be (rows of a larger tensor start at any element, as those of a
+    concatenation's gradient do)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _SparseLinearFn(torch.autograd.Function):
     """Y = X . W_s^T (+ (X . L) . R); gradients dX (through W_dp), dW at the
     static mask, dL and dR."""
@@ -259,17 +267,17 @@ class _ResidualRMSNormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, gamma, eps):
         K = x.shape[-1]
-        rows = lambda t: t.reshape(-1, K).contiguous()
-        x2 = rows(x)
+        rows = lambda t: _aligned(t.reshape(-1, K))
+        x2, g = rows(x), _aligned(gamma)
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         rstd = torch.empty(x2.shape[0], dtype=torch.float32, device=x.device)
         if residual is None:
             h, h2 = None, x2
-            slope_rmsnorm(x2, gamma, eps, Y=y.view(x2.shape), rstd=rstd)
+            slope_rmsnorm(x2, g, eps, Y=y.view(x2.shape), rstd=rstd)
         else:
             h = torch.empty_like(y)
             h2 = h.view(x2.shape)
-            slope_rmsnorm(x2, gamma, eps, residual=rows(residual), H=h2, Y=y.view(x2.shape), rstd=rstd)
+            slope_rmsnorm(x2, g, eps, residual=rows(residual), H=h2, Y=y.view(x2.shape), rstd=rstd)
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(h2 if h is None else h, rstd, gamma)
         return y if h is None else (y, h)
@@ -281,7 +289,7 @@ class _ResidualRMSNormFn(torch.autograd.Function):
         need_x, need_r, need_g = ctx.needs_input_grad[:3]
         if dy is None:                               # only h was used
             return dh if need_x else None, dh if need_r else None, None, None
-        rows = lambda t: t.reshape(-1, gamma.shape[0]).contiguous()
+        rows = lambda t: _aligned(t.reshape(-1, gamma.shape[0]))
         dx = dgamma = ws = None
         if need_x or need_r:
             dx = torch.empty(dy.shape, dtype=h.dtype, device=h.device)
@@ -289,8 +297,9 @@ class _ResidualRMSNormFn(torch.autograd.Function):
             dgamma = torch.empty_like(gamma)
             ws = _bytes(slope_rmsnorm_bwd_workspace_bytes(rstd.shape[0], gamma.shape[0]), h.device)
         if dx is not None or need_g:
-            slope_rmsnorm_bwd(rows(dy), rows(h), rstd, gamma, dX=None if dx is None else dx.view(-1, gamma.shape[0]),
-                              dgamma=dgamma, workspace=ws, dH=None if dh is None or dx is None else rows(dh))
+            slope_rmsnorm_bwd(rows(dy), rows(h), rstd, _aligned(gamma),
+                              dX=None if dx is None else dx.view(-1, gamma.shape[0]), dgamma=dgamma, workspace=ws,
+                              dH=None if dh is None or dx is None else rows(dh))
         return dx if need_x else None, dx if need_r else None, dgamma, None
 
 
@@ -301,7 +310,9 @@ class ResidualRMSNorm(torch.nn.Module):
 
     for bf16, fp16 or fp32 x; weight in x's format or fp32.  `norm(x)` returns y,
     `norm(x, residual)` returns (y, h); both are differentiable in x, residual and
-    weight.  `norm.codes(...)` (inference) returns y as 8-bit integer codes with a
+    weight.  They may have any strides and start at any element (the library's own
+    calls ask for contiguous tensors at 16-byte addresses, so others are copied).
+    `norm.codes(...)` (inference) returns y as 8-bit integer codes with a
     scale for each row, the input of Int8SparseLinear.
 
     A step captured into a HIP graph is run once before on a side stream, and no
@@ -328,13 +339,14 @@ class ResidualRMSNorm(torch.nn.Module):
         """(codes, h), or (codes, h, y) with output=True, in one pass over x; h is
         x itself without a residual.  bf16 or fp16 x."""
         self._check(x, residual)
-        x2 = x.reshape(-1, self.features).contiguous()
-        r2 = None if residual is None else residual.reshape(-1, self.features).contiguous()
+        x2 = _aligned(x.reshape(-1, self.features))
+        r2 = None if residual is None else _aligned(residual.reshape(-1, self.features))
         q = torch.empty(x2.shape, dtype=torch.int8, device=x.device)
         scale = torch.empty(x2.shape[0], dtype=torch.float32, device=x.device)
         h = x2 if r2 is None else torch.empty_like(x2)
         y = torch.empty_like(x2) if output else None
-        slope_rmsnorm(x2, self.weight, self.eps, residual=r2, H=None if r2 is None else h, Y=y, q=q, q_scale=scale)
+        slope_rmsnorm(x2, _aligned(self.weight), self.eps, residual=r2, H=None if r2 is None else h, Y=y, q=q,
+                      q_scale=scale)
         rows = Int8Rows(q.view(x.shape), scale.view(x.shape[:-1]))
         return (rows, h.view(x.shape), y.view(x.shape)) if output else (rows, h.view(x.shape))
 
@@ -370,12 +382,12 @@ class Int8SparseLinear(torch.nn.Module):
             raise ValueError("input must have in_features columns and the layer's format")
         if self.rank and x is None:
             raise ValueError("the adapter needs the 16-bit input next to its codes")
-        x2 = None if x is None else x.reshape(-1, K).contiguous()
+        x2 = None if x is None else _aligned(x.reshape(-1, K))
         if isinstance(rows, Int8Rows):
             if rows.q.shape[-1] != K or rows.scale.shape != rows.q.shape[:-1] or (x is not None and x.shape != rows.q.shape):
                 raise ValueError("codes must have in_features columns, one scale a row, and the input's shape")
             lead = rows.q.shape[:-1]
-            q, scale = rows.q.reshape(-1, K).contiguous(), rows.scale.reshape(-1).contiguous()
+            q, scale = _aligned(rows.q.reshape(-1, K)), rows.scale.reshape(-1).contiguous()
         else:
             lead = x.shape[:-1]
             q = torch.empty(x2.shape, dtype=torch.int8, device=x2.device)

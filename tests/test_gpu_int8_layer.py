@@ -264,3 +264,78 @@ def test_captured_forward_and_backward():
         for a, b in zip(got, step()):
             assert torch.equal(a, b), i
         torch.cuda.synchronize()
+
+
+def at_offset(t, n):
+    """The same values, contiguous, n elements behind an aligned address."""
+    v = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)[n:].view(t.shape)
+    v.copy_(t)
+    assert v.is_contiguous() and v.data_ptr() % 16
+    return v
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("K", [768, 771])
+def test_norm_of_tensors_at_any_address(K, dtype):
+    """Contiguous inputs, weight and gradients that start at any element: the same
+    bits as from aligned ones."""
+    w, x, r, dy, dh = (rand(i, *s, dtype=dtype) for i, s in enumerate([(K,)] + [(5, K)] * 4))
+
+    def outputs(place):
+        norm = ResidualRMSNorm(K, dtype=dtype)
+        norm.weight = torch.nn.Parameter(place(w))
+        a, b = place(x).requires_grad_(), place(r).requires_grad_()
+        y, h = norm(a, b)
+        out = [y, h, *torch.autograd.grad([y, h], [a, b, norm.weight], [place(dy), place(dh)])]
+        y = norm(a)
+        out += [y, *torch.autograd.grad([y], [a, norm.weight], [place(dy)])]
+        if dtype != torch.float32:
+            rows, h, y = norm.codes(place(x), place(r), output=True)
+            out += [*rows, h, y]
+            rows, h = norm.codes(place(x))
+            out += [*rows, h]
+        return out
+    for got, want in zip(outputs(lambda t: at_offset(t, 1)), outputs(lambda t: t)):
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norms_of_odd_width_under_a_concatenation(dtype):
+    """cat's gradient reaches the second norm as rows of a larger tensor that start
+    at any element, x[1:] its input likewise."""
+    norm = ResidualRMSNorm(771, dtype=dtype)
+    x, r, g = rand(1, 4, 771, dtype=dtype), rand(2, 3, 771, dtype=dtype), rand(3, 12, 771, dtype=dtype)
+    a = x[1:].detach().requires_grad_()
+    assert a.data_ptr() % 16
+    b = r.clone().requires_grad_()
+    y, h = norm(a, b)
+    torch.cat([norm(a), y, norm(b), h]).backward(g)
+    got = a.grad, b.grad, norm.weight.grad
+    want = [torch.zeros(t.shape, dtype=torch.float64) for t in got]
+    hs = f64(h).requires_grad_()                         # h as stored; its gradient is a's and b's
+    a64, b64, w = f64(a).requires_grad_(), f64(b).requires_grad_(), f64(norm.weight).requires_grad_()
+    cat = torch.cat([norm64(a64, w, norm.eps), norm64(hs, w, norm.eps), norm64(b64, w, norm.eps), hs])
+    cat.backward(f64(g))
+    want = a64.grad + hs.grad, b64.grad + hs.grad, w.grad
+    # every gradient is a sum of two (weight: three) rounded terms: half a step of each
+    # term and each partial sum, none above the magnitudes added here, and 2^-16 for
+    # the kernels' sums (the terms of test_norm_gradients)
+    def terms(v, d):
+        rs = 1 / torch.sqrt((v * v).mean(-1, keepdim=True) + norm.eps)
+        p, xh = f64(d) * f64(norm.weight), v * rs
+        return (rs * (p.abs() + xh.abs() * (p * xh).abs().mean(-1, keepdim=True))).detach(), (f64(d) * xh).abs().sum(0).detach()
+    (ma, wa), (mh, wh), (mb, wb) = (terms(v, d) for v, d in ((f64(a), g[:3]), (f64(h), g[3:6]), (f64(b), g[6:9])))
+    mh = mh + f64(g[9:]).abs()
+    for t, ref, mag, n in zip(got, want, (ma + mh, mb + mh, wa + wh + wb), (2, 2, 3)):
+        assert ((f64(t) - ref).abs() <= (n * HALF[dtype] + 2.0 ** -16) * mag).all()
+
+
+@pytest.mark.parametrize("rank", [0, 8])
+def test_int8_linear_of_tensors_at_any_address(rank):
+    lin = SparseLinear(rand(1, 64, 128, sigma=0.05), *((rand(2, 128, rank), rand(3, rank, 64)) if rank else ()))
+    q8, x = Int8SparseLinear(lin), rand(4, 5, 128)
+    q, s = torch.empty(5, 128, dtype=torch.int8, device="cuda"), torch.empty(5, device="cuda")
+    S.slope_quantize_rows_i8(x, q, s)
+    want = q8(x)
+    assert torch.equal(q8(at_offset(x, 1)), want)
+    assert torch.equal(q8(Int8Rows(at_offset(q, 3), at_offset(s, 1)), at_offset(x, 5)), want)
