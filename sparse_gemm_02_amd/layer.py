@@ -357,7 +357,9 @@ class Int8SparseLinear(torch.nn.Module):
         y = (q . W_q^T) * scale_row * w_scale (+ (x . L) . R)
 
     The weight's codes and scales (one for each output) are made once, from the
-    layer's current values; the 16-bit weight is not kept.  `lin(x)` quantizes
+    layer's current values; the 16-bit weight is not kept.  All of its tensors keep
+    their formats (float32 scales, the adapter in the layer's own) when the model
+    around it is converted to another; devices change as usual.  `lin(x)` quantizes
     the rows of a bf16 or fp16 x itself; `lin(rows)` takes an Int8Rows, and then,
     if the layer has an adapter, the 16-bit values as well: `lin(rows, x)`."""
 
@@ -372,6 +374,15 @@ class Int8SparseLinear(torch.nn.Module):
             slope_pack_sparse_i8(layer.values, layer.meta, N, K, self.w_scale, self.packed)
             self.register_buffer("L", layer.L.detach().clone() if layer.rank else None)
             self.register_buffer("R", layer.R.detach().clone() if layer.rank else None)
+
+    def _apply(self, fn, recurse=True):
+        kept = dict(self._buffers)
+        super()._apply(fn, recurse)
+        for name, b in kept.items():
+            now = self._buffers[name]
+            if b is not None and now.dtype != b.dtype:   # a conversion: b's values and format, on the new device
+                self._buffers[name] = b.to(now.device)
+        return self
 
     @torch.no_grad()
     def forward(self, rows: Int8Rows | torch.Tensor, x: torch.Tensor | None = None) -> torch.Tensor:

@@ -339,3 +339,26 @@ def test_int8_linear_of_tensors_at_any_address(rank):
     want = q8(x)
     assert torch.equal(q8(at_offset(x, 1)), want)
     assert torch.equal(q8(Int8Rows(at_offset(q, 3), at_offset(s, 1)), at_offset(x, 5)), want)
+
+
+@pytest.mark.parametrize("rank", [0, 8])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_int8_linear_under_conversions_of_its_model(dtype, rank):
+    """A conversion of the model's floating-point tensors leaves the layer's scales
+    in float32 and its adapter in the layer's format; moves between devices take
+    everything along."""
+    lin = SparseLinear(rand(1, 64, 128, dtype=dtype, sigma=0.05),
+                       *((rand(2, 128, rank, dtype=dtype), rand(3, rank, 64, dtype=dtype)) if rank else ()))
+    q8, x = Int8SparseLinear(lin), rand(4, 5, 128, dtype=dtype)
+    want, scale = q8(x), q8.w_scale.clone()
+    model = torch.nn.Sequential(q8)
+    for convert in (lambda m: m.to(torch.bfloat16), lambda m: m.half(), lambda m: m.float(), lambda m: m.double(),
+                    lambda m: m.to("cuda", torch.bfloat16), lambda m: m.cpu().cuda(),
+                    lambda m: m.to("cpu", torch.float16).to("cuda", torch.float64)):
+        convert(model)
+        assert q8.w_scale.dtype == torch.float32 and torch.equal(q8.w_scale, scale)
+        assert torch.equal(model(x), want)
+    with pytest.raises(ValueError, match="format"):
+        model(x.float())
+    model.cpu()
+    assert not any(b.is_cuda for b in model.buffers())
