@@ -93,7 +93,8 @@ slope_status slope_rmsnorm_bwd(slope_dtype dt, const void* dY, const void* H, co
 
 /* The 8-bit integer reading of each row of X [T, K] (BF16 or F16), for
  * activations that no norm precedes and for dY: q [T, K] int8, scale [T]
- * float32, both overwritten.  Any K.  Errors: SLOPE_ERR_UNSUPPORTED for F32. */
+ * float32, both overwritten.  Any K (K = 0: scales 0).  Errors:
+ * SLOPE_ERR_UNSUPPORTED for F32. */
 slope_status slope_quantize_rows_i8(slope_dtype dt, const void* X, int64_t T, int64_t K, int8_t* q, float* scale,
                                     void* stream);
 

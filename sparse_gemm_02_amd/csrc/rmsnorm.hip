@@ -820,7 +820,8 @@ hipError_t launch_rmsnorm(Dt dt, const void* X, const void* res, Dt gamma_dt, co
 
 hipError_t launch_quantize_rows_i8(Dt dt, const void* X, int64_t T, int64_t K, int8_t* q, float* scale,
                                    hipStream_t s) {
-  if (T == 0 || K == 0) return hipSuccess;
+  if (K == 0) return launch_fill_zero(Dt::F32, scale, T, s);   // rows of no values: the scale of zeros
+  if (T == 0) return hipSuccess;
   const NormOut o{nullptr, nullptr, q, scale, nullptr, false};
   return dt == Dt::F16 ? rms_any<_Float16>(X, nullptr, false, nullptr, T, K, 0.f, o, s)
                        : rms_any<uint16_t>(X, nullptr, false, nullptr, T, K, 0.f, o, s);

@@ -288,6 +288,22 @@ def test_empty_calls_write_nothing():
     S.slope_rmsnorm(none, None, EPS, Y=torch.empty_like(none))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [1, 5, 300])
+def test_quantizer_of_rows_without_values(T, dt):
+    """K = 0: the scales of rows of zeros, so that a product with them is zeros."""
+    sc = torch.full((T + GUARD,), float("nan"), device="cuda")
+    sc[T:] = 77
+    q = torch.empty((T, 0), dtype=torch.int8, device="cuda")
+    S.slope_quantize_rows_i8(torch.empty((T, 0), dtype=DT[dt], device="cuda"), q, sc[:T])
+    torch.cuda.synchronize()
+    assert not sc[:T].any() and bool((sc[T:] == 77).all())
+    y = torch.full((T, 8), 4.0, device="cuda")
+    S.slope_spmm_i8_packed(q, sc[:T], torch.empty(0, dtype=torch.uint8, device="cuda"), torch.ones(8, device="cuda"), 8, y)
+    torch.cuda.synchronize()
+    assert not y.any()
+
+
 # ------------------------------------------------------------------ gradient
 
 def check_bwd(T, K, dt, gdt, with_dh, seed=0, accumulate=False, in_place=None):
