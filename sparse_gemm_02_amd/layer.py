@@ -410,5 +410,6 @@ class Int8SparseLinear(torch.nn.Module):
         product(q, scale, self.packed, self.w_scale, N, y)
         if self.rank and T:
             ws = _bytes(slope_lowrank_workspace_bytes(T, K, self.rank, N), q.device)
-            slope_lowrank_add(x2, self.L, self.R, ws, y)
+            with torch.cuda.device(q.device):        # the call takes the current device's stream
+                slope_lowrank_add(x2, self.L, self.R, ws, y)
         return y.view(*lead, N)

@@ -150,3 +150,32 @@ def test_binding_refuses_shapes_types_and_places(lib):
         S.slope_spmm_i8_packed(i8(4, 32), f(4), i8(20480), f(7), 8, f(4, 8))
     with pytest.raises(ValueError, match="Y must"):
         S.slope_spmm_i8_decode(i8(4, 32), f(4), i8(20480), f(8), 8, f(8, 4))
+
+
+def test_adapter_of_the_int8_linear_runs_on_its_tensors_device(monkeypatch):
+    """With another device current, the adapter's call (which takes the current
+    device's stream) is made with the tensors' device current."""
+    import contextlib
+    from sparse_gemm_02_amd import layer as M
+    made = []
+    current = ["another"]
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], d
+        yield
+        current[0] = before
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for name in ("slope_quantize_rows_i8", "slope_spmm_i8_decode", "slope_spmm_i8_packed"):
+        monkeypatch.setattr(M, name, lambda *a: None)
+    monkeypatch.setattr(M, "slope_lowrank_workspace_bytes", lambda *a: 16)
+    monkeypatch.setattr(M, "slope_lowrank_add", lambda *a, **k: made.append(current[0]))
+    lin = M.Int8SparseLinear.__new__(M.Int8SparseLinear)
+    torch.nn.Module.__init__(lin)
+    lin.in_features, lin.out_features, lin.rank, lin.dtype = 32, 16, 4, torch.bfloat16
+    for name, shape in (("packed", 16), ("w_scale", 16), ("L", (32, 4)), ("R", (4, 16))):
+        lin.register_buffer(name, torch.zeros(shape))
+    x = torch.zeros((3, 32), dtype=torch.bfloat16)
+    lin(x)
+    lin(M.Int8Rows(torch.zeros((3, 32), dtype=torch.int8), torch.zeros(3)), x)
+    assert made == [x.device, x.device] and current == ["another"]
