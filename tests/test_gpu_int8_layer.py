@@ -362,3 +362,9 @@ def test_int8_linear_under_conversions_of_its_model(dtype, rank):
         model(x.float())
     model.cpu()
     assert not any(b.is_cuda for b in model.buffers())
+
+
+def test_int8_linear_refuses_a_second_input_it_would_not_read():
+    q8, x = Int8SparseLinear(SparseLinear(rand(1, 64, 128, sigma=0.05))), rand(2, 5, 128)
+    with pytest.raises(ValueError, match="one input"):
+        q8(x, rand(3, 5, 128))
