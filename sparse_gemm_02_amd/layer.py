@@ -388,7 +388,7 @@ class Int8SparseLinear(torch.nn.Module):
     def forward(self, rows: Int8Rows | torch.Tensor, x: torch.Tensor | None = None) -> torch.Tensor:
         K, N = self.in_features, self.out_features
         if not isinstance(rows, Int8Rows):
-            if x is not None:
+            if x is not None and x is not rows:
                 raise ValueError("give one input, or its Int8Rows and the input itself")
             x = rows
         if x is not None and (x.shape[-1] != K or x.dtype != self.dtype):

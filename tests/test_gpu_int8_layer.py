@@ -368,3 +368,4 @@ def test_int8_linear_refuses_a_second_input_it_would_not_read():
     q8, x = Int8SparseLinear(SparseLinear(rand(1, 64, 128, sigma=0.05))), rand(2, 5, 128)
     with pytest.raises(ValueError, match="one input"):
         q8(x, rand(3, 5, 128))
+    assert torch.equal(q8(x, x), q8(x))
