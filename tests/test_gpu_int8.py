@@ -149,6 +149,15 @@ def test_product_on_many_tiles(T, K, N):
     assert np.array_equal(c.run(S.slope_spmm_i8_packed, "bf16"), c.ref("bf16"))
 
 
+# the full tiles' ring of three slots over 19 stages: full tiles alone, full tiles
+# with a last rows of half tiles, and half tiles alone
+@pytest.mark.parametrize("T,K,N", [(1000, 2320, 9220), (4100, 2320, 4612), (500, 2320, 9216)])
+def test_product_of_large_tiles_over_many_stages(T, K, N):
+    say(f"[i8 product] T={T} K={K} N={N}")
+    c = Case(T, K, N, seed=T + N)
+    assert np.array_equal(c.run(S.slope_spmm_i8_packed, "bf16"), c.ref("bf16"))
+
+
 @pytest.mark.parametrize("T", [1 << 22, (1 << 22) - 64])
 def test_product_of_as_many_tokens_as_there_may_be(T):
     K, N = 16, 4
