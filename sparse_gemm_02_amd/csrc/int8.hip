@@ -33,8 +33,8 @@ constexpr int kChunkValueBytes = kChunkRows * 64, kChunkBytes = kChunkValueBytes
 // the rows' kept values for their largest magnitudes, a second (served by the
 // caches) for the codes, written as chunk pieces.  Lane k of a row takes its
 // compressed values 8k .. 8k+7 of each chunk and metadata word k.  Made once for a
-// weight: 27648 x 9216 168 us (2.4 TB/s of 1.125 bytes in and 0.625 out, the first
-// walk's latency and the second walk's).
+// weight: 27648 x 9216 165 to 182 us (2.5 to 2.7 TB/s of 1.125 bytes in and 0.625
+// out, the first walk's latency and the second walk's).
 template <typename In>
 __global__ __launch_bounds__(256) void pack_i8_kernel(const In* __restrict__ vals, const uint32_t* __restrict__ meta,
                                                       int64_t M, int64_t K, int64_t stages, float* __restrict__ scale,
@@ -112,8 +112,8 @@ __device__ __forceinline__ void store4(O* p, const float (&y)[4]) {
 //
 // Every source and LDS address is kept and stepped (one add a load and stage):
 // with offsets, ring slots and bounds computed anew each stage the same schedule
-// took 436 us for 8192 x 9216 x 9216, against 389 (and 374 since tiles are stored
-// by whole lines).
+// took 436 us for 8192 x 9216 x 9216, against 389 (and less since tiles are stored
+// by whole lines: below).
 template <int BM_, int BT_, int WGM_, int WGT_, int BLOCKS_, int NST_ = 3>
 struct GeoI8 {
   static constexpr int BM = BM_, BT = BT_, WGM = WGM_, WGT = WGT_, WAVES = WGM * WGT, THREADS = 64 * WAVES;
@@ -356,10 +356,13 @@ __global__ __launch_bounds__(G::THREADS, G::BLOCKS* G::WAVES / 4) void spmm_i8_k
 // reads are complete before the barrier that ends its memory phase, so a slot is
 // free (both groups have read it) in the phase its refill is issued.
 //
-// 8192 x 9216 x 9216, bf16 out: 374 us, 3.7e15 dense-equivalent operations a
-// second, half of what the instruction alone reaches in a tight loop.  The matrix
-// cores are busy 49% of the cycles, at 1.8 GHz, where the card's power holds the
-// clock.  Timing copies of the loop (of 388 us then): without the loads into LDS
+// 8192 x 9216 x 9216, bf16 out: 360 to 400 us with the clock that the card holds
+// (1.8 GHz at 376), 3.7e15 dense-equivalent operations a second, half of what the
+// instruction alone reaches in a tight loop.  Counted, a stage of a full tile takes
+// about 2030 cycles, 1024 of them products (the matrix cores are busy 49% of the
+// time): a phase lasts some 1015 cycles where its products take 512, so the memory
+// phase, twice as long as the products beside it, is what bounds the loop.
+// Timing copies of it (of 388 us then): without the loads into LDS
 // 310, without the reads from it 306, without the products 327, products alone
 // 275.  Slower were: one schedule for all waves (5 to 8%), 128 x 128 a wave in
 // four waves, a raised priority for the multiplying waves, the refill issued
@@ -474,13 +477,15 @@ struct SpmmArgs {
 // needs two neighbouring words (one 8-byte load) and two neighbouring granules.
 // Its B operand is then k 32s + 16h .. and 64 + 32s + 16h .. (h = lane / 32).
 //
-// Measured (bf16 out; floor: the weight at a copy's 5.13 TB/s): 9216 -> 27648 at
-// 1 / 16 / 64 tokens 31.2 / 34.1 / 44.9 us (floor 31.0), 9216 -> 9216 11.1 /
-// 11.8 / 16.4 (10.3), 5120 -> 15360 10.4 / 10.7 / 12.6 (9.6), 20480 -> 5120 12.6
-// / 14.4 / 23.2 (12.8), 36864 -> 9216 42.3 / 50.8 / 74.4 (41.4); decode_launch
-// below gives some of them to the GEMM's tiles.  At one token
-// HBM bounds it; at 64 the L1s, through which every block draws all of X (two and
-// three sets in flight, 12 and 16 waves: the same or slower).
+// Measured (us, bf16 out, with the better of 64 and 32 rows; floor: the weight at the
+// 6.04 TB/s of a large read): 9216 -> 27648 at 1 / 16 / 64 tokens 30.3 / 33.9 / 44.6
+// (floor 26.4), 9216 -> 9216 10.9 / 11.8 / 18.3 (8.8), 5120 -> 15360 10.2 / 10.8 /
+// 13.2 (8.1), 20480 -> 5120 12.7 / 14.4 / 23.2 (10.9), 36864 -> 9216 42.2 / 50.5 /
+// 77.2 (35.2); decode_launch below gives some of them to the GEMM's tiles.  At one
+// token HBM bounds it.  At 64 a block takes in all of X beside its weight, at about
+// 75 GB/s a compute unit whatever its queue (two and three sets in flight, 12 and 16
+// waves: the same or slower; what sets that rate is not established), and a long
+// reduction leaves units without a block (20480 -> 5120: 160 blocks).
 template <int FM>
 struct DecodeA {
   i32x4 a[FM][2];
@@ -694,19 +699,19 @@ hipError_t tiles_go(const SpmmArgs<O>& a) {
 
 // Tiles of the GEMM's kind in one round: where BM rows a tile leave more than half
 // of the compute units one tile each, and none two, its deeper queue of weight
-// streams faster than the kernel above (us, tiles against it):
-//   9216 -> 27648 (216 tiles of 128): 1 token 29.9 / 30.8, 32: 30.3 / 36.7, 64: 33.3 / 44.8
-//   9216 -> 36864 (144 of 256):       1 token 39.4 / 42.4, 32: 43.2 / 50.6, 64: 48.3 / 64.0
-//   5120 -> 20480 (160 of 128):       1 token 11.4 / 14.3, 32: 12.3 / 16.6, 64: 13.3 / 19.1
-//   5120 -> 15360 (240 of 64):                             32: 11.1 / 11.0, 64: 11.2 / 12.9
-//   9216 -> 9216 (144 of 64):                              32: 16.7 / 11.8, 64: 16.8 / 17.8
+// streams faster than the kernel above (us, tiles against the better of its two forms):
+//   9216 -> 27648 (216 tiles of 128): 1 token 29.8 / 30.3, 32: 30.3 / 36.4, 64: 33.5 / 44.6
+//   9216 -> 36864 (144 of 256):       1 token 39.3 / 40.3, 32: 43.0 / 49.9, 64: 48.1 / 63.9
+//   5120 -> 20480 (160 of 128):       1 token 11.5 / 14.3, 32: 12.4 / 15.9, 64: 13.2 / 19.2
+//   5120 -> 15360 (240 of 64):                             32: 11.0 / 11.1, 64: 11.3 / 13.2
+//   9216 -> 9216 (144 of 64):                              32: 16.9 / 12.0, 64: 16.9 / 18.3
 // (so 64 rows only from 33 tokens on).  With fewer tiles a compute unit's share
-// takes longer (20480 -> 5120, 80 tiles of 64, 64 tokens: 33.0 / 22.8).
+// takes longer (20480 -> 5120, 80 tiles of 64, 64 tokens: 32.8 / 23.2).
 //
 // Otherwise 64 rows a block where that leaves 128 blocks or more (9216 outputs, 9216 wide,
-// 32 tokens: 11.9 us against 16.4 with 32 rows): every block draws all of X, so
+// 32 tokens: 12.0 us against 16.6 with 32 rows): every block draws all of X, so
 // wider ones draw it less often.  Below, 64 rows would leave too many compute
-// units idle (5120 outputs, 20480 wide, 32 tokens: 20.4 us against 16.6).
+// units idle (5120 outputs, 20480 wide, 32 tokens: 20.7 us against 16.7).
 // Waves, stages and sets as measured best over the five shapes above: the
 // registers are kept to 128 (two blocks a compute unit) up to 32 tokens; at 64
 // the 64-row block needs more, and four waves beat eight (44.9 against 46.8 us).
@@ -733,7 +738,7 @@ hipError_t decode_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K
 //   large   0.010 a unit of full_width_rows' cost (100 a round of full tiles, 65
 //           of half tiles)
 //   small   128 x 128 tiles: 0.42 up to one a compute unit (eight waves, four
-//           slots: 5120 -> 20480 at 128 tokens 17.1 us, as below 18.6), then 0.35 +
+//           slots: 5120 -> 20480 at 128 tokens 17.6 us, as below 18.8), then 0.35 +
 //           0.0014 a tile (two a unit, four waves and three slots each)
 //   narrow  128 x 64 tiles, at most one a compute unit: 0.25, or 64 x 64: 0.215.
 //           A compute unit takes in some 70 GB/s by LDS-DMA however deep the ring
@@ -742,15 +747,24 @@ hipError_t decode_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K
 //           smaller tiles is enough, less to load is faster.
 //   direct  the few-token kernel over groups of 64 tokens, 64 rows a block: 0.13 +
 //           0.0006 a block; up to 128 such blocks 32 rows (4096 -> 1024 at 512
-//           tokens 7.2 us against 8.9; 5120 -> 5120 at 65, 160 blocks, 12.5
+//           tokens 7.3 us against 9.2; 5120 -> 5120 at 65, 160 blocks, 12.8
 //           against 11.5)
-// Measured, us (large / small / direct), before the tiles were stored by whole
-// lines, which took 3 to 9% off the first two alike: 9216 -> 9216 at 128 tokens 40
-// / 29.5 / 24, 256: 41 / 31 / 37, 512: 42 / 49 / 62, 1000: 65 / 79 / 111, 8192: 380
-// / 491 / 895; 20480 -> 5120 at 256: 79 / 58 / 51, 512: 80 / 59 / 78, 1000: 85 /
-// 103 / 130.  Narrow against the best of these: 9216 -> 9216 at 128 tokens 19.9 /
-// 24.1, 20480 -> 5120 at 128: 38.6 (64 x 64 33.1) / 32.1, at 192: 39.0 (33.7) / 46,
-// at 256: 39.1 / 50.7, 5120 -> 5120 at 256: 13.1 / 15.9.
+// Measured, us (large / small, up to one tile a compute unit in its eight-wave form /
+// 128 x 64 / 64 x 64 / direct with 64 rows), the rule's choice starred:
+//   9216 -> 9216    128 tokens  37.7 /  26.3 /  20.3* /  22.8  /  24.1
+//                   256         37.7 /  26.7*/  31.3  /  33.7  /  36.3
+//                   512         38.7*/  45.7 /  49.6  /  54.4  /  61.4
+//                  1000         58.3*/  73.1 /  80.9  /  99.4  / 109
+//                  8192        359 * / 465   /        /        / 882
+//   20480 -> 5120    65         75.9 /  52.4 /  38.6  /  33.1* /  31.4
+//                   256         76.8 /  52.8 /  39.4* /  47.5  /  50.7
+//                   512         77.2 /  53.5*/  68.9  /  73.1  /  77.3
+//                  1000         78.8*/  99.3 / 104    / 125    / 129
+//   5120 -> 5120     65         22.4 /  16.4 /  12.8  /  10.9* /  11.5
+//                   256         23.3 /  17.1 /  13.2* /  15.5  /  15.9
+//   9216 -> 27648   128         54.3 /  41.6*/  50.8  /  65.0  /  76.1
+//                   512         80.8*/ 118   / 147    / 181    / 207
+//   4096 -> 1024    512         19.3 /  14.1 /  11.1  /   9.6  /   9.2 (32 rows 7.3*)
 template <typename O>
 hipError_t spmm_launch(const int8_t* Xq, const float* xs, int64_t T, int64_t K, const void* packed, const float* ws,
                        int64_t M, void* Y, hipStream_t s) {

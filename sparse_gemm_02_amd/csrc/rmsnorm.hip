@@ -8,20 +8,26 @@
 // code (1) out.  A row is read once into registers, its sum of squares and its
 // largest |h g| are reduced together (the codes do not need rstd: it is common
 // to the row and cancels), and the outputs are made from the registers.
-// Measured: 8192 x 9216 bf16 with residual and codes 97.5 us (5.4 TB/s; a plain
-// copy reaches 5.1), with y in place of the codes 106; 16384 x 1024 23 us; 1021 x
-// 5120 fp16 with an fp32 gamma 7.6 us and 2047 x 771 fp32 6.5 us, of which one row
-// alone takes 4.2; without a residual (8192 x 9216 fp16, 64 us, 3.5 TB/s) the
-// arithmetic bounds it.
+// Measured (kernel times, medians): 8192 x 9216 bf16 with residual and codes 99 us
+// (5.3 TB/s; a plain copy reaches 5.1), with y in place of the codes 106; 16384 x
+// 1024 21 us; 1021 x 5120 fp16 with an fp32 gamma 9.4 us and 2047 x 771 fp32 6.6 us,
+// of which one row alone takes 4.2.  Codes without a residual (8192 x 9216, 44 us at
+// a copy's rate): bf16 without a gamma 44 us, fp16 50, with an fp16 gamma 52 (the
+// vector units issue 80% of the cycles: the arithmetic bounds it), with an fp32 gamma
+// 72 (63%: the search for the left-over, with its reduction, comes on top).
 //
 // Gradient:  a = dy g,  xh = h rstd,  c = mean(a xh)
 //   dx = rstd (a - xh c) + dh,   dg = sum over tokens of dy xh
 // The same row layout; a block keeps its columns over many rows, so dg's
 // partial sums stay in registers, and a second kernel adds the blocks' rows in
-// order.  Measured, with both kernels: 8192 x 9216 bf16 with dh 119 us (5.1 TB/s),
-// 16384 x 1024 28, 4096 x 5120 36, 8192 x 768 fp16 14.3 us (11 and 3.5: launches
-// and the first loads, not bandwidth); few long rows (512 x 20480, 34 us) pay for
-// the partial rows.
+// order.  Measured, with both kernels: 8192 x 9216 bf16 with dh 120 us (5.1 TB/s),
+// 16384 x 1024 30, 4096 x 5120 38, 8192 x 768 fp16 15.1 us (11.2 and 3.9: launches
+// and the first loads, not bandwidth).  Above 1536 vectors a row (12288 elements of
+// 16 bits) a thread has four vectors, and 1024 threads leave it 128 registers: with
+// 16-bit rows and a gamma these forms spill (7 to 59 of them, 135 in the odd-width
+// form of fp16 rows and an fp32 gamma).  8192 x 16384 with dh (209 us at a copy's rate):
+// bf16 298, fp16 with an fp32 gamma 442; 8192 x 16387: 450 and 903.  Few long rows
+// (512 x 20480, 31 us against 12) pay for the partial rows too.
 #include <type_traits>
 
 #include "common.h"
