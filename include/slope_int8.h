@@ -44,7 +44,8 @@ extern "C" {
  *   q, q_scale = the 8-bit integer reading of the row u = h * gamma, the
  *          products taken exactly, the scale amax / 127 * rstd
  * h is used as rounded, so a gradient or a later call that starts from H sees
- * the same numbers.  Sums are float32.
+ * the same numbers.  Sums are float32 (a row whose squares' sum passes float32's
+ * range has rstd 0, and so y and q_scale 0).
  *   X, residual_or_null  [T, K] dt
  *   gamma_or_null        [K] gamma_dt (dt or F32), NULL = all ones
  *   eps                  positive, a normal number in float32
@@ -135,7 +136,8 @@ slope_status slope_spmm_i8_packed(slope_dtype out_dt, const int8_t* Xq, const fl
 
 /* slope_spmm_i8_packed for T <= SLOPE_I8_DECODE_MAX_TOKENS tokens, where the
  * cost is the weight's stream from memory: the same arguments and the same
- * results, bit for bit, without a workspace.  Errors: those of
+ * results, bit for bit, without a workspace (slope_spmm_i8_packed takes the same
+ * path for that many tokens; this entry refuses more).  Errors: those of
  * slope_spmm_i8_packed, SLOPE_ERR_UNSUPPORTED for more tokens. */
 slope_status slope_spmm_i8_decode(slope_dtype out_dt, const int8_t* Xq, const float* x_scale, int64_t T, int64_t K,
                                   const void* packed_w, int64_t packed_w_bytes, const float* w_scale, int64_t N,

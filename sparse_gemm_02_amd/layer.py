@@ -337,7 +337,8 @@ class ResidualRMSNorm(torch.nn.Module):
     @torch.no_grad()
     def codes(self, x: torch.Tensor, residual: torch.Tensor | None = None, output: bool = False):
         """(codes, h), or (codes, h, y) with output=True, in one pass over x; h is
-        x itself without a residual.  bf16 or fp16 x."""
+        x itself without a residual (a copy where x is strided or unaligned).  bf16
+        or fp16 x."""
         self._check(x, residual)
         x2 = _aligned(x.reshape(-1, self.features))
         r2 = None if residual is None else _aligned(residual.reshape(-1, self.features))
