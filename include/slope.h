@@ -555,4 +555,7 @@ slope_status slope_spmm_e4m3_packed(slope_dtype out_dt, const uint8_t* Xq, const
 /* The RMS norm with 8-bit codes, its gradient, and the int8 products. */
 #include "slope_int8.h"
 
+/* AdamW over many tensors with 8-bit moments; 4-bit floating point. */
+#include "slope_mx.h"
+
 #endif /* SLOPE_H_ */

@@ -1,0 +1,79 @@
+/*
+ * slope_mx.h - microscaled formats: small floating-point codes with one power-of-two
+ * scale for each block of 32 values.  The AdamW step over many tensors at once with
+ * moments held so, in 8 bits; and the 2:4 sparse product on 4-bit codes.  Part of the
+ * C ABI of libslope.so (included by slope.h; its conventions on memory, streams and
+ * errors hold here).
+ *
+ * A scale is one byte b standing for 2^(b - 127); 255 marks a block without values:
+ * everything in it is NaN.
+ */
+#ifndef SLOPE_MX_H_
+#define SLOPE_MX_H_
+
+#include "slope.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Values with one scale. */
+#define SLOPE_MX_BLOCK 32
+
+/* One AdamW step (slope_adamw's formula and its float32 arithmetic) on `count`
+ * tensors, in one launch for up to 56 tensors of one pair of types.
+ *
+ * state_bits = 32: m[i], v[i] are float32 [n[i]]; results are slope_adamw's on each
+ * tensor, bit for bit; m_exp and v_exp are not looked at.
+ *
+ * state_bits = 8: m[i], v[i] are codes, uint8 [n[i]], and m_exp[i], v_exp[i] the
+ * scales, uint8 [ceil(n[i] / 32)], one for 32 consecutive values (the last block may be
+ * short).  m is in E4M3 (sign, 4 exponent bits with bias 7, 3 mantissa bits), v in
+ * E5M3 without a sign (5 exponent bits with bias 15, 3 mantissa bits; no infinities,
+ * no NaN).  All bytes zero are moments of zero.  Of a block's new moments x in float32
+ *   scale  2^E, E = max(-127, floor(log2 max |x|) - top), top = 7 for m, 15 for v
+ *   code   |x| 2^-E as a place on the format's grid, to 2^-20 of a code, rounded down
+ *          after 20 random bits are added below the last bit kept (stochastic
+ *          rounding); a positive v never becomes zero
+ * and with an infinity or a NaN in the block its scale is 255 and its codes are 0.
+ * The weights' update uses the moments before they are rounded.
+ * The random bits of value j of tensor i are those of a 32-bit word: m takes bits
+ * 31..12, v bits 19..0.  With r = low 32 bits of j / 8 and z_i the low 32 bits of
+ * SplitMix64 (Steele, Lea and Flood, 2014) at state seed + i * 0x9E3779B97F4A7C15,
+ * s = r * 0x9E3779B1 ^ z_i, s = (s ^ s >> 16) * 0xBB67AE85, s ^= s >> 15, and the
+ * words of values 8r .. 8r+7 are the next eight states of Marsaglia's xorshift (13,
+ * 17, 5).  Give every step another seed.  Equal arguments give equal results.
+ *
+ *   state_bits           8 or 32
+ *   count                tensors; the arrays below are host memory, read during the call
+ *   param_dt, grad_dt    [count] slope_dtype values
+ *   params               [count] the weights, updated in place
+ *   grads                [count] their gradients
+ *   m, v, m_exp, v_exp   [count] the moments, updated in place
+ *   n                    [count] numbers of values (0: the tensor is left out)
+ *   hp                   hyper-parameters; step counts from 1
+ * Tensors need only their element type's alignment.  The step's number and the seed are
+ * the call's own: a call recorded into a graph repeats them at each replay.
+ * Errors: slope_adamw's, and SLOPE_ERR_INVALID_ARG for other state_bits, count < 0
+ * or two of the written tensors that share memory; SLOPE_ERR_ALIGN for a tensor not
+ * aligned to its elements. */
+slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* param_dt, const int32_t* grad_dt,
+                               void* const* params, const void* const* grads, void* const* m, void* const* v,
+                               uint8_t* const* m_exp, uint8_t* const* v_exp, const int64_t* n,
+                               const slope_adamw_params* hp, uint64_t seed, void* stream);
+
+/* The values of 8-bit moments (code * 2^E; NaN where the scale is 255): m, v codes
+ * [n], m_exp, v_exp scales [ceil(n / 32)], outputs [n] in out_dt: BF16 or F32, both
+ * hold every value exactly (bfloat16 has four significant bits to spare).  Either
+ * moment may be left out: its three arguments are NULL.  Any alignment of the codes;
+ * outputs need their element's.  Errors: SLOPE_ERR_INVALID_ARG for an incomplete
+ * moment or none, SLOPE_ERR_UNSUPPORTED for F16 or n > 2^40. */
+slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, const uint8_t* m_exp_or_null,
+                                 const uint8_t* v_or_null, const uint8_t* v_exp_or_null, int64_t n,
+                                 void* m_out_or_null, void* v_out_or_null, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SLOPE_MX_H_ */

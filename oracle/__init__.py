@@ -7,5 +7,7 @@ from .slope_ref import *  # noqa: F401,F403
 from .slope_ref import __all__ as _slope_all
 from .int8_ref import *  # noqa: F401,F403
 from .int8_ref import __all__ as _int8_all
+from .mx_ref import *  # noqa: F401,F403
+from .mx_ref import __all__ as _mx_all
 
-__all__ = [*_slope_all, *_int8_all]
+__all__ = [*_slope_all, *_int8_all, *_mx_all]

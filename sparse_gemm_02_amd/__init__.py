@@ -2,7 +2,7 @@
 
 Argument marshalling only: every function below checks that its tensors are
 contiguous device tensors, reads their shapes and dtypes, and calls the C ABI
-function of the same name (declared in include/slope.h and slope_int8.h) on the
+function of the same name (declared in include/slope.h, slope_int8.h and slope_mx.h) on the
 current HIP stream.  All computation happens in the library's HIP kernels; there is no
 fallback.  If the shared library has not been built, every call raises.
 
@@ -39,6 +39,7 @@ __all__ = [
     "slope_rmsnorm", "slope_rmsnorm_bwd_workspace_bytes", "slope_rmsnorm_bwd", "slope_quantize_rows_i8",
     "slope_packed_sparse_i8_bytes", "slope_pack_sparse_i8", "slope_spmm_i8_packed", "slope_spmm_i8_decode",
     "I8_DECODE_MAX_TOKENS", "I8_MAX_COLS", "EXPORTED_SYMBOLS_INT8",
+    "slope_adamw_multi", "slope_adamw_moments", "MX_BLOCK", "EXPORTED_SYMBOLS_MX",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -126,6 +127,15 @@ _SIGS_INT8 = {
 }
 EXPORTED_SYMBOLS_INT8 = tuple(_SIGS_INT8)
 
+# include/slope_mx.h
+_P_I32, _P_VP = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(_vp)
+_SIGS_MX = {
+    "slope_adamw_multi": (_i32, [_i32, _i64, _P_I32, _P_I32, _P_VP, _P_VP, _P_VP, _P_VP, _P_VP, _P_VP, _P_I64, _P_HP,
+                                 ctypes.c_uint64, _vp]),
+    "slope_adamw_moments": (_i32, [_i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+}
+EXPORTED_SYMBOLS_MX = tuple(_SIGS_MX)
+
 _lib = None
 
 
@@ -143,7 +153,7 @@ def library() -> ctypes.CDLL:
             raise RuntimeError(f"{library_path} is missing: build it first "
                                "(python -m sparse_gemm_02_amd.build); there is no fallback path")
         lib = ctypes.CDLL(library_path)
-        for name, (res, args) in (*_SIGS.items(), *_SIGS_INT8.items()):
+        for name, (res, args) in (*_SIGS.items(), *_SIGS_INT8.items(), *_SIGS_MX.items()):
             f = getattr(lib, name)
             f.restype, f.argtypes = res, args
         _lib = lib
@@ -681,3 +691,91 @@ def slope_spmm_i8_packed(Xq, x_scale, packed_w, w_scale, N, Y, stream=None) -> N
 def slope_spmm_i8_decode(Xq, x_scale, packed_w, w_scale, N, Y, stream=None) -> None:
     """slope_spmm_i8_packed for at most I8_DECODE_MAX_TOKENS tokens: the same result, bit for bit."""
     _spmm_i8("slope_spmm_i8_decode", Xq, x_scale, packed_w, w_scale, N, Y, stream)
+
+
+# ------------------------------------------------------------------ microscaled formats
+# Codes and scales travel as torch.uint8 tensors.  As above these calls check shapes,
+# dtypes and devices, and run on the tensors' device.
+
+MX_BLOCK = 32               # SLOPE_MX_BLOCK
+
+_u8 = torch.uint8
+
+
+def _multi_refuse(i, p, g, m, v, me, ve, dev, mdt):
+    """Raises what tensor i of a list is refused for."""
+    n = p.numel()
+    for name, t in (("params", p), ("grads", g), ("m", m), ("v", v), ("m_exp", me), ("v_exp", ve)):
+        if t is None:
+            continue
+        name = f"{name}[{i}]"
+        want = -(-n // MX_BLOCK) if "_exp" in name else n
+        if t.numel() != want:
+            raise ValueError(f"{name} must have {want} elements, got {t.numel()}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {_place(t.get_device())}, not on {_place(dev)}")
+    _dt(p), _dt(g)
+    for name, t, dtype in (("m", m, mdt), ("v", v, mdt), ("m_exp", me, _u8), ("v_exp", ve, _u8)):
+        if t is not None and t.dtype is not dtype:
+            raise TypeError(f"{name}[{i}] must be {dtype}, got {t.dtype}")
+    raise ValueError(f"tensor {i} of the lists is not accepted")
+
+
+def slope_adamw_multi(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, m_exp=None,
+                      v_exp=None, seed=0, stream=None) -> None:
+    """One AdamW step on lists of tensors (weights and moments updated in place).
+    With float32 moments m, v: slope_adamw's results on each.  With uint8 codes
+    m, v and the scales of their blocks of 32 in m_exp, v_exp: 8-bit moments,
+    rounded stochastically with random bits from `seed` (another for each step)."""
+    count = len(params)
+    if count == 0:
+        if grads or m or v or m_exp or v_exp:
+            raise ValueError("the lists must have the same length")
+        return
+    eight = m_exp is not None or v_exp is not None
+    mes, ves = (m_exp, v_exp) if eight else (m, v)
+    if mes is None or ves is None:
+        raise ValueError("8-bit moments need both m_exp and v_exp")
+    if not len(grads) == len(m) == len(v) == len(mes) == len(ves) == count:
+        raise ValueError("the lists must have the same length")
+    dev, mdt = params[0].get_device(), _u8 if eight else _f32t
+    sizes = []
+    for i in range(count):
+        p, g, a, b = params[i], grads[i], m[i], v[i]
+        n = p.numel()
+        if not (g.numel() == a.numel() == b.numel() == n and a.dtype is mdt and b.dtype is mdt and p.dtype in _CODES
+                and g.dtype in _CODES and p.is_contiguous() and g.is_contiguous() and a.is_contiguous()
+                and b.is_contiguous() and p.get_device() == g.get_device() == a.get_device() == b.get_device() == dev):
+            _multi_refuse(i, p, g, a, b, mes[i] if eight else None, ves[i] if eight else None, dev, mdt)
+        if eight:
+            x, y = mes[i], ves[i]
+            if not (x.numel() == y.numel() == -(-n // MX_BLOCK) and x.dtype is _u8 and y.dtype is _u8
+                    and x.is_contiguous() and y.is_contiguous() and x.get_device() == y.get_device() == dev):
+                _multi_refuse(i, p, g, a, b, x, y, dev, mdt)
+        sizes.append(n)
+    ptrs, codes = _vp * count, ctypes.c_int32 * count
+    addresses = lambda ts: ptrs(*[t.data_ptr() for t in ts])
+    hp = _hp(step, lr, beta1, beta2, eps, weight_decay)
+    _on_device("slope_adamw_multi", dev, stream, 8 if eight else 32, count, codes(*[_CODES[p.dtype] for p in params]),
+               codes(*[_CODES[g.dtype] for g in grads]), addresses(params), addresses(grads), addresses(m), addresses(v),
+               addresses(mes) if eight else None, addresses(ves) if eight else None, (_i64 * count)(*sizes),
+               ctypes.byref(hp), int(seed) & (2 ** 64 - 1))
+
+
+def slope_adamw_moments(m, m_exp, v, v_exp, m_out=None, v_out=None, stream=None) -> None:
+    """The values of 8-bit moments as bfloat16 or float32 (m_out, v_out; one
+    moment may be left out: None for its three tensors)."""
+    first = m if m is not None else v
+    if first is None:
+        raise ValueError("give one moment at least")
+    n, d = first.numel(), first.get_device()
+    out = m_out if m_out is not None else v_out
+    odt = _f32t if out is None else out.dtype
+    blocks = -(-n // MX_BLOCK)
+    flat = lambda t, name, size, dtype: None if t is None else _arg(t.view(-1) if t.is_contiguous() else t, name, (size,),
+                                                                    dtype, d)
+    _on_device("slope_adamw_moments", d, stream, _code(odt), flat(m, "m", n, _u8), flat(m_exp, "m_exp", blocks, _u8),
+               flat(v, "v", n, _u8), flat(v_exp, "v_exp", blocks, _u8), n, flat(m_out, "m_out", n, odt),
+               flat(v_out, "v_out", n, odt))

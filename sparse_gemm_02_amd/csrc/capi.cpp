@@ -6,9 +6,12 @@
 #include <cmath>
 
 #include "../../include/slope.h"
+#include "adamw_args.h"
 #include "launch.h"
 
+using slope::adamw_step;
 using slope::Dt;
+using slope::kAdamwMaxElems;
 
 namespace {
 
@@ -45,27 +48,6 @@ constexpr int64_t kPackedMaxCols = 1 << 21, kPackedMaxRank = 128;
 constexpr int64_t kDecodeMaxTokens = 64;   // the few-token forward
 
 int64_t workspace_need(int64_t T, int64_t K, int64_t r, int64_t N) { return slope::lowrank_workspace_bytes(T, K, r, N); }
-
-// Checks AdamW hyper-parameters and derives the per-update fp32 constants.
-slope_status adamw_step(const slope_adamw_params* hp, slope::AdamWStep* c) {
-  if (!hp) return SLOPE_ERR_INVALID_ARG;
-  if (hp->step < 1 || !(hp->beta1 >= 0.0 && hp->beta1 < 1.0) || !(hp->beta2 >= 0.0 && hp->beta2 < 1.0) ||
-      !(hp->eps >= 0.0) || !std::isfinite(hp->eps) || !std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay))
-    return SLOPE_ERR_INVALID_ARG;
-  const double t = (double)hp->step;
-  const double bc1 = 1.0 - std::pow(hp->beta1, t), bc2 = 1.0 - std::pow(hp->beta2, t);
-  c->decay = (float)(1.0 - hp->lr * hp->weight_decay);
-  c->beta1 = (float)hp->beta1;
-  c->omb1 = (float)(1.0 - hp->beta1);
-  c->beta2 = (float)hp->beta2;
-  c->omb2 = (float)(1.0 - hp->beta2);
-  c->step_size = (float)(hp->lr / bc1);
-  c->inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bc2));
-  c->eps = (float)hp->eps;
-  return SLOPE_OK;
-}
-
-constexpr int64_t kAdamwMaxElems = int64_t(1) << 40;
 
 // Adapter arguments: both factors with r > 0 (adapter on), or neither with any
 // r >= 0 (adapter off).  One factor without the other, or factors with r == 0,

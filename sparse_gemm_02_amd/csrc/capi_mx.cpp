@@ -1,0 +1,106 @@
+// C ABI of the microscaled operators: argument checks, then kernel launches.  As in
+// capi.cpp every check comes before the first launch.  Declarations and the meaning
+// of every argument: include/slope_mx.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <new>
+#include <utility>
+#include <vector>
+
+#include "../../include/slope.h"
+#include "adamw_args.h"
+#include "launch.h"
+
+using slope::Dt;
+
+namespace {
+
+bool dt_ok(int d) { return d == SLOPE_F32 || d == SLOPE_BF16 || d == SLOPE_F16; }
+int64_t size_of(int d) { return d == SLOPE_F32 ? 4 : 2; }
+slope_status from_hip(hipError_t e) { return e == hipSuccess ? SLOPE_OK : SLOPE_ERR_HIP; }
+
+// A pointer that has to be there (required) and, if there, aligned to `align`.
+slope_status ptr(const void* p, bool required, unsigned align = 16) {
+  if (!p) return required ? SLOPE_ERR_INVALID_ARG : SLOPE_OK;
+  return (reinterpret_cast<uintptr_t>(p) & (align - 1)) ? SLOPE_ERR_ALIGN : SLOPE_OK;
+}
+
+#define SLOPE_TRY(x)                       \
+  do {                                     \
+    slope_status _st = (x);                \
+    if (_st != SLOPE_OK) return _st;       \
+  } while (0)
+
+// Whether two of the byte ranges [first, second) overlap.
+bool overlap(std::vector<std::pair<uintptr_t, uintptr_t>>& r) {
+  std::sort(r.begin(), r.end());
+  for (size_t i = 1; i < r.size(); ++i)
+    if (r[i].first < r[i - 1].second) return true;
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* param_dt, const int32_t* grad_dt,
+                               void* const* params, const void* const* grads, void* const* m, void* const* v,
+                               uint8_t* const* m_exp, uint8_t* const* v_exp, const int64_t* n,
+                               const slope_adamw_params* hp, uint64_t seed, void* stream) {
+  if ((state_bits != 8 && state_bits != 32) || count < 0) return SLOPE_ERR_INVALID_ARG;
+  const bool eight = state_bits == 8;
+  slope::AdamWStep c;
+  SLOPE_TRY(slope::adamw_step(hp, &c));
+  if (count == 0) return SLOPE_OK;
+  if (!param_dt || !grad_dt || !params || !grads || !m || !v || !n || (eight && (!m_exp || !v_exp)))
+    return SLOPE_ERR_INVALID_ARG;
+  try {
+    std::vector<std::pair<uintptr_t, uintptr_t>> written;
+    written.reserve((size_t)count * (eight ? 5 : 3));
+    auto writes = [&](const void* p, int64_t bytes) {
+      written.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes);
+    };
+    for (int64_t i = 0; i < count; ++i) {
+      if (!dt_ok(param_dt[i]) || !dt_ok(grad_dt[i]) || n[i] < 0) return SLOPE_ERR_INVALID_ARG;
+      if (n[i] > slope::kAdamwMaxElems) return SLOPE_ERR_UNSUPPORTED;
+      if (n[i] == 0) continue;
+      const int64_t e = size_of(param_dt[i]);
+      SLOPE_TRY(ptr(params[i], true, (unsigned)e));
+      SLOPE_TRY(ptr(grads[i], true, (unsigned)size_of(grad_dt[i])));
+      SLOPE_TRY(ptr(m[i], true, eight ? 1 : 4));
+      SLOPE_TRY(ptr(v[i], true, eight ? 1 : 4));
+      writes(params[i], n[i] * e);
+      writes(m[i], n[i] * (eight ? 1 : 4));
+      writes(v[i], n[i] * (eight ? 1 : 4));
+      if (eight) {
+        const int64_t blocks = (n[i] + SLOPE_MX_BLOCK - 1) / SLOPE_MX_BLOCK;
+        SLOPE_TRY(ptr(m_exp[i], true, 1));
+        SLOPE_TRY(ptr(v_exp[i], true, 1));
+        writes(m_exp[i], blocks);
+        writes(v_exp[i], blocks);
+      }
+    }
+    if (overlap(written)) return SLOPE_ERR_INVALID_ARG;
+  } catch (const std::bad_alloc&) {
+    return SLOPE_ERR_HIP;
+  }
+  const slope::AdamWTensors t{count, param_dt, grad_dt, params, grads, m, v, m_exp, v_exp, n};
+  return from_hip(slope::launch_adamw_multi(eight, t, c, seed, (hipStream_t)stream));
+}
+
+slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, const uint8_t* m_exp_or_null,
+                                 const uint8_t* v_or_null, const uint8_t* v_exp_or_null, int64_t n,
+                                 void* m_out_or_null, void* v_out_or_null, void* stream) {
+  if (!dt_ok(out_dt) || n < 0) return SLOPE_ERR_INVALID_ARG;
+  const int in_m = !!m_or_null + !!m_exp_or_null + !!m_out_or_null, in_v = !!v_or_null + !!v_exp_or_null + !!v_out_or_null;
+  if (in_m % 3 || in_v % 3 || in_m + in_v == 0) return SLOPE_ERR_INVALID_ARG;
+  SLOPE_TRY(ptr(m_out_or_null, false, (unsigned)size_of(out_dt)));
+  SLOPE_TRY(ptr(v_out_or_null, false, (unsigned)size_of(out_dt)));
+  if (out_dt == SLOPE_F16 || n > slope::kAdamwMaxElems) return SLOPE_ERR_UNSUPPORTED;
+  if (m_out_or_null && m_out_or_null == v_out_or_null && n > 0) return SLOPE_ERR_INVALID_ARG;
+  return from_hip(slope::launch_adamw_moments((Dt)out_dt, m_or_null, m_exp_or_null, v_or_null, v_exp_or_null, n,
+                                              m_out_or_null, v_out_or_null, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -217,4 +217,22 @@ hipError_t launch_spmm_i8(Dt out, const int8_t* Xq, const float* x_scale, int64_
 hipError_t launch_spmm_i8_decode(Dt out, const int8_t* Xq, const float* x_scale, int64_t T, int64_t K,
                                  const void* packed, const float* w_scale, int64_t M, void* Y, hipStream_t s);
 
+// AdamW over `count` tensors (host arrays; types as slope_dtype values), moments in
+// fp32 or in 8 bits (m, v codes, me, ve their blocks' scales); the values of 8-bit moments
+// (mo, vo may be null).
+struct AdamWTensors {
+  int64_t count;
+  const int32_t *param_dt, *grad_dt;
+  void* const* p;
+  const void* const* g;
+  void* const* m;
+  void* const* v;
+  uint8_t* const* me;
+  uint8_t* const* ve;
+  const int64_t* n;
+};
+hipError_t launch_adamw_multi(bool eight, const AdamWTensors& t, const AdamWStep& c, uint64_t seed, hipStream_t s);
+hipError_t launch_adamw_moments(Dt out, const uint8_t* m, const uint8_t* me, const uint8_t* v, const uint8_t* ve,
+                                int64_t n, void* mo, void* vo, hipStream_t s);
+
 }  // namespace slope

@@ -31,7 +31,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import (I8_DECODE_MAX_TOKENS, slope_adamw, slope_adamw_double_prune_packed, slope_double_prune_packed,
+from . import (I8_DECODE_MAX_TOKENS, MX_BLOCK, slope_adamw_double_prune_packed, slope_adamw_moments,
+               slope_adamw_multi, slope_double_prune_packed,
                slope_lowrank_add, slope_lowrank_grads_packed, slope_lowrank_grads_workspace_bytes,
                slope_lowrank_workspace_bytes, slope_masked_wgrad_packed, slope_pack_sparse, slope_pack_sparse_i8,
                slope_pack_tokens, slope_packed_sparse_bytes, slope_packed_sparse_i8_bytes, slope_packed_tokens_bytes,
@@ -173,16 +174,28 @@ class SparseLinear(torch.nn.Module):
 
 
 class SparseAdamW(torch.optim.Optimizer):
-    """AdamW for SparseLinear layers (and any other bf16 / fp32 parameters).
+    """AdamW for SparseLinear layers (and any other bf16 / fp16 / fp32 parameters).
 
-    The compressed values of each layer are updated by the fused kernel that
-    also rewrites them inside W_s's tile chunks and re-derives the
-    double-pruned transposed weight's tile chunks, so both GEMM operands are
-    current after one pass; other parameters (the adapter factors) take the
-    elementwise kernel.  Moments are fp32, two per stored value: the
-    optimizer state of a 2:4 weight is half that of a dense one."""
+    state_bits=32: two fp32 moments per stored value (the optimizer state of a 2:4
+    weight is half that of a dense one).  The compressed values of each layer are
+    updated by the fused kernel that also rewrites them inside W_s's tile chunks
+    and re-derives the double-pruned transposed weight's tile chunks, so both GEMM
+    operands are current after one pass; all other parameters (adapter factors,
+    norm weights) take one launch together.
 
-    def __init__(self, modules, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, extra_params=()):
+    state_bits=8: both moments as 8-bit codes with a scale for each 32 values
+    (slope_adamw_multi; a quarter of the fp32 moments' memory), rounded
+    stochastically with random bits from `seed` and the step; all parameters take
+    one launch together, and the layers' operands are re-derived from the new
+    values.  `moments(p)` gives them as values.
+
+    A step recorded into a graph repeats its step number (and random bits)."""
+
+    def __init__(self, modules, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, extra_params=(),
+                 state_bits=32, seed=0):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        self.state_bits, self.seed = state_bits, seed
         modules = list(modules)
         self._layer_of = {}
         params = []
@@ -200,30 +213,81 @@ class SparseAdamW(torch.optim.Optimizer):
                 uniq.append(p)
         super().__init__(uniq, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
 
+    def _state_of(self, p):
+        st = self.state[p]
+        if not st:
+            st["step"] = 0
+            if self.state_bits == 32:
+                st["exp_avg"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+                st["exp_avg_sq"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+            else:
+                blocks = -(-p.numel() // MX_BLOCK)
+                for name in ("exp_avg", "exp_avg_sq"):
+                    st[name] = torch.zeros(p.shape, dtype=torch.uint8, device=p.device)
+                    st[name + "_exp"] = torch.zeros(blocks, dtype=torch.uint8, device=p.device)
+        return st
+
     @torch.no_grad()
     def step(self, closure=None):
         loss = closure() if closure is not None else None
+        done = 0                                     # lists of this step, each with random bits of its own
         for group in self.param_groups:
             b1, b2 = group["betas"]
             hp = dict(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"], weight_decay=group["weight_decay"])
+            lists = {}                               # by step number and device: parameters without a gradient sit steps out
             for p in group["params"]:
                 if p.grad is None:
                     continue
-                st = self.state[p]
-                if not st:
-                    st["step"] = 0
-                    st["exp_avg"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
-                    st["exp_avg_sq"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+                st = self._state_of(p)
                 st["step"] += 1
                 g = p.grad.contiguous()
                 layer = self._layer_of.get(p)
-                if layer is not None:
+                if layer is not None and self.state_bits == 32:
                     slope_adamw_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_sq"],
                                                     layer.out_features, layer.in_features, layer.packed_s,
                                                     layer.packed_dpT, st["step"], **hp)
                 else:
-                    slope_adamw(p, g, st["exp_avg"], st["exp_avg_sq"], st["step"], **hp)
+                    lists.setdefault((st["step"], p.device), []).append((p, g, st))
+            for (t, _), each in lists.items():
+                ps, gs, sts = zip(*each)
+                take = lambda name: [st[name] for st in sts]
+                eight = {} if self.state_bits == 32 else dict(m_exp=take("exp_avg_exp"), v_exp=take("exp_avg_sq_exp"),
+                                                              seed=(self.seed << 40) + (done << 32) + t)
+                slope_adamw_multi(ps, gs, take("exp_avg"), take("exp_avg_sq"), t, **eight, **hp)
+                done += 1
+                for p in ps:
+                    layer = self._layer_of.get(p)
+                    if layer is not None:
+                        layer.refresh()
         return loss
+
+    @torch.no_grad()
+    def moments(self, p):
+        """(exp_avg, exp_avg_sq) of parameter p as float32 values."""
+        st = self.state[p]
+        if not st:
+            raise ValueError("the parameter has no state yet")
+        m, v = st["exp_avg"], st["exp_avg_sq"]
+        if self.state_bits == 8:
+            values = [torch.empty(p.shape, dtype=torch.float32, device=p.device) for _ in range(2)]
+            slope_adamw_moments(m, st["exp_avg_exp"], v, st["exp_avg_sq_exp"], *values)
+            return tuple(values)
+        return m, v
+
+    def load_state_dict(self, state_dict):
+        """As torch's, with the moments in their own formats (torch's converts a
+        parameter's floating and integer states to the parameter's format)."""
+        saved = state_dict["state"]
+        ids = [i for g in state_dict["param_groups"] for i in g["params"]]
+        want = torch.float32 if self.state_bits == 32 else torch.uint8
+        for i in ids:
+            if i in saved and saved[i] and saved[i]["exp_avg"].dtype is not want:
+                raise ValueError(f"the saved moments are {saved[i]['exp_avg'].dtype}, the optimizer's {want}")
+        super().load_state_dict(state_dict)
+        for p, i in zip((p for g in self.param_groups for p in g["params"]), ids):
+            for k, t in saved.get(i, {}).items():
+                if isinstance(t, torch.Tensor):
+                    self.state[p][k] = t.detach().clone().to(p.device)
 
 
 def training_state_bytes(layer: SparseLinear, optimizer: SparseAdamW | None = None) -> dict:
@@ -232,7 +296,8 @@ def training_state_bytes(layer: SparseLinear, optimizer: SparseAdamW | None = No
     moments).  `canonical` counts what the pages' accounting counts: the
     compressed weight, its double-pruned copy (held only as tile chunks, 1.125
     bytes per weight up to the chunks' padding), the gradient at the kept
-    weights and two moments per kept weight; no separate binary mask is kept
+    weights and two moments per kept weight (fp32, or 8-bit codes with their scales
+    if that is what the optimizer keeps); no separate binary mask is kept
     (the metadata is the mask).  `with_packed_operands` adds W_s's tile-chunk
     copy, the forward's operand."""
     def nb(t):
@@ -241,7 +306,9 @@ def training_state_bytes(layer: SparseLinear, optimizer: SparseAdamW | None = No
     vals = layer.values
     grad = vals.numel() * vals.element_size()
     if optimizer is not None and vals in optimizer.state and optimizer.state[vals]:
-        moments = nb(optimizer.state[vals]["exp_avg"]) + nb(optimizer.state[vals]["exp_avg_sq"])
+        moments = sum(nb(t) for t in optimizer.state[vals].values() if isinstance(t, torch.Tensor))
+    elif optimizer is not None and optimizer.state_bits == 8:
+        moments = 2 * (vals.numel() + -(-vals.numel() // MX_BLOCK))
     else:
         moments = 2 * 4 * vals.numel()
     canonical = nb(vals) + nb(layer.meta) + nb(layer.packed_dpT) + grad + moments

@@ -1,0 +1,126 @@
+"""The C ABI of the microscaled operators: it exports what include/slope_mx.h
+declares and refuses bad arguments on the host, before the GPU is touched."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import sparse_gemm_02_amd as S
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 1 << 20  # aligned, never dereferenced: every call below fails its checks first
+F32, BF16, F16 = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(S.library_path):
+        from sparse_gemm_02_amd.build import build
+        build()
+    return S.library()
+
+
+def test_exports_every_declared_symbol(lib):
+    txt = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "slope_mx.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(slope_[a-z0-9_]+)\s*\(", txt))
+    assert names == set(S.EXPORTED_SYMBOLS_MX)
+    assert not names & (set(S.EXPORTED_SYMBOLS) | set(S.EXPORTED_SYMBOLS_INT8))
+    for n in names:
+        assert hasattr(lib, n) and callable(getattr(S, n)) and n in S.__all__
+
+
+def _multi(lib, bits=8, count=2, pdt=(BF16, F32), gdt=(BF16, F32), p=(FAKE, 2 * FAKE), g=(3 * FAKE, 4 * FAKE),
+           m=(5 * FAKE, 6 * FAKE), v=(7 * FAKE, 8 * FAKE), me=(9 * FAKE, 10 * FAKE), ve=(11 * FAKE, 12 * FAKE),
+           n=(64, 65), hp=(1e-3, 0.9, 0.999, 1e-8, 0.01, 1)):
+    vp = lambda a: None if a is None else (ctypes.c_void_p * len(a))(*a)
+    i32 = lambda a: None if a is None else (ctypes.c_int32 * len(a))(*a)
+    h = None if hp is None else ctypes.byref(S.AdamWParams(*hp))
+    return lib.slope_adamw_multi(bits, count, i32(pdt), i32(gdt), vp(p), vp(g), vp(m), vp(v), vp(me), vp(ve),
+                                 None if n is None else (ctypes.c_int64 * len(n))(*n), h, 0, None)
+
+
+def test_adamw_multi_refusals(lib):
+    f = lambda **k: _multi(lib, **k)
+    for bits in (0, 4, 16, 64, -8):
+        assert f(bits=bits) == -1
+    assert f(count=-1) == -1 and f(hp=None) == -1
+    for k in ("pdt", "gdt", "p", "g", "m", "v", "n"):
+        assert f(**{k: None}) == -1, k
+    assert f(me=None) == -1 and f(ve=None) == -1
+    assert f(pdt=(BF16, 3)) == -1 and f(gdt=(-1, BF16)) == -1 and f(n=(64, -1)) == -1
+    for k in ("p", "g", "m", "v", "me", "ve"):
+        assert f(**{k: (FAKE * 20, 0)}) == -1, k                     # a tensor that is not there
+    for hp in [(1e-3, 0.9, 0.999, 1e-8, 0.01, 0), (1e-3, 1.0, 0.999, 1e-8, 0.01, 1), (1e-3, 0.9, -0.1, 1e-8, 0.01, 1),
+               (1e-3, 0.9, 0.999, -1.0, 0.01, 1), (float("nan"), 0.9, 0.999, 1e-8, 0.01, 1),
+               (1e-3, 0.9, 0.999, 1e-8, float("inf"), 1)]:
+        assert f(hp=hp) == -1, hp
+    # addresses: an element's alignment is enough, less is not
+    assert f(p=(FAKE + 1, 2 * FAKE)) == -3 and f(p=(FAKE, 2 * FAKE + 2)) == -3 and f(g=(3 * FAKE + 1, 4 * FAKE)) == -3
+    assert f(bits=32, m=(5 * FAKE + 2, 6 * FAKE)) == -3 and f(bits=32, v=(7 * FAKE, 8 * FAKE + 1)) == -3
+    assert f(n=(64, (1 << 40) + 1)) == -6
+
+
+def test_adamw_multi_refuses_tensors_that_share_memory(lib):
+    f = lambda **k: _multi(lib, **k)
+    assert f(p=(FAKE, FAKE), pdt=(BF16, BF16)) == -1                 # the same weight twice
+    assert f(p=(FAKE, FAKE + 126), pdt=(BF16, BF16)) == -1           # its last value
+    assert f(m=(5 * FAKE, 5 * FAKE + 63)) == -1 and f(v=(7 * FAKE, 5 * FAKE)) == -1
+    assert f(me=(9 * FAKE, 9 * FAKE + 1)) == -1 and f(ve=(9 * FAKE, 12 * FAKE)) == -1
+    assert f(bits=32, m=(5 * FAKE, 5 * FAKE + 252)) == -1
+    assert f(m=(FAKE, 6 * FAKE)) == -1                               # a moment over a weight
+
+
+def test_adamw_moments_refusals(lib):
+    f = lambda dt=BF16, m=FAKE, me=2 * FAKE, v=3 * FAKE, ve=4 * FAKE, n=64, mo=5 * FAKE, vo=6 * FAKE: \
+        lib.slope_adamw_moments(dt, m, me, v, ve, n, mo, vo, None)
+    assert f(dt=3) == -1 and f(n=-1) == -1 and f(mo=7 * FAKE, vo=7 * FAKE) == -1
+    for k in ("m", "me", "mo", "v", "ve", "vo"):
+        assert f(**{k: None}) == -1, k
+    assert f(m=None, me=None, mo=None, v=None, ve=None, vo=None) == -1
+    assert f(mo=5 * FAKE + 1) == -3 and f(dt=F32, vo=6 * FAKE + 2) == -3
+    assert f(dt=F16) == -6 and f(n=(1 << 40) + 1) == -6
+
+
+def test_binding_checks_lists():
+    """The Python calls refuse lists that do not fit before anything reaches the library."""
+    bf, u8 = torch.bfloat16, torch.uint8
+    p = [torch.zeros(40, dtype=bf), torch.zeros(3, 5)]
+    g = [torch.zeros(40), torch.zeros(3, 5, dtype=torch.float16)]
+    m32 = [torch.zeros(40), torch.zeros(3, 5)]
+    v32 = [torch.zeros(40), torch.zeros(3, 5)]
+    m8 = [torch.zeros(40, dtype=u8), torch.zeros(3, 5, dtype=u8)]
+    v8 = [torch.zeros(40, dtype=u8), torch.zeros(3, 5, dtype=u8)]
+    e = [torch.zeros(2, dtype=u8), torch.zeros(1, dtype=u8)]
+    step = dict(step=1, lr=1e-3)
+    with pytest.raises(ValueError, match="GPU memory"):
+        S.slope_adamw_multi(p, g, m32, v32, **step)
+    with pytest.raises(ValueError, match="GPU memory"):
+        S.slope_adamw_multi(p, g, m8, v8, m_exp=e, v_exp=e, **step)
+    for lists in ((p, g[:1], m32, v32), (p, g, m32[:1], v32), (p[:1], g, m32, v32), ([], g, m32, v32)):
+        with pytest.raises(ValueError, match="same length"):
+            S.slope_adamw_multi(*lists, **step)
+    with pytest.raises(ValueError, match="both m_exp and v_exp"):
+        S.slope_adamw_multi(p, g, m8, v8, m_exp=e, **step)
+    with pytest.raises(ValueError, match="same length"):
+        S.slope_adamw_multi(p, g, m8, v8, m_exp=e, v_exp=e[:1], **step)
+    with pytest.raises(TypeError, match=r"m\[0\] must be torch.float32"):
+        S.slope_adamw_multi(p, g, m8, v32, **step)
+    with pytest.raises(TypeError, match=r"v\[1\] must be torch.uint8"):
+        S.slope_adamw_multi(p, g, m8, [v8[0], v32[1]], m_exp=e, v_exp=e, **step)
+    with pytest.raises(ValueError, match=r"grads\[1\] must have 15 elements, got 14"):
+        S.slope_adamw_multi(p, [g[0], g[1].view(-1)[:14]], m32, v32, **step)
+    with pytest.raises(ValueError, match=r"m_exp\[0\] must have 2 elements, got 1"):
+        S.slope_adamw_multi(p, g, m8, v8, m_exp=[e[1], e[1]], v_exp=e, **step)
+    with pytest.raises(ValueError, match=r"params\[1\] must be contiguous"):
+        S.slope_adamw_multi([p[0], torch.zeros(5, 3).t()], g, m32, v32, **step)
+    with pytest.raises(TypeError, match="expected bfloat16"):
+        S.slope_adamw_multi([p[0], torch.zeros(3, 5, dtype=torch.float64)], g, m32, v32, **step)
+    S.slope_adamw_multi([], [], [], [], **step)                      # no tensors: nothing to do
+    with pytest.raises(ValueError, match="one moment"):
+        S.slope_adamw_moments(None, None, None, None)
+    with pytest.raises(ValueError, match="m_exp must have shape"):
+        S.slope_adamw_moments(m8[0], e[1], None, None, torch.zeros(40))
+    with pytest.raises(ValueError, match="GPU memory"):
+        S.slope_adamw_moments(m8[0], e[0], None, None, torch.zeros(40))

@@ -1,0 +1,431 @@
+"""GPU parity of the AdamW step over many tensors.
+
+32-bit moments: the results of slope_adamw on each tensor, bit for bit.  8-bit
+moments: the float32 moments are determined numbers (fixed operations), scaling
+by a power of two rounds nothing and the random bits are part of the definition, so
+codes and scales are compared with the oracle's bit for bit; the weights within the
+bound of the elementwise step (gpu_util.check_adamw_update)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import sparse_gemm_02_amd as S
+from sparse_gemm_02_amd.layer import ResidualRMSNorm, SparseAdamW, SparseLinear, training_state_bytes
+from workloads import layer_inputs
+
+from gpu_util import check_adamw_update, dev, host, say
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+HP = dict(lr=2e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
+U8 = torch.uint8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    S.library()
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+def blocks(n):
+    return -(-n // 32)
+
+
+class Lists:
+    """Lists of tensors in mid-training, each cut from a larger buffer at `shift`
+    elements past an aligned address, with guard values around it."""
+
+    def __init__(self, sizes, dts, gdts, seed, eight, shift=0):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.buffers, self.eight = [], eight
+        self.p, self.g, self.m, self.v, self.me, self.ve = [], [], [], [], [], []
+        for n, dt, gdt in zip(sizes, dts, gdts):
+            r = lambda sigma: torch.randn(n, device="cuda", generator=gen) * sigma
+            self.p.append(self._cut(r(0.02).to(DT[dt]), shift))
+            self.g.append(self._cut((r(1.0) * torch.exp(r(2.0))).to(DT[gdt]), shift))
+            if eight:
+                for codes, exps, top in ((self.m, self.me, 0x7F), (self.v, self.ve, 0xF9)):
+                    c = torch.randint(0, top, (n,), device="cuda", generator=gen).to(U8)
+                    if codes is self.m:
+                        c |= (torch.rand(n, device="cuda", generator=gen) < 0.5).to(U8) << 7
+                    codes.append(self._cut(c, shift))
+                    exps.append(self._cut(torch.randint(100, 125, (blocks(n),), device="cuda", generator=gen).to(U8), shift))
+            else:
+                self.m.append(self._cut(r(0.05), shift))
+                self.v.append(self._cut((r(0.1)).square(), shift))
+
+    def _cut(self, t, shift):
+        raw = torch.full((t.numel() + shift + 16,), 0x5A, dtype=U8, device="cuda").repeat(t.element_size()).view(t.dtype)
+        raw[shift:shift + t.numel()] = t
+        self.buffers.append((raw, shift, t.numel()))
+        return raw[shift:shift + t.numel()]
+
+    def guards_whole(self):
+        for raw, shift, n in self.buffers:
+            rest = torch.cat([raw[:shift], raw[shift + n:]]).view(U8)
+            assert (rest == 0x5A).all()
+
+    def bits(self):
+        return [[host(t).copy() if t.dtype != torch.float32 else t.cpu().numpy() for t in x]
+                for x in (self.p, self.g, self.m, self.v, self.me, self.ve)]
+
+    def call(self, step, seed=0, **kw):
+        eight = dict(m_exp=self.me, v_exp=self.ve, seed=seed) if self.eight else {}
+        S.slope_adamw_multi(self.p, self.g, self.m, self.v, step, **eight, **{**HP, **kw})
+
+
+COMBOS = [(p, g) for p in DT for g in DT]
+SIZES = [1, 7, 8, 31, 32, 33, 255, 2048, 2049, 100003]
+
+
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_32_bit_moments_are_slope_adamw_bit_for_bit(shift):
+    sizes = [n for n in SIZES for _ in COMBOS]
+    dts, gdts = zip(*(COMBOS * len(SIZES)))
+    a, b = Lists(sizes, dts, gdts, 1, False, shift), Lists(sizes, dts, gdts, 1, False)
+    for step in (1, 2, 7):
+        a.call(step)
+        for p, g, m, v in zip(b.p, b.g, b.m, b.v):
+            S.slope_adamw(p.contiguous(), g, m, v, step, **HP)
+    torch.cuda.synchronize()
+    for x, y in zip((a.p, a.m, a.v, a.g), (b.p, b.m, b.v, b.g)):
+        for s, t in zip(x, y):
+            assert torch.equal(s, t)
+    a.guards_whole()
+
+
+def check_8(before, after, i, dt, step, seed, hp=HP):
+    """Tensor i of a list after one step, against the oracle."""
+    (p0, g, m0, v0, me0, ve0), (p1, _, m1, v1, me1, ve1) = before, after
+    gw = oracle.widen(g[i]) if g[i].dtype != np.float32 else g[i].astype(np.float64)
+    cm, em, cv, ev, mf, vf = oracle.adamw8(gw, m0[i], me0[i], v0[i], ve0[i], hp["beta1"], hp["beta2"],
+                                           oracle.tensor_seed(seed, i))
+    assert np.array_equal(m1[i], cm) and np.array_equal(me1[i], em)
+    assert np.array_equal(v1[i], cv) and np.array_equal(ve1[i], ev)
+    if not p0[i].size:
+        return
+    md, vd = oracle.moments8(m0[i], me0[i], v0[i], ve0[i])
+    enc = lambda a: a.view(np.uint32) if a.dtype == np.float32 else a
+    check_adamw_update(enc(p0[i]), enc(g[i]), md, vd, step, hp, enc(p1[i]), mf.astype(np.float32), vf.astype(np.float32))
+
+
+@pytest.mark.parametrize("shift", [0, 1, 5])
+def test_8_bit_moments_against_the_oracle(shift):
+    sizes = [n for n in SIZES for _ in COMBOS]
+    dts, gdts = zip(*(COMBOS * len(SIZES)))
+    a = Lists(sizes, dts, gdts, 2, True, shift)
+    for step, seed in ((1, 11), (2, 12), (3, (1 << 64) - 1)):
+        before = a.bits()
+        a.call(step, seed=seed)
+        torch.cuda.synchronize()
+        after = a.bits()
+        for i in range(len(sizes)):
+            check_8(before, after, i, dts[i], step, seed)
+    a.guards_whole()
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_many_tensors_take_several_launches(eight):
+    sizes = [(37 * i) % 3001 for i in range(200)]                    # some of no values among them
+    say(f"[adamw_multi] {len(sizes)} tensors, {'8' if eight else '32'} bits")
+    a = Lists(sizes, ["bf16"] * 200, ["bf16"] * 200, 3, eight)
+    before = a.bits()
+    a.call(4, seed=5)
+    torch.cuda.synchronize()
+    after = a.bits()
+    if eight:
+        for i in range(200):
+            check_8(before, after, i, "bf16", 4, 5)
+    else:
+        b = Lists(sizes, ["bf16"] * 200, ["bf16"] * 200, 3, False)
+        for p, g, m, v in zip(b.p, b.g, b.m, b.v):
+            S.slope_adamw(p, g, m, v, 4, **HP)
+        assert all(torch.equal(s, t) for x, y in zip((a.p, a.m, a.v), (b.p, b.m, b.v)) for s, t in zip(x, y))
+    a.guards_whole()
+
+
+def test_large_lists_take_several_slices_a_block():
+    n = (1 << 24) + 5                                                # four slices a block from 2^24 values on
+    a = Lists([n, 3000], ["bf16", "bf16"], ["bf16", "bf16"], 4, True)
+    before = a.bits()
+    a.call(2, seed=77)
+    torch.cuda.synchronize()
+    after = a.bits()
+    for i in (0, 1):
+        check_8(before, after, i, "bf16", 2, 77)
+
+
+def test_a_tensor_past_32_bits_of_offset():
+    n = (1 << 31) + 4133
+    say(f"[adamw_multi] n={n}")
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    m, v = (torch.zeros(n, dtype=U8, device="cuda") for _ in range(2))
+    me, ve = (torch.zeros(blocks(n), dtype=U8, device="cuda") for _ in range(2))
+    tail = 8192 + 4133
+    at = n - tail                                                    # a multiple of 32: 2^31 - 8192
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    g[at:] = torch.randn(tail, device="cuda", generator=gen).bfloat16()
+    p[at:] = torch.randn(tail, device="cuda", generator=gen).bfloat16()
+    p0, g0 = host(p[at:]).copy(), host(g[at:]).copy()
+    S.slope_adamw_multi([p], [g], [m], [v], 1, m_exp=[me], v_exp=[ve], seed=9, **HP)
+    torch.cuda.synchronize()
+    z, ze = np.zeros(tail, np.uint8), np.zeros(blocks(tail), np.uint8)
+    cm, em, cv, ev, mf, vf = oracle.adamw8(oracle.widen(g0), z, ze, z, ze, 0.9, 0.999, oracle.tensor_seed(9, 0), first=at)
+    for got, want in ((m[at:], cm), (me[at // 32:], em), (v[at:], cv), (ve[at // 32:], ev)):
+        assert np.array_equal(got.cpu().numpy(), want)
+    check_adamw_update(p0, g0, np.zeros(tail, np.float32), np.zeros(tail, np.float32), 1, HP, host(p[at:]),
+                       mf.astype(np.float32), vf.astype(np.float32))
+    assert not m[:at].any() and not p[:at].any() and not v[:at].any()
+    mo, vo = (torch.empty(n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    S.slope_adamw_moments(m, me, v, ve, mo, vo)
+    md, vd = oracle.moments8(cm, em, cv, ev)
+    assert np.array_equal(mo[at:].double().cpu().numpy(), md) and np.array_equal(vo[at:].double().cpu().numpy(), vd)
+
+
+def test_special_values_stay_in_their_block():
+    n = 256
+    a = Lists([n], ["f32"], ["f32"], 6, True)
+    a.m[0].zero_(), a.v[0].zero_(), a.me[0].zero_(), a.ve[0].zero_()
+    g = a.g[0]
+    g.fill_(1e-3)
+    g[3] = float("nan")              # block 0
+    g[40] = float("inf")             # block 1
+    g[70] = 1e25                     # block 2: its square passes float32
+    g[96:128] = 0.0                  # block 3: nothing at all
+    g[128:160] = 1e-30               # block 4: squares below float32's smallest number
+    g[160:192] = 1e-12               # block 5: one large value, the others' v at the least code
+    g[160] = 10.0
+    before = a.bits()
+    a.call(1, seed=1)
+    torch.cuda.synchronize()
+    after = a.bits()
+    me, ve = after[4][0], after[5][0]
+    assert list(me[:3]) == [255, 255, me[2]] and list(ve[:3]) == [255, 255, 255] and me[2] != 255
+    assert me[3] == 0 and ve[3] == 0 and not after[2][0][96:128].any()
+    gw = before[1][0].astype(np.float64)
+    cm, em, cv, ev, mf, vf = oracle.adamw8(gw, before[2][0], before[4][0], before[3][0], before[5][0], 0.9, 0.999,
+                                           oracle.tensor_seed(1, 0))
+    for got, want in zip((after[2][0], me, after[3][0], ve), (cm, em, cv, ev)):
+        assert np.array_equal(got, want)
+    assert np.all(after[3][0][161:192] == 1)                         # positive, so not zero
+    p = after[0][0]
+    assert np.isnan(p[3]) and np.isnan(p[40]) and np.isfinite(np.delete(p, [3, 40])).all()
+    # the next step: everything in the blocks without values is NaN, nothing else
+    g.fill_(1e-3)
+    a.call(2, seed=2)
+    torch.cuda.synchronize()
+    nan = np.isnan(a.p[0].cpu().numpy())
+    assert nan[:96].all() and not nan[96:].any()
+    assert list(a.me[0][:2].cpu()) == [255, 255] and list(a.ve[0][:3].cpu()) == [255] * 3
+
+
+def test_all_codes_and_scales_as_values():
+    codes = torch.arange(256, dtype=torch.int16).to(U8).repeat(256)
+    exps = torch.arange(256, dtype=torch.int16).to(U8).repeat_interleave(8)
+    m, e = codes.cuda(), exps.cuda()
+    md, vd = oracle.moments8(codes.numpy(), exps.numpy(), codes.numpy(), exps.numpy())
+    # both formats hold every value (the smallest ones as subnormals down to bfloat16's 2^-133 and float32's 2^-149)
+    for dt, least in ((torch.float32, -149), (torch.bfloat16, -133)):
+        mo, vo = torch.empty(m.shape, dtype=dt, device="cuda"), torch.empty(m.shape, dtype=dt, device="cuda")
+        S.slope_adamw_moments(m, e, m, e, mo, vo)
+        for got, want in ((mo, md), (vo, vd)):
+            got = got.double().cpu().numpy()
+            with np.errstate(invalid="ignore"):
+                whole = np.isnan(want) | (np.ldexp(want, -least) == np.rint(np.ldexp(want, -least)))
+                over = np.abs(want) >= 2.0 ** 128                    # v's upper codes at the largest scales
+            assert np.array_equal(got[whole & ~over], want[whole & ~over], equal_nan=True)
+            assert np.all(np.isinf(got[over])) and np.all(np.abs(got[~whole] - want[~whole]) <= 2.0 ** (least - 1))
+        # one moment alone, other sizes
+        for n in (1, 33, 2049):
+            o = torch.full((n,), 7.0, dtype=dt, device="cuda")
+            S.slope_adamw_moments(None, None, m[:n], e[:blocks(n)], None, o)
+            assert torch.equal(o.isnan(), vo[:n].isnan()) and torch.equal(o.nan_to_num(), vo[:n].nan_to_num())
+
+
+def test_the_second_moment_follows_the_exact_average():
+    """200 steps with beta2 = 0.999: rounding to nearest would leave v where its steps fall
+    below half a code.  A step rounds up or down by less than one code, an eighth of its
+    binade's power of two, so by less than v / 8 with a variance of at most (v / 8)^2 / 4;
+    200 of them add up to a variance of at most 200 v^2 / 256 (v the largest on the
+    way), over 2^20 values to a mean within 5 sqrt(200 / 256) 2^-10 = 0.0044 of it."""
+    n = 1 << 20
+    a = Lists([n], ["f32"], ["f32"], 7, True)
+    for t in (a.m[0], a.v[0], a.me[0], a.ve[0]):
+        t.zero_()
+    a.g[0].fill_(0.5)
+    for step in range(1, 201):
+        a.call(step, seed=1000 + step, lr=0.0)
+    m, v = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    S.slope_adamw_moments(a.m[0], a.me[0], a.v[0], a.ve[0], m, v)
+    exact = 0.25 * (1 - 0.999 ** 200)
+    assert abs(v.double().mean().item() / exact - 1) < 0.0044
+    assert abs(m.double().mean().item() / 0.5 - 1) < 0.0044
+
+
+def test_equal_arguments_give_equal_results_and_seeds_matter():
+    make = lambda: Lists([5000, 5000], ["bf16"] * 2, ["bf16"] * 2, 8, True)
+    a, b, c = make(), make(), make()
+    a.call(3, seed=4)
+    b.call(3, seed=4)
+    c.call(3, seed=5)
+    assert all(torch.equal(x, y) for s, t in zip((a.p, a.m, a.v, a.me, a.ve), (b.p, b.m, b.v, b.me, b.ve))
+               for x, y in zip(s, t))
+    assert torch.equal(a.p[0], c.p[0]) and not torch.equal(a.m[0], c.m[0]) and not torch.equal(a.v[0], c.v[0])
+
+
+def test_another_stream_and_a_captured_call():
+    a, b = (Lists([4097, 100], ["bf16", "f32"], ["bf16", "f32"], 9, True) for _ in range(2))
+    start = [t.clone() for x in (a.p, a.m, a.v, a.me, a.ve) for t in x]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a.call(1, seed=3)
+    side.synchronize()
+    b.call(1, seed=3)
+    torch.cuda.synchronize()
+    after = [t.clone() for x in (b.p, b.m, b.v, b.me, b.ve) for t in x]
+    tensors = [t for x in (a.p, a.m, a.v, a.me, a.ve) for t in x]
+    assert all(torch.equal(s, t) for s, t in zip(tensors, after))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.call(1, seed=3)
+    for _ in range(3):                                               # the captured call on the same state: the same result
+        for t, s in zip(tensors, start):
+            t.copy_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(s, t) for s, t in zip(tensors, after))
+        torch.zeros(1 << 20, device="cuda").add_(1)
+
+
+# ------------------------------------------------------------------ the optimizer
+
+def _layers(seed):
+    d = layer_inputs(256, 512, 64, 8, "bf16", seed=seed)
+    layer = SparseLinear(dev(d["W"]), dev(d["L"]), dev(d["R"]))
+    norm = ResidualRMSNorm(256, dtype=torch.float32)
+    return d, layer, norm
+
+
+def test_optimizer_with_32_bits_keeps_its_results():
+    """All parameters but the layers' values take one launch: results of slope_adamw on each."""
+    d, layer, norm = _layers(31)
+    opt = SparseAdamW([layer, norm], lr=1e-2)
+    ref = {p: (p.detach().clone(), torch.zeros(p.shape, device="cuda"), torch.zeros(p.shape, device="cuda"))
+           for p in (layer.L, layer.R, norm.weight)}
+    for step in (1, 2):
+        for p in (layer.values, layer.L, layer.R, norm.weight):
+            p.grad = torch.randn(p.shape, device="cuda").to(p.dtype)
+        opt.step()
+        for p, (w, m, v) in ref.items():
+            S.slope_adamw(w, p.grad, m, v, step, lr=1e-2, weight_decay=0.01)
+            assert torch.equal(w, p.detach()) and torch.equal(opt.state[p]["exp_avg"], m)
+            assert torch.equal(opt.moments(p)[1], v)
+
+
+def test_optimizer_with_8_bits_trains_a_layer():
+    d, layer, norm = _layers(32)
+    opt = SparseAdamW([layer, norm], lr=1e-2, state_bits=8, seed=6)
+    x = dev(d["X"]).clone().requires_grad_(True)
+    params = [layer.values, layer.L, layer.R, norm.weight]
+    order = [p for g in opt.param_groups for p in g["params"]]
+    for step in (1, 2, 3):
+        y = layer(norm(x))
+        y.backward(dev(d["dY"]))
+        skip = norm.weight if step == 2 else None                    # a parameter without a gradient sits the step out
+        if skip is not None:
+            kept, skip.grad = skip.detach().clone(), None
+        before = {p: (host(p).copy(), None if p.grad is None else host(p.grad).copy(),
+                      [opt.state[p][k].cpu().numpy().reshape(-1) for k in
+                       ("exp_avg", "exp_avg_exp", "exp_avg_sq", "exp_avg_sq_exp")] if opt.state[p] else None)
+                  for p in params}
+        opt.step()
+        torch.cuda.synchronize()
+        if skip is not None:
+            assert torch.equal(skip.detach(), kept)
+        # one list for each step number: the norm's own number lags by one after it sat out
+        for p in params:
+            p0, g, st = before[p]
+            if g is None:
+                continue
+            t = opt.state[p]["step"]
+            lists = [[q for q in order if before[q][1] is not None and opt.state[q]["step"] == k]
+                     for k in dict.fromkeys(opt.state[q]["step"] for q in order if before[q][1] is not None)]
+            which = next(i for i, l in enumerate(lists) if any(q is p for q in l))
+            place = next(i for i, q in enumerate(lists[which]) if q is p)
+            n = p.numel()
+            z, ze = np.zeros(n, np.uint8), np.zeros(blocks(n), np.uint8)
+            m0, me0, v0, ve0 = st if st is not None else (z, ze, z, ze)
+            want = oracle.adamw8(oracle.widen(g).reshape(-1), m0, me0, v0, ve0, 0.9, 0.999,
+                                 oracle.tensor_seed((6 << 40) + (which << 32) + t, place))
+            got = [opt.state[p][k].cpu().numpy().reshape(-1) for k in
+                   ("exp_avg", "exp_avg_exp", "exp_avg_sq", "exp_avg_sq_exp")]
+            for a, b in zip(got, want):
+                assert np.array_equal(a, b)
+            mv = oracle.moments8(got[0], got[1], got[2], got[3])
+            for a, b in zip(opt.moments(p), mv):
+                assert np.array_equal(a.double().cpu().numpy().reshape(-1), b)
+        # both GEMM operands follow the new values
+        want_s, want_dp = torch.empty_like(layer.packed_s), torch.empty_like(layer.packed_dpT)
+        S.slope_pack_sparse(layer.values.detach(), layer.meta, 512, 256, want_s)
+        S.slope_double_prune_packed(layer.values.detach(), layer.meta, 512, 256, want_dp)
+        assert torch.equal(layer.packed_s, want_s) and torch.equal(layer.packed_dpT, want_dp)
+        for p in params:
+            p.grad = None
+        x.grad = None
+    acc, full = training_state_bytes(layer, opt), training_state_bytes(layer)
+    n = layer.values.numel()
+    assert full["canonical"] - acc["canonical"] == 8 * n - 2 * (n + n // 32)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_optimizer_state_survives_a_checkpoint(bits, tmp_path):
+    d, layer, norm = _layers(33)
+    opt = SparseAdamW([layer, norm], lr=1e-2, state_bits=bits)
+    params = [layer.values, layer.L, layer.R, norm.weight]
+    grads = [[torch.randn(p.shape, device="cuda").to(p.dtype) for p in params] for _ in range(2)]
+
+    def run(o, gs):
+        for p, g in zip(params, gs):
+            p.grad = g
+        o.step()
+
+    run(opt, grads[0])
+    torch.save(opt.state_dict(), tmp_path / "opt.pt")
+    kept = [p.detach().clone() for p in params]
+    run(opt, grads[1])
+    want = [p.detach().clone() for p in params]
+    with torch.no_grad():
+        for p, k in zip(params, kept):
+            p.copy_(k)
+    layer.refresh()
+    again = SparseAdamW([layer, norm], lr=1e-2, state_bits=bits)
+    again.load_state_dict(torch.load(tmp_path / "opt.pt", weights_only=True))
+    run(again, grads[1])
+    for p, w in zip(params, want):
+        assert torch.equal(p.detach(), w)
+        for a, b in zip(again.moments(p), opt.moments(p)):
+            assert torch.equal(a, b)
+    other = SparseAdamW([layer, norm], lr=1e-2, state_bits=40 - bits)
+    with pytest.raises(ValueError, match="moments are"):
+        other.load_state_dict(torch.load(tmp_path / "opt.pt", weights_only=True))
+
+
+def test_refusals_on_the_gpu():
+    with pytest.raises(ValueError, match="state_bits"):
+        SparseAdamW([], extra_params=[torch.nn.Parameter(torch.zeros(3, device="cuda"))], state_bits=16)
+    p = torch.zeros(64, device="cuda")
+    m, v = torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
+    with pytest.raises(S.SlopeError, match="INVALID_ARG"):
+        S.slope_adamw_multi([p, p], [p, p], [m, m.clone()], [v, v.clone()], 1, lr=1e-3)
+    with pytest.raises(ValueError, match="is on the CPU"):
+        S.slope_adamw_multi([p], [p.cpu()], [m], [v], 1, lr=1e-3)
+    opt = SparseAdamW([], extra_params=[torch.nn.Parameter(p)])
+    with pytest.raises(ValueError, match="no state"):
+        opt.moments(opt.param_groups[0]["params"][0])
