@@ -72,6 +72,73 @@ slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, c
                                  const uint8_t* v_or_null, const uint8_t* v_exp_or_null, int64_t n,
                                  void* m_out_or_null, void* v_out_or_null, void* stream);
 
+/* Largest reduction width of the 4-bit product. */
+#define SLOPE_MXFP4_MAX_COLS (1 << 21)
+
+/* 4-bit floating point with a scale for 32 values.  Of each 32 consecutive values x of
+ * a row (the last block filled up with zeros):
+ *   scale  2^E, E = max(-127, e - 2), e the exponent of the largest magnitude rounded to
+ *          two significant bits (ties away from zero)
+ *   code   the E2M1 number (sign, 2 exponent bits with bias 1, 1 mantissa bit:
+ *          magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6) nearest to x 2^-E, ties to the even
+ *          code, beyond 6 the code of 6
+ * and with an infinity or a NaN in the block its scale is 255 and its codes are 0.
+ *
+ * Rows of codes: a row of K values is filled up with zero blocks (codes 0, scale 0) to
+ * a multiple of 128 values and takes 64 ceil(K / 128) bytes of codes, 16 for each block,
+ * and 4 ceil(K / 128) bytes of scales.  Within a block value 4g + p is nibble g of the
+ * p-th 32-bit word (g = 0..7, p = 0..3). */
+
+/* Bytes of codes and of scales of one row of K values.  Host-only. */
+slope_status slope_mxfp4_row_bytes(int64_t K, int64_t* code_bytes, int64_t* scale_bytes);
+
+/* Codes and scales of the rows of X [T, K] (BF16, F16 or F32; any K): codes
+ * [T, code_bytes], exps [T, scale_bytes], both overwritten whole.  X needs its element's
+ * alignment, codes 16 bytes, exps 4.  K = 0 or T = 0 does nothing. */
+slope_status slope_quantize_mxfp4(slope_dtype dt, const void* X, int64_t T, int64_t K, uint8_t* codes, uint8_t* exps,
+                                  void* stream);
+
+/* out [T, K] out_dt <- the values that rows of codes stand for (NaN where the scale is
+ * 255).  BF16 and F32 hold them exactly (bfloat16 but for values below 2^-133), F16
+ * rounds to its own range.  out needs its element's alignment. */
+slope_status slope_mxfp4_values(slope_dtype out_dt, const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K,
+                                void* out, void* stream);
+
+/* Bytes of the 4-bit tile-chunk form of a compressed [rows, cols] matrix (see
+ * slope_pack_sparse_mxfp4).  Host-only; SLOPE_ERR_SHAPE if cols % 16 != 0,
+ * SLOPE_ERR_UNSUPPORTED if cols > SLOPE_MXFP4_MAX_COLS. */
+slope_status slope_packed_sparse_mxfp4_bytes(int64_t rows, int64_t cols, int64_t* bytes);
+
+/* 4-bit tile chunks of a compressed 16-bit 2:4 matrix (values [rows, cols/2], meta
+ * [rows, ceil(cols/32)] as slope_compress24 or slope_double_prune write them): 3.25 bits
+ * for a dense value.  A block is 32 dense columns, its 16 kept values coded as above.
+ * Chunk (t, s) holds rows 64t .. 64t+63 and dense columns 128s .. 128s+127 (four blocks a
+ * row), 3328 bytes at offset (t * ceil(cols/128) + s) * 3328:
+ *   codes      block b of row r at ((b / 2) * 64 + r) * 16 + (b % 2) * 8: two words, the
+ *              first and the second kept code of its groups of four, nibble g for group g
+ *   positions  at 2048 + ((b / 2) * 64 + r) * 8 + (b % 2) * 4: a word whose nibble g has
+ *              the bits of group g's kept positions
+ *   scales     at 3072 + r * 4 + b: one byte
+ * Rows past `rows` and columns past `cols` have codes and scales 0.  packed: caller-owned,
+ * at least slope_packed_sparse_mxfp4_bytes(rows, cols) bytes, overwritten.  Errors:
+ * SLOPE_ERR_UNSUPPORTED for F32 or cols > SLOPE_MXFP4_MAX_COLS, SLOPE_ERR_SHAPE if cols %
+ * 16 != 0, SLOPE_ERR_WORKSPACE if packed is short. */
+slope_status slope_pack_sparse_mxfp4(slope_dtype dt, const void* values, const uint32_t* meta, int64_t rows,
+                                     int64_t cols, void* packed, int64_t packed_bytes, void* stream);
+
+/* The 2:4 sparse product on 4-bit floating point:
+ *   Y [T, N] = Xq [T, K] . W_q^T
+ * of the values that the codes stand for; codes, exps from slope_quantize_mxfp4, packed_w
+ * from slope_pack_sparse_mxfp4 of W_s (rows N, cols K), or of W_dp^T (rows K, cols N)
+ * with dY's codes, for dX.  float32 sums (the matrix instruction's; which order depends on the
+ * sizes), rounded once to out_dt (BF16, F16 or F32).  Any T; Y is overwritten, K = 0 gives 0.
+ * No adapter term (slope_lowrank_add adds it).  Y needs 16-byte alignment.  Errors:
+ * SLOPE_ERR_SHAPE unless K % 16 == 0 and N % 4 == 0; SLOPE_ERR_UNSUPPORTED for K >
+ * SLOPE_MXFP4_MAX_COLS; SLOPE_ERR_WORKSPACE if packed_w is short. */
+slope_status slope_spmm_mxfp4_packed(slope_dtype out_dt, const uint8_t* codes, const uint8_t* exps, int64_t T,
+                                     int64_t K, const void* packed_w, int64_t packed_w_bytes, int64_t N, void* Y,
+                                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif

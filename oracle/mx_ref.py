@@ -119,3 +119,81 @@ def adamw8(g, m, m_exp, v, v_exp, beta1, beta2, seed32, first=0):
     cm, em, _ = moment_codes8(mf, w >> 12, GRID_M, TOP_M, True)
     cv, ev, _ = moment_codes8(vf, w & 0xFFFFF, GRID_V, TOP_V, False)
     return cm, em, cv, ev, mf, vf
+
+
+# ------------------------------------------------------------------ 4-bit floating point
+
+GRID4 = float_grid(2, 1, 1)        # E2M1's magnitudes
+
+__all__ += ["mxfp4_codes", "mxfp4_values", "mxfp4_rows", "mxfp4_kept_codes", "spmm_mxfp4"]
+
+
+def _block_codes(blocks):
+    """(codes, scales) of rows that are one block each: the exponent is found by trying
+    them, a code by the distance to every grid value."""
+    R = blocks.shape[0]
+    bad = ~np.isfinite(blocks).all(axis=1)
+    x = np.where(bad[:, None], 0.0, blocks)
+    peak = np.abs(x).max(axis=1) if x.size else np.zeros(R)
+    # the largest E with peak >= 7 * 2^(E-1): from there on the peak rounds past 6 * 2^(E-1)
+    e = np.full(R, -127)
+    some = peak > 0
+    guess = np.where(some, np.frexp(np.where(some, peak, 1.0))[1] - 4, -127)
+    for _ in range(4):
+        guess = np.where(some & (peak >= 7 * np.ldexp(1.0, guess)), guess + 1, guess)
+    e = np.maximum(guess, -127)
+    a = np.abs(x) * np.ldexp(1.0, -e)[:, None]
+    d = np.abs(a[:, :, None] - GRID4)
+    best = d.min(axis=2)
+    low = np.argmin(d, axis=2)                       # of a tie the lower one; the even one of the two
+    tie = (low < 7) & (np.take_along_axis(d, np.minimum(low + 1, 7)[:, :, None], 2)[:, :, 0] == best)
+    code = np.where(tie & (low % 2 == 1), low + 1, low).astype(np.uint8)
+    code = np.where(bad[:, None], 0, code | (np.signbit(x).astype(np.uint8) << 3)).astype(np.uint8)
+    return code, np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def mxfp4_codes(x):
+    """(codes [R, P], scales [R, P / 32]) of rows x [R, K] in value order; P is K rounded
+    up to a multiple of 128, the blocks past K's have codes and scales 0."""
+    R, K = x.shape
+    own = -(-K // 32) * 32
+    P = -(-K // 128) * 128
+    full = np.zeros((R, own))
+    full[:, :K] = x
+    c, e = _block_codes(full.reshape(-1, 32))
+    codes, exps = np.zeros((R, P), np.uint8), np.zeros((R, P // 32), np.uint8)
+    codes[:, :own] = c.reshape(R, own)
+    exps[:, :own // 32] = e.reshape(R, own // 32)
+    return codes, exps
+
+
+def mxfp4_values(codes, exps, K):
+    """What codes [R, P] and scales stand for, the first K of a row, in float64."""
+    s = np.where(exps == 255, np.nan, np.ldexp(1.0, exps.astype(np.int64) - 127))
+    v = GRID4[codes & 7] * np.where(codes & 8, -1.0, 1.0) * np.repeat(s, 32, axis=1)
+    return v[:, :K]
+
+
+def mxfp4_rows(codes):
+    """The bytes of rows of codes: value 4g + p of a block in nibble g of its word p."""
+    R, P = codes.shape
+    nib = codes.reshape(R, P // 32, 8, 4).transpose(0, 1, 3, 2).astype(np.uint32)     # [.., p, g]
+    words = (nib << (4 * np.arange(8, dtype=np.uint32))).sum(axis=3, dtype=np.uint32)
+    return np.ascontiguousarray(words.astype("<u4")).view(np.uint8).reshape(R, P // 2)
+
+
+def mxfp4_kept_codes(values, cols):
+    """(codes [R, cols/2], scales [R, ceil(cols/32)]) of a compressed matrix's values:
+    16 kept values have one scale."""
+    R, half = values.shape
+    own = -(-cols // 32) * 16
+    full = np.zeros((R, own))
+    full[:, :half] = values
+    c, e = _block_codes(full.reshape(-1, 16))
+    return c.reshape(R, own)[:, :half], e.reshape(R, own // 16)
+
+
+def spmm_mxfp4(xv, wv):
+    """Y and the sums of magnitudes of the products, in float64."""
+    with np.errstate(invalid="ignore"):
+        return xv @ wv.T, np.abs(xv) @ np.abs(wv).T

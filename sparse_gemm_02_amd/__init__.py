@@ -39,7 +39,8 @@ __all__ = [
     "slope_rmsnorm", "slope_rmsnorm_bwd_workspace_bytes", "slope_rmsnorm_bwd", "slope_quantize_rows_i8",
     "slope_packed_sparse_i8_bytes", "slope_pack_sparse_i8", "slope_spmm_i8_packed", "slope_spmm_i8_decode",
     "I8_DECODE_MAX_TOKENS", "I8_MAX_COLS", "EXPORTED_SYMBOLS_INT8",
-    "slope_adamw_multi", "slope_adamw_moments", "MX_BLOCK", "EXPORTED_SYMBOLS_MX",
+    "slope_adamw_multi", "slope_adamw_moments", "slope_mxfp4_row_bytes", "slope_quantize_mxfp4", "slope_mxfp4_values",
+    "slope_packed_sparse_mxfp4_bytes", "slope_pack_sparse_mxfp4", "slope_spmm_mxfp4_packed", "MX_BLOCK", "EXPORTED_SYMBOLS_MX",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -133,6 +134,12 @@ _SIGS_MX = {
     "slope_adamw_multi": (_i32, [_i32, _i64, _P_I32, _P_I32, _P_VP, _P_VP, _P_VP, _P_VP, _P_VP, _P_VP, _P_I64, _P_HP,
                                  ctypes.c_uint64, _vp]),
     "slope_adamw_moments": (_i32, [_i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
+    "slope_mxfp4_row_bytes": (_i32, [_i64, _P_I64, _P_I64]),
+    "slope_quantize_mxfp4": (_i32, [_i32, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "slope_mxfp4_values": (_i32, [_i32, _vp, _vp, _i64, _i64, _vp, _vp]),
+    "slope_packed_sparse_mxfp4_bytes": (_i32, [_i64, _i64, _P_I64]),
+    "slope_pack_sparse_mxfp4": (_i32, [_i32, _vp, _vp, _i64, _i64, _vp, _i64, _vp]),
+    "slope_spmm_mxfp4_packed": (_i32, [_i32, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp]),
 }
 EXPORTED_SYMBOLS_MX = tuple(_SIGS_MX)
 
@@ -779,3 +786,61 @@ def slope_adamw_moments(m, m_exp, v, v_exp, m_out=None, v_out=None, stream=None)
     _on_device("slope_adamw_moments", d, stream, _code(odt), flat(m, "m", n, _u8), flat(m_exp, "m_exp", blocks, _u8),
                flat(v, "v", n, _u8), flat(v_exp, "v_exp", blocks, _u8), n, flat(m_out, "m_out", n, odt),
                flat(v_out, "v_out", n, odt))
+
+
+def _mxfp4_width(K):
+    """(bytes of codes, bytes of scales) of a row of K values."""
+    stages = -(-K // 128)
+    return 64 * stages, 4 * stages
+
+
+def slope_mxfp4_row_bytes(K: int):
+    """(bytes of codes, bytes of scales) of one row of K 4-bit values."""
+    c, e = ctypes.c_int64(), ctypes.c_int64()
+    _check("slope_mxfp4_row_bytes", library().slope_mxfp4_row_bytes(K, ctypes.byref(c), ctypes.byref(e)))
+    return c.value, e.value
+
+
+def slope_quantize_mxfp4(X, codes, exps, stream=None) -> None:
+    """4-bit codes [T, code bytes] and scales [T, scale bytes] (slope_mxfp4_row_bytes)
+    of the rows of X [T, K]."""
+    T, K = shape = _rows(X, "X")
+    d = X.get_device()
+    nc, ne = _mxfp4_width(K)
+    _on_device("slope_quantize_mxfp4", d, stream, _code(X.dtype), _arg(X, "X", shape, X.dtype, d), T, K,
+               _arg(codes, "codes", (T, nc), _u8, d), _arg(exps, "exps", (T, ne), _u8, d))
+
+
+def slope_mxfp4_values(codes, exps, out, stream=None) -> None:
+    """out [T, K] <- the values of 4-bit rows."""
+    T, K = shape = _rows(out, "out")
+    d = out.get_device()
+    nc, ne = _mxfp4_width(K)
+    _on_device("slope_mxfp4_values", d, stream, _code(out.dtype), _arg(codes, "codes", (T, nc), _u8, d),
+               _arg(exps, "exps", (T, ne), _u8, d), T, K, _arg(out, "out", shape, out.dtype, d))
+
+
+def slope_packed_sparse_mxfp4_bytes(rows: int, cols: int) -> int:
+    b = ctypes.c_int64()
+    _check("slope_packed_sparse_mxfp4_bytes", library().slope_packed_sparse_mxfp4_bytes(rows, cols, ctypes.byref(b)))
+    return b.value
+
+
+def slope_pack_sparse_mxfp4(values, meta, rows, cols, packed, stream=None) -> None:
+    """4-bit tile chunks of a compressed 16-bit matrix."""
+    d = values.get_device()
+    pp, pb = _buffer(packed, "packed", d)
+    _on_device("slope_pack_sparse_mxfp4", d, stream, _code(values.dtype),
+               _arg(values, "values", (rows, cols // 2), values.dtype, d),
+               _arg(meta, "meta", (rows, (cols // 4 + 7) // 8), torch.int32, d), rows, cols, pp, pb)
+
+
+def slope_spmm_mxfp4_packed(codes, exps, K, packed_w, N, Y, stream=None) -> None:
+    """Y [T, N] = Xq . W_q^T on 4-bit rows of K values and a 2:4 weight's 4-bit chunks, any T."""
+    T = _rows(codes, "codes")[0]
+    d = codes.get_device()
+    pp, pb = _buffer(packed_w, "packed_w", d)
+    nc, ne = _mxfp4_width(K)
+    odt = Y.dtype
+    _on_device("slope_spmm_mxfp4_packed", d, stream, _code(odt), _arg(codes, "codes", (T, nc), _u8, d),
+               _arg(exps, "exps", (T, ne), _u8, d), T, K, pp, pb, N, _arg(Y, "Y", (T, N), odt, d))

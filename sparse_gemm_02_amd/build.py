@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libslope.so")
 SOURCES = ["capi.cpp", "prune.hip", "generic.hip", "spmm.hip", "lowrank.hip", "wgrad.hip", "decode.hip", "lowrank_bwd.hip", "adamw.hip", "e4m3.hip",
-           "capi_int8.cpp", "rmsnorm.hip", "int8.hip", "capi_mx.cpp", "adamw_multi.hip"]
+           "capi_int8.cpp", "rmsnorm.hip", "int8.hip", "capi_mx.cpp", "adamw_multi.hip", "mxfp4.hip", "spmm_mxfp4.hip"]
 
 ARCH = "gfx950"
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-unused-function",

@@ -16,6 +16,7 @@ using slope::Dt;
 
 namespace {
 
+bool in_range(int64_t v) { return v >= 0 && v <= SLOPE_MAX_DIM; }
 bool dt_ok(int d) { return d == SLOPE_F32 || d == SLOPE_BF16 || d == SLOPE_F16; }
 int64_t size_of(int d) { return d == SLOPE_F32 ? 4 : 2; }
 slope_status from_hip(hipError_t e) { return e == hipSuccess ? SLOPE_OK : SLOPE_ERR_HIP; }
@@ -101,6 +102,69 @@ slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, c
   if (m_out_or_null && m_out_or_null == v_out_or_null && n > 0) return SLOPE_ERR_INVALID_ARG;
   return from_hip(slope::launch_adamw_moments((Dt)out_dt, m_or_null, m_exp_or_null, v_or_null, v_exp_or_null, n,
                                               m_out_or_null, v_out_or_null, (hipStream_t)stream));
+}
+
+slope_status slope_mxfp4_row_bytes(int64_t K, int64_t* code_bytes, int64_t* scale_bytes) {
+  if (!code_bytes || !scale_bytes || K < 0) return SLOPE_ERR_INVALID_ARG;
+  if (!in_range(K)) return SLOPE_ERR_UNSUPPORTED;
+  *code_bytes = (K + 127) / 128 * 64;
+  *scale_bytes = (K + 127) / 128 * 4;
+  return SLOPE_OK;
+}
+
+slope_status slope_quantize_mxfp4(slope_dtype dt, const void* X, int64_t T, int64_t K, uint8_t* codes, uint8_t* exps,
+                                  void* stream) {
+  if (!dt_ok(dt) || T < 0 || K < 0) return SLOPE_ERR_INVALID_ARG;
+  SLOPE_TRY(ptr(X, true, (unsigned)size_of(dt)));
+  SLOPE_TRY(ptr(codes, true));
+  SLOPE_TRY(ptr(exps, true, 4));
+  if (!in_range(T) || !in_range(K)) return SLOPE_ERR_UNSUPPORTED;
+  return from_hip(slope::launch_quantize_mxfp4((Dt)dt, X, T, K, codes, exps, (hipStream_t)stream));
+}
+
+slope_status slope_mxfp4_values(slope_dtype out_dt, const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K,
+                                void* out, void* stream) {
+  if (!dt_ok(out_dt) || T < 0 || K < 0) return SLOPE_ERR_INVALID_ARG;
+  SLOPE_TRY(ptr(codes, true));
+  SLOPE_TRY(ptr(exps, true, 4));
+  SLOPE_TRY(ptr(out, true, (unsigned)size_of(out_dt)));
+  if (!in_range(T) || !in_range(K)) return SLOPE_ERR_UNSUPPORTED;
+  return from_hip(slope::launch_mxfp4_values((Dt)out_dt, codes, exps, T, K, out, (hipStream_t)stream));
+}
+
+slope_status slope_packed_sparse_mxfp4_bytes(int64_t rows, int64_t cols, int64_t* bytes) {
+  if (!bytes || rows < 0 || cols < 0) return SLOPE_ERR_INVALID_ARG;
+  if (cols % 16) return SLOPE_ERR_SHAPE;
+  if (!in_range(rows) || cols > SLOPE_MXFP4_MAX_COLS) return SLOPE_ERR_UNSUPPORTED;
+  *bytes = slope::packed_sparse_mxfp4_bytes(rows, cols);
+  return SLOPE_OK;
+}
+
+slope_status slope_pack_sparse_mxfp4(slope_dtype dt, const void* values, const uint32_t* meta, int64_t rows,
+                                     int64_t cols, void* packed, int64_t packed_bytes, void* stream) {
+  if (!dt_ok(dt) || rows < 0 || cols < 0 || packed_bytes < 0) return SLOPE_ERR_INVALID_ARG;
+  SLOPE_TRY(ptr(values, true));
+  SLOPE_TRY(ptr(meta, true));
+  SLOPE_TRY(ptr(packed, true));
+  if (dt == SLOPE_F32) return SLOPE_ERR_UNSUPPORTED;   // a weight's values are in 16 bits
+  if (cols % 16) return SLOPE_ERR_SHAPE;
+  if (!in_range(rows) || cols > SLOPE_MXFP4_MAX_COLS) return SLOPE_ERR_UNSUPPORTED;
+  if (packed_bytes < slope::packed_sparse_mxfp4_bytes(rows, cols)) return SLOPE_ERR_WORKSPACE;
+  return from_hip(slope::launch_pack_sparse_mxfp4((Dt)dt, values, meta, rows, cols, packed, (hipStream_t)stream));
+}
+
+slope_status slope_spmm_mxfp4_packed(slope_dtype out_dt, const uint8_t* codes, const uint8_t* exps, int64_t T,
+                                     int64_t K, const void* packed_w, int64_t packed_w_bytes, int64_t N, void* Y,
+                                     void* stream) {
+  if (!dt_ok(out_dt) || T < 0 || K < 0 || N < 0 || packed_w_bytes < 0) return SLOPE_ERR_INVALID_ARG;
+  SLOPE_TRY(ptr(codes, true));
+  SLOPE_TRY(ptr(exps, true, 4));
+  SLOPE_TRY(ptr(packed_w, true));
+  SLOPE_TRY(ptr(Y, true));
+  if (K % 16 || N % 4) return SLOPE_ERR_SHAPE;
+  if (!in_range(T) || !in_range(N) || K > SLOPE_MXFP4_MAX_COLS) return SLOPE_ERR_UNSUPPORTED;
+  if (packed_w_bytes < slope::packed_sparse_mxfp4_bytes(N, K)) return SLOPE_ERR_WORKSPACE;
+  return from_hip(slope::launch_spmm_mxfp4((Dt)out_dt, codes, exps, T, K, packed_w, N, Y, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -235,4 +235,17 @@ hipError_t launch_adamw_multi(bool eight, const AdamWTensors& t, const AdamWStep
 hipError_t launch_adamw_moments(Dt out, const uint8_t* m, const uint8_t* me, const uint8_t* v, const uint8_t* ve,
                                 int64_t n, void* mo, void* vo, hipStream_t s);
 
+// 4-bit floating point (E2M1, a power of two for 32 values): codes of rows (padded to a
+// multiple of 128 values: 64 code bytes and 4 scale bytes for each 128) and what they
+// stand for; tile chunks of a compressed 16-bit 2:4 matrix; their product Y [T, M].
+int64_t packed_sparse_mxfp4_bytes(int64_t rows, int64_t cols);
+hipError_t launch_quantize_mxfp4(Dt dt, const void* X, int64_t T, int64_t K, uint8_t* codes, uint8_t* exps,
+                                 hipStream_t s);
+hipError_t launch_mxfp4_values(Dt out, const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K, void* Y,
+                               hipStream_t s);
+hipError_t launch_pack_sparse_mxfp4(Dt dt, const void* values, const uint32_t* meta, int64_t M, int64_t K, void* packed,
+                                    hipStream_t s);
+hipError_t launch_spmm_mxfp4(Dt out, const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K, const void* packed,
+                             int64_t M, void* Y, hipStream_t s);
+
 }  // namespace slope

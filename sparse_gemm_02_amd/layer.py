@@ -1,7 +1,7 @@
 """Module wrappers over the C ABI: a 2:4 sparse linear layer with an optional
 low-rank adapter, its autograd function, AdamW on its compressed values; the
 RMS norm with the residual's addition, its autograd function; and the linear
-layer on 8-bit integer codes, for inference.
+layer on 8-bit integer codes and on 4-bit floating point, for inference.
 
 Orchestration only: every arithmetic step runs in libslope.so through the
 binding in this package (the forward product with the fused adapter term, the
@@ -36,11 +36,14 @@ from . import (I8_DECODE_MAX_TOKENS, MX_BLOCK, slope_adamw_double_prune_packed, 
                slope_lowrank_add, slope_lowrank_grads_packed, slope_lowrank_grads_workspace_bytes,
                slope_lowrank_workspace_bytes, slope_masked_wgrad_packed, slope_pack_sparse, slope_pack_sparse_i8,
                slope_pack_tokens, slope_packed_sparse_bytes, slope_packed_sparse_i8_bytes, slope_packed_tokens_bytes,
-               slope_prune_compress24, slope_quantize_rows_i8, slope_rmsnorm, slope_rmsnorm_bwd,
+               slope_mxfp4_row_bytes, slope_mxfp4_values, slope_pack_sparse_mxfp4, slope_packed_sparse_mxfp4_bytes,
+               slope_prune_compress24, slope_quantize_mxfp4, slope_quantize_rows_i8, slope_rmsnorm, slope_rmsnorm_bwd,
                slope_rmsnorm_bwd_workspace_bytes, slope_spmm_bwd_dx_packed, slope_spmm_bwd_dx_packed_tokens,
-               slope_spmm_fwd_packed, slope_spmm_i8_decode, slope_spmm_i8_packed, slope_wgrad_split_workspace_bytes)
+               slope_spmm_fwd_packed, slope_spmm_i8_decode, slope_spmm_i8_packed, slope_spmm_mxfp4_packed,
+               slope_wgrad_split_workspace_bytes)
 
-__all__ = ["SparseLinear", "SparseAdamW", "training_state_bytes", "ResidualRMSNorm", "Int8Rows", "Int8SparseLinear"]
+__all__ = ["SparseLinear", "SparseAdamW", "training_state_bytes", "ResidualRMSNorm", "Int8Rows", "Int8SparseLinear",
+           "Mxfp4Rows", "Mxfp4SparseLinear"]
 
 
 def _bytes(n, device):
@@ -419,6 +422,17 @@ class ResidualRMSNorm(torch.nn.Module):
         return (rows, h.view(x.shape), y.view(x.shape)) if output else (rows, h.view(x.shape))
 
 
+def _apply_keeping_formats(self, fn, recurse=True):
+    """nn.Module._apply for a module whose buffers keep their formats under .half(), .to(dtype) and the like."""
+    kept = dict(self._buffers)
+    torch.nn.Module._apply(self, fn, recurse)
+    for name, b in kept.items():
+        now = self._buffers[name]
+        if b is not None and now.dtype != b.dtype:       # a conversion: b's values and format, on the new device
+            self._buffers[name] = b.to(now.device)
+    return self
+
+
 class Int8SparseLinear(torch.nn.Module):
     """Inference form of a SparseLinear on 8-bit integer codes:
 
@@ -443,14 +457,7 @@ class Int8SparseLinear(torch.nn.Module):
             self.register_buffer("L", layer.L.detach().clone() if layer.rank else None)
             self.register_buffer("R", layer.R.detach().clone() if layer.rank else None)
 
-    def _apply(self, fn, recurse=True):
-        kept = dict(self._buffers)
-        super()._apply(fn, recurse)
-        for name, b in kept.items():
-            now = self._buffers[name]
-            if b is not None and now.dtype != b.dtype:   # a conversion: b's values and format, on the new device
-                self._buffers[name] = b.to(now.device)
-        return self
+    _apply = _apply_keeping_formats
 
     @torch.no_grad()
     def forward(self, rows: Int8Rows | torch.Tensor, x: torch.Tensor | None = None) -> torch.Tensor:
@@ -482,4 +489,86 @@ class Int8SparseLinear(torch.nn.Module):
             ws = _bytes(slope_lowrank_workspace_bytes(T, K, self.rank, N), q.device)
             with torch.cuda.device(q.device):        # the call takes the current device's stream
                 slope_lowrank_add(x2, self.L, self.R, ws, y)
+        return y.view(*lead, N)
+
+
+class Mxfp4Rows(NamedTuple):
+    """Activations as 4-bit floating point with a scale for 32 values: codes [...,
+    code bytes] and exps [..., scale bytes] uint8 (slope_mxfp4_row_bytes), for rows
+    of `features` values."""
+    codes: torch.Tensor
+    exps: torch.Tensor
+    features: int
+
+    @classmethod
+    def of(cls, x: torch.Tensor) -> "Mxfp4Rows":
+        """The rows of a bf16, fp16 or fp32 x [..., K]."""
+        K = x.shape[-1]
+        x2 = x.detach().reshape(-1, K).contiguous()
+        nc, ne = slope_mxfp4_row_bytes(K)
+        codes = torch.empty((x2.shape[0], nc), dtype=torch.uint8, device=x.device)
+        exps = torch.empty((x2.shape[0], ne), dtype=torch.uint8, device=x.device)
+        slope_quantize_mxfp4(x2, codes, exps)
+        lead = x.shape[:-1]
+        return cls(codes.view(*lead, nc), exps.view(*lead, ne), K)
+
+    def values(self, dtype=torch.float32) -> torch.Tensor:
+        """What the codes stand for."""
+        lead = self.codes.shape[:-1]
+        out = torch.empty((*lead, self.features), dtype=dtype, device=self.codes.device)
+        flat = lambda t: _aligned(t.reshape(-1, t.shape[-1]))
+        slope_mxfp4_values(flat(self.codes), flat(self.exps), out.view(-1, self.features))
+        return out
+
+
+class Mxfp4SparseLinear(torch.nn.Module):
+    """Inference form of a SparseLinear on 4-bit floating point:
+
+        y = Xq . W_q^T (+ (x . L) . R)
+
+    The weight's codes, positions and scales (3.25 bits for a dense weight) are made
+    once, from the layer's current values; the 16-bit weight is not kept.  Its tensors
+    keep their formats when the model around it is converted to another; devices change
+    as usual.  `lin(x)` quantizes the rows of an x in the layer's format itself;
+    `lin(rows)` takes an Mxfp4Rows, and then, if the layer has an adapter, the 16-bit
+    values as well: `lin(rows, x)`."""
+
+    def __init__(self, layer: SparseLinear):
+        super().__init__()
+        N, K, dev = layer.out_features, layer.in_features, layer.values.device
+        self.in_features, self.out_features, self.rank = K, N, layer.rank
+        self.dtype = layer.values.dtype
+        self.register_buffer("packed", _bytes(slope_packed_sparse_mxfp4_bytes(N, K), dev))
+        with torch.no_grad():
+            slope_pack_sparse_mxfp4(layer.values, layer.meta, N, K, self.packed)
+            self.register_buffer("L", layer.L.detach().clone() if layer.rank else None)
+            self.register_buffer("R", layer.R.detach().clone() if layer.rank else None)
+
+    _apply = _apply_keeping_formats
+
+    @torch.no_grad()
+    def forward(self, rows: Mxfp4Rows | torch.Tensor, x: torch.Tensor | None = None) -> torch.Tensor:
+        K, N = self.in_features, self.out_features
+        if not isinstance(rows, Mxfp4Rows):
+            if x is not None and x is not rows:
+                raise ValueError("give one input, or its Mxfp4Rows and the input itself")
+            x = rows
+        if x is not None and (x.shape[-1] != K or x.dtype != self.dtype):
+            raise ValueError("input must have in_features columns and the layer's format")
+        if self.rank and x is None:
+            raise ValueError("the adapter needs the 16-bit input next to its codes")
+        if not isinstance(rows, Mxfp4Rows):
+            rows = Mxfp4Rows.of(x)
+        lead = rows.codes.shape[:-1]
+        if rows.features != K or rows.exps.shape[:-1] != lead or (x is not None and x.shape[:-1] != lead):
+            raise ValueError("codes must be of in_features values, with scales for each row, and the input's rows")
+        flat = lambda t: _aligned(t.reshape(-1, t.shape[-1]))
+        codes, exps = flat(rows.codes), flat(rows.exps)
+        T = codes.shape[0]
+        y = torch.empty((T, N), dtype=self.dtype, device=codes.device)
+        slope_spmm_mxfp4_packed(codes, exps, K, self.packed, N, y)
+        if self.rank and T:
+            ws = _bytes(slope_lowrank_workspace_bytes(T, K, self.rank, N), y.device)
+            with torch.cuda.device(y.device):        # the call takes the current device's stream
+                slope_lowrank_add(_aligned(x.reshape(-1, K)), self.L, self.R, ws, y)
         return y.view(*lead, N)

@@ -124,3 +124,75 @@ def test_binding_checks_lists():
         S.slope_adamw_moments(m8[0], e[1], None, None, torch.zeros(40))
     with pytest.raises(ValueError, match="GPU memory"):
         S.slope_adamw_moments(m8[0], e[0], None, None, torch.zeros(40))
+
+
+def test_4_bit_size_queries(lib):
+    assert S.slope_mxfp4_row_bytes(0) == (0, 0) and S.slope_mxfp4_row_bytes(1) == (64, 4)
+    assert S.slope_mxfp4_row_bytes(128) == (64, 4) and S.slope_mxfp4_row_bytes(4999) == (40 * 64, 160)
+    assert S.slope_packed_sparse_mxfp4_bytes(27648, 9216) == 432 * 72 * 3328
+    assert S.slope_packed_sparse_mxfp4_bytes(300, 272) == 5 * 3 * 3328 and S.slope_packed_sparse_mxfp4_bytes(0, 16) == 0
+    for rows, cols in [(4, 8), (4, (1 << 21) + 16), (-1, 16), ((1 << 22) + 1, 16)]:
+        with pytest.raises(S.SlopeError):
+            S.slope_packed_sparse_mxfp4_bytes(rows, cols)
+    for k in (-1, (1 << 22) + 1):
+        with pytest.raises(S.SlopeError):
+            S.slope_mxfp4_row_bytes(k)
+    c = ctypes.c_int64()
+    assert lib.slope_mxfp4_row_bytes(4, None, ctypes.byref(c)) == -1
+    assert lib.slope_mxfp4_row_bytes(4, ctypes.byref(c), None) == -1
+    assert lib.slope_packed_sparse_mxfp4_bytes(4, 16, None) == -1
+
+
+def test_4_bit_refusals(lib):
+    q = lambda dt=BF16, X=FAKE, T=4, K=64, c=FAKE, e=FAKE: lib.slope_quantize_mxfp4(dt, X, T, K, c, e, None)
+    v = lambda dt=BF16, c=FAKE, e=FAKE, T=4, K=64, o=FAKE: lib.slope_mxfp4_values(dt, c, e, T, K, o, None)
+    for f in (q, v):
+        assert f(dt=3) == -1 and f(T=-1) == -1 and f(K=-1) == -1 and f(c=None) == -1 and f(e=None) == -1
+        assert f(c=FAKE + 8) == -3 and f(e=FAKE + 2) == -3
+        assert f(T=(1 << 22) + 1) == -6 and f(K=(1 << 22) + 1) == -6
+    assert q(X=None) == -1 and q(X=FAKE + 1) == -3 and q(dt=F32, X=FAKE + 2) == -3
+    assert v(o=None) == -1 and v(o=FAKE + 1) == -3 and v(dt=F32, o=FAKE + 2) == -3
+    big = 1 << 40
+    p = lambda dt=BF16, vals=FAKE, meta=FAKE, rows=64, cols=64, out=FAKE, nb=big: \
+        lib.slope_pack_sparse_mxfp4(dt, vals, meta, rows, cols, out, nb, None)
+    assert p(dt=5) == -1 and p(vals=None) == -1 and p(meta=None) == -1 and p(out=None) == -1
+    assert p(rows=-1) == -1 and p(cols=-1) == -1 and p(nb=-1) == -1
+    assert p(vals=FAKE + 2) == -3 and p(meta=FAKE + 4) == -3 and p(out=FAKE + 8) == -3
+    assert p(cols=24) == -2 and p(dt=F32) == -6 and p(cols=(1 << 21) + 16) == -6 and p(rows=(1 << 22) + 1) == -6
+    assert p(nb=3327) == -4
+    y = lambda dt=BF16, c=FAKE, e=FAKE, T=4, K=64, w=FAKE, nb=big, N=64, Y=FAKE: \
+        lib.slope_spmm_mxfp4_packed(dt, c, e, T, K, w, nb, N, Y, None)
+    assert y(dt=3) == -1 and y(c=None) == -1 and y(e=None) == -1 and y(w=None) == -1 and y(Y=None) == -1
+    assert y(T=-1) == -1 and y(K=-1) == -1 and y(N=-1) == -1 and y(nb=-1) == -1
+    assert y(c=FAKE + 8) == -3 and y(e=FAKE + 1) == -3 and y(w=FAKE + 4) == -3 and y(Y=FAKE + 8) == -3
+    assert y(K=24) == -2 and y(N=66) == -2
+    assert y(T=(1 << 22) + 1) == -6 and y(N=(1 << 22) + 4) == -6 and y(K=(1 << 21) + 16) == -6
+    assert y(nb=3327) == -4
+
+
+def test_binding_checks_4_bit_tensors():
+    u8 = torch.uint8
+    x, c, e = torch.zeros(3, 40), torch.zeros(3, 64, dtype=u8), torch.zeros(3, 4, dtype=u8)
+    with pytest.raises(ValueError, match="GPU memory"):
+        S.slope_quantize_mxfp4(x, c, e)
+    with pytest.raises(ValueError, match="two dimensions"):
+        S.slope_quantize_mxfp4(x.view(-1), c, e)
+    with pytest.raises(ValueError, match="codes must have shape"):
+        S.slope_quantize_mxfp4(x, c[:2], e)
+    with pytest.raises(TypeError, match="exps must be torch.uint8"):
+        S.slope_quantize_mxfp4(x, c, e.float())
+    with pytest.raises(TypeError, match="expected bfloat16"):
+        S.slope_quantize_mxfp4(x.double(), c, e)
+    with pytest.raises(ValueError, match="X must be contiguous"):
+        S.slope_quantize_mxfp4(torch.zeros(40, 3).t(), c, e)
+    with pytest.raises(ValueError, match="exps must have shape"):
+        S.slope_mxfp4_values(c, e[:, :2].contiguous(), x)
+    w = torch.zeros(3328, dtype=u8)
+    with pytest.raises(ValueError, match="Y must have shape"):
+        S.slope_spmm_mxfp4_packed(c, e, 48, w, 64, torch.zeros(3, 60))
+    with pytest.raises(ValueError, match="codes must have shape"):
+        S.slope_spmm_mxfp4_packed(c, e, 144, w, 64, torch.zeros(3, 64))
+    with pytest.raises(ValueError, match="GPU memory"):
+        S.slope_spmm_mxfp4_packed(c, e, 48, w, 64, torch.zeros(3, 64))
+    with pytest.raises(ValueError, match="values must have shape"):
+        S.slope_pack_sparse_mxfp4(torch.zeros(64, 20, dtype=torch.bfloat16), torch.zeros(64, 2, dtype=torch.int32), 64, 48, w)

@@ -88,3 +88,62 @@ def test_float32_moments_against_exact_fractions():
     for i in range(300):
         assert mn[i] == near(F(b1) * F(m[i]) + F(near(F(o1) * F(g[i]))))
         assert vn[i] == near(F(b2) * F(v[i]) + F(near(F(o2) * F(near(F(g[i]) * F(g[i]))))))
+
+
+def test_4_bit_codes_by_search_and_by_hand():
+    # the scale: magnitudes up to 7 units stay, from 7 on the next power of two is taken
+    for peak, e in [(6.0, 0), (6.999, 0), (7.0, 1), (8.0, 1), (4.0, 0), (3.5, 0), (3.499, -1), (1.0, -2), (0.0, -127)]:
+        x = np.zeros((1, 32))
+        x[0, 5] = -peak
+        codes, exps = oracle.mxfp4_codes(x)
+        assert exps[0, 0] == e + 127 and not exps[0, 1:].any(), peak
+        assert codes.shape == (1, 128)
+    x = np.zeros((1, 32))
+    x[0, :16] = [0, 0.25, 0.2501, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 5.01, 6.5, -0.25, -0.75, -5.0, 4.0, -0.0]
+    want = [0, 0, 0.5, 1.0, 1.0, 2.0, 2.0, 4.0, 4.0, 6.0, 6.0, -0.0, -1.0, -4.0, 4.0, -0.0]
+    codes, exps = oracle.mxfp4_codes(x)
+    got = oracle.mxfp4_values(codes, exps, 16)
+    assert exps[0, 0] == 127 and np.array_equal(got[0], want) and np.array_equal(np.signbit(got[0]), np.signbit(want))
+    # the nearest value of the format at the block's scale, random blocks
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((50, 96)) * np.exp(rng.standard_normal((50, 96)) * 3)
+    codes, exps = oracle.mxfp4_codes(x)
+    v = oracle.mxfp4_values(codes, exps, 96)
+    s = np.repeat(np.ldexp(1.0, exps.astype(int) - 127), 32, axis=1)[:, :96]
+    grid = np.concatenate([mx_ref.GRID4, -mx_ref.GRID4])
+    best = np.abs(x[:, :, None] - s[:, :, None] * grid).min(axis=2)
+    assert np.array_equal(np.abs(x - v), best)
+    assert np.array_equal(mx_ref.GRID4, [0, 0.5, 1, 1.5, 2, 3, 4, 6])
+    # blocks without values
+    x[3, 40], x[4, 0] = np.nan, np.inf
+    codes, exps = oracle.mxfp4_codes(x)
+    assert exps[3, 1] == 255 and exps[4, 0] == 255 and not codes[3, 32:64].any()
+    v = oracle.mxfp4_values(codes, exps, 96)
+    assert np.isnan(v[3, 32:64]).all() and np.isnan(v).sum() == 64
+
+
+def test_row_bytes_and_kept_codes():
+    codes = np.arange(128, dtype=np.uint8).reshape(1, 128) % 16
+    rows = oracle.mxfp4_rows(codes)
+    words = rows.view("<u4")[0]
+    for b in range(4):
+        for p in range(4):
+            for g in range(8):
+                assert (words[4 * b + p] >> (4 * g)) & 15 == codes[0, 32 * b + 4 * g + p]
+    # a 2:4 row quantised dense and compressed has the same scales and the same kept codes
+    rng = np.random.default_rng(2)
+    w = rng.standard_normal((7, 80)).astype(np.float32).view(np.uint32)
+    mask, ws = oracle.prune24(w)
+    vals, meta, _ = oracle.compress24(w, mask)
+    kept, e = oracle.mxfp4_kept_codes(oracle.widen(vals), 80)
+    dense, ed = oracle.mxfp4_codes(oracle.widen(ws))
+    assert np.array_equal(e, ed[:, :3])
+    assert np.array_equal(oracle.decompress24(kept, meta, 80), dense[:, :80] * (mask > 0))
+
+
+def test_mutations_of_the_4_bit_oracle_would_show():
+    """Ties away from zero, a scale by the floor of the exponent, or a saturating 8 change values that the pins hold."""
+    x = np.zeros((1, 32))
+    x[0, :3] = [7.0, 2.5, 5.0]
+    codes, exps = oracle.mxfp4_codes(x)
+    assert list(oracle.mxfp4_values(codes, exps, 3)[0]) == [8.0, 2.0, 4.0]
