@@ -84,17 +84,17 @@ slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, c
  *          code, beyond 6 the code of 6
  * and with an infinity or a NaN in the block its scale is 255 and its codes are 0.
  *
- * Rows of codes: a row of K values is filled up with zero blocks (codes 0, scale 0) to
- * a multiple of 128 values and takes 64 ceil(K / 128) bytes of codes, 16 for each block,
- * and 4 ceil(K / 128) bytes of scales.  Within a block value 4g + p is nibble g of the
- * p-th 32-bit word (g = 0..7, p = 0..3). */
+ * Rows of codes: a row of K values takes 64 ceil(K / 128) bytes of codes, 16 for each
+ * block, and 16 ceil(K / 512) bytes of scales, one for each block; those of blocks past
+ * K are 0.  Within a block value 4g + p is nibble g of the p-th 32-bit word (g = 0..7,
+ * p = 0..3). */
 
 /* Bytes of codes and of scales of one row of K values.  Host-only. */
 slope_status slope_mxfp4_row_bytes(int64_t K, int64_t* code_bytes, int64_t* scale_bytes);
 
 /* Codes and scales of the rows of X [T, K] (BF16, F16 or F32; any K): codes
  * [T, code_bytes], exps [T, scale_bytes], both overwritten whole.  X needs its element's
- * alignment, codes 16 bytes, exps 4.  K = 0 or T = 0 does nothing. */
+ * alignment, codes and exps 16 bytes.  K = 0 or T = 0 does nothing. */
 slope_status slope_quantize_mxfp4(slope_dtype dt, const void* X, int64_t T, int64_t K, uint8_t* codes, uint8_t* exps,
                                   void* stream);
 

@@ -153,15 +153,15 @@ def _block_codes(blocks):
 
 
 def mxfp4_codes(x):
-    """(codes [R, P], scales [R, P / 32]) of rows x [R, K] in value order; P is K rounded
-    up to a multiple of 128, the blocks past K's have codes and scales 0."""
+    """(codes [R, P], scales [R, E]) of rows x [R, K] in value order; P is K rounded up to
+    a multiple of 128, E counts blocks up to a multiple of 512; past K both are 0."""
     R, K = x.shape
     own = -(-K // 32) * 32
     P = -(-K // 128) * 128
     full = np.zeros((R, own))
     full[:, :K] = x
     c, e = _block_codes(full.reshape(-1, 32))
-    codes, exps = np.zeros((R, P), np.uint8), np.zeros((R, P // 32), np.uint8)
+    codes, exps = np.zeros((R, P), np.uint8), np.zeros((R, -(-K // 512) * 16), np.uint8)
     codes[:, :own] = c.reshape(R, own)
     exps[:, :own // 32] = e.reshape(R, own // 32)
     return codes, exps
@@ -170,7 +170,7 @@ def mxfp4_codes(x):
 def mxfp4_values(codes, exps, K):
     """What codes [R, P] and scales stand for, the first K of a row, in float64."""
     s = np.where(exps == 255, np.nan, np.ldexp(1.0, exps.astype(np.int64) - 127))
-    v = GRID4[codes & 7] * np.where(codes & 8, -1.0, 1.0) * np.repeat(s, 32, axis=1)
+    v = GRID4[codes & 7] * np.where(codes & 8, -1.0, 1.0) * np.repeat(s, 32, axis=1)[:, :codes.shape[1]]
     return v[:, :K]
 
 

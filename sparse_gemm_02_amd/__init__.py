@@ -790,8 +790,7 @@ def slope_adamw_moments(m, m_exp, v, v_exp, m_out=None, v_out=None, stream=None)
 
 def _mxfp4_width(K):
     """(bytes of codes, bytes of scales) of a row of K values."""
-    stages = -(-K // 128)
-    return 64 * stages, 4 * stages
+    return 64 * -(-K // 128), 16 * -(-K // 512)
 
 
 def slope_mxfp4_row_bytes(K: int):

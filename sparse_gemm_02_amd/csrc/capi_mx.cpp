@@ -11,6 +11,7 @@
 #include "../../include/slope.h"
 #include "adamw_args.h"
 #include "launch.h"
+#include "mxfp4.h"
 
 using slope::Dt;
 
@@ -107,8 +108,8 @@ slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, c
 slope_status slope_mxfp4_row_bytes(int64_t K, int64_t* code_bytes, int64_t* scale_bytes) {
   if (!code_bytes || !scale_bytes || K < 0) return SLOPE_ERR_INVALID_ARG;
   if (!in_range(K)) return SLOPE_ERR_UNSUPPORTED;
-  *code_bytes = (K + 127) / 128 * 64;
-  *scale_bytes = (K + 127) / 128 * 4;
+  *code_bytes = slope::mx_code_bytes(K);
+  *scale_bytes = slope::mx_scale_bytes(K);
   return SLOPE_OK;
 }
 
@@ -117,7 +118,7 @@ slope_status slope_quantize_mxfp4(slope_dtype dt, const void* X, int64_t T, int6
   if (!dt_ok(dt) || T < 0 || K < 0) return SLOPE_ERR_INVALID_ARG;
   SLOPE_TRY(ptr(X, true, (unsigned)size_of(dt)));
   SLOPE_TRY(ptr(codes, true));
-  SLOPE_TRY(ptr(exps, true, 4));
+  SLOPE_TRY(ptr(exps, true));
   if (!in_range(T) || !in_range(K)) return SLOPE_ERR_UNSUPPORTED;
   return from_hip(slope::launch_quantize_mxfp4((Dt)dt, X, T, K, codes, exps, (hipStream_t)stream));
 }
@@ -126,7 +127,7 @@ slope_status slope_mxfp4_values(slope_dtype out_dt, const uint8_t* codes, const 
                                 void* out, void* stream) {
   if (!dt_ok(out_dt) || T < 0 || K < 0) return SLOPE_ERR_INVALID_ARG;
   SLOPE_TRY(ptr(codes, true));
-  SLOPE_TRY(ptr(exps, true, 4));
+  SLOPE_TRY(ptr(exps, true));
   SLOPE_TRY(ptr(out, true, (unsigned)size_of(out_dt)));
   if (!in_range(T) || !in_range(K)) return SLOPE_ERR_UNSUPPORTED;
   return from_hip(slope::launch_mxfp4_values((Dt)out_dt, codes, exps, T, K, out, (hipStream_t)stream));
@@ -158,7 +159,7 @@ slope_status slope_spmm_mxfp4_packed(slope_dtype out_dt, const uint8_t* codes, c
                                      void* stream) {
   if (!dt_ok(out_dt) || T < 0 || K < 0 || N < 0 || packed_w_bytes < 0) return SLOPE_ERR_INVALID_ARG;
   SLOPE_TRY(ptr(codes, true));
-  SLOPE_TRY(ptr(exps, true, 4));
+  SLOPE_TRY(ptr(exps, true));
   SLOPE_TRY(ptr(packed_w, true));
   SLOPE_TRY(ptr(Y, true));
   if (K % 16 || N % 4) return SLOPE_ERR_SHAPE;

@@ -235,9 +235,8 @@ hipError_t launch_adamw_multi(bool eight, const AdamWTensors& t, const AdamWStep
 hipError_t launch_adamw_moments(Dt out, const uint8_t* m, const uint8_t* me, const uint8_t* v, const uint8_t* ve,
                                 int64_t n, void* mo, void* vo, hipStream_t s);
 
-// 4-bit floating point (E2M1, a power of two for 32 values): codes of rows (padded to a
-// multiple of 128 values: 64 code bytes and 4 scale bytes for each 128) and what they
-// stand for; tile chunks of a compressed 16-bit 2:4 matrix; their product Y [T, M].
+// 4-bit floating point (E2M1, a power of two for 32 values): codes of rows (layouts:
+// mxfp4.h) and what they stand for; tile chunks of a compressed 16-bit 2:4 matrix; their product Y [T, M].
 int64_t packed_sparse_mxfp4_bytes(int64_t rows, int64_t cols);
 hipError_t launch_quantize_mxfp4(Dt dt, const void* X, int64_t T, int64_t K, uint8_t* codes, uint8_t* exps,
                                  hipStream_t s);

@@ -85,59 +85,57 @@ __device__ __forceinline__ uint32_t largest(const In (&x)[N]) {
   return __float_as_uint(a);
 }
 
-// A thread makes a block of 32 values; blocks past K are zeros up to a multiple of 128.
+// A thread makes a block of 32 values; what lies past K is zero.
 template <typename In>
-__global__ __launch_bounds__(kThreads) void quantize_kernel(const In* __restrict__ X, int64_t T, int64_t K, int64_t padded,
+__global__ __launch_bounds__(kThreads) void quantize_kernel(const In* __restrict__ X, int64_t T, int64_t K,
                                                             uint8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
-  const int64_t per_row = padded / 32, all = T * per_row, stride = (int64_t)gridDim.x * kThreads;
+  const int64_t per_row = mx_scale_bytes(K), coded = mx_code_bytes(K) / 16;
+  const int64_t all = T * per_row, stride = (int64_t)gridDim.x * kThreads;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += stride) {
-    const int64_t t = i / per_row, k = (i - t * per_row) * 32;
+    const int64_t t = i / per_row, block = i - t * per_row, k = block * 32;
     In x[32];
     load_some<32>(X + t * K + (k < K ? k : 0), K - k, x);
     const uint32_t b = scale_byte(largest(x));
     const float s = scale_value(b);
     u32x4 w = {codes8<4>(x, s), codes8<4>(x + 1, s), codes8<4>(x + 2, s), codes8<4>(x + 3, s)};
     if (b == kMxBad) w = u32x4{0u, 0u, 0u, 0u};
-    *reinterpret_cast<u32x4*>(codes + i * 16) = w;
+    if (block < coded) *reinterpret_cast<u32x4*>(codes + (t * coded + block) * 16) = w;
     exps[i] = (uint8_t)b;
   }
 }
 
 // ---------------------------------------------------------------- values
+// A thread makes eight values, a quarter of a block: byte q of each of its four words.
 template <typename O>
 __global__ __launch_bounds__(kThreads) void values_kernel(const uint8_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ exps, int64_t T, int64_t K,
-                                                          int64_t padded, O* __restrict__ out) {
-  const int64_t per_row = (K + 31) / 32, all = T * per_row, stride = (int64_t)gridDim.x * kThreads;
+                                                          O* __restrict__ out) {
+  const int64_t per_row = (K + 7) / 8, all = T * per_row, stride = (int64_t)gridDim.x * kThreads;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += stride) {
-    const int64_t t = i / per_row, k = (i - t * per_row) * 32, at = t * (padded / 32) + k / 32;
-    const u32x4 w = *reinterpret_cast<const u32x4*>(codes + at * 16);
-    const uint32_t b = exps[at];
+    const int64_t t = i / per_row, k = (i - t * per_row) * 8;
+    const u32x4 w = *reinterpret_cast<const u32x4*>(codes + t * mx_code_bytes(K) + k / 32 * 16);
+    const int shift = (int)(k & 24);                 // byte k / 8 % 4
+    const uint32_t b = exps[t * mx_scale_bytes(K) + k / 32];
     const float s = b == kMxBad ? __builtin_nanf("") : scale_value(b);
-    O y[32];
+    Pack<O, 8> y;
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
+    for (int p = 0; p < 4; ++p) {
+      const uint32_t two = w[p] >> shift;
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
+      for (int g = 0; g < 2; ++g) {
         // magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6: the three bits are an exponent of bias 1 and one more bit
-        const uint32_t c = (w[p] >> (4 * g)) & 15u;
-        const float mag = __uint_as_float((c & 7u) << 22) * 0x1p126f;
-        y[4 * g + p] = elem_of<O>((c & 8u ? -mag : mag) * s);
+        const uint32_t c = two >> (4 * g);
+        const float v = __uint_as_float(((c & 7u) << 22) | ((c & 8u) << 28)) * 0x1p126f;
+        y.v[4 * g + p] = elem_of<O>(v * s);
       }
+    }
     O* o = out + t * K + k;
-    constexpr int E = 16 / sizeof(O);
-    if (K - k >= 32) {
-#pragma unroll
-      for (int j = 0; j < 32 / E; ++j) {
-        Pack<O, E> v;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v.v[e] = y[j * E + e];
-        store_pack<O, E>(o + j * E, v);
-      }
+    if (K - k >= 8) {
+      store_pack<O, 8>(o, y);
     } else {
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (k + e < K) o[e] = y[e];
+      for (int e = 0; e < 8; ++e)
+        if (k + e < K) o[e] = y.v[e];
     }
   }
 }
@@ -180,23 +178,21 @@ int64_t packed_sparse_mxfp4_bytes(int64_t rows, int64_t cols) {
 
 hipError_t launch_quantize_mxfp4(Dt dt, const void* X, int64_t T, int64_t K, uint8_t* codes, uint8_t* exps,
                                  hipStream_t s) {
-  const int64_t padded = cdiv(K, kMxCols) * kMxCols;
   if (T == 0 || K == 0) return hipSuccess;
-  const unsigned grid = grid_for(T * padded / 32);
-  if (dt == Dt::BF16) quantize_kernel<<<grid, kThreads, 0, s>>>((const uint16_t*)X, T, K, padded, codes, exps);
-  else if (dt == Dt::F16) quantize_kernel<<<grid, kThreads, 0, s>>>((const _Float16*)X, T, K, padded, codes, exps);
-  else quantize_kernel<<<grid, kThreads, 0, s>>>((const float*)X, T, K, padded, codes, exps);
+  const unsigned grid = grid_for(T * mx_scale_bytes(K));
+  if (dt == Dt::BF16) quantize_kernel<<<grid, kThreads, 0, s>>>((const uint16_t*)X, T, K, codes, exps);
+  else if (dt == Dt::F16) quantize_kernel<<<grid, kThreads, 0, s>>>((const _Float16*)X, T, K, codes, exps);
+  else quantize_kernel<<<grid, kThreads, 0, s>>>((const float*)X, T, K, codes, exps);
   return hipGetLastError();
 }
 
 hipError_t launch_mxfp4_values(Dt out, const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K, void* Y,
                                hipStream_t s) {
-  const int64_t padded = cdiv(K, kMxCols) * kMxCols;
   if (T == 0 || K == 0) return hipSuccess;
-  const unsigned grid = grid_for(T * cdiv(K, 32));
-  if (out == Dt::BF16) values_kernel<<<grid, kThreads, 0, s>>>(codes, exps, T, K, padded, (uint16_t*)Y);
-  else if (out == Dt::F16) values_kernel<<<grid, kThreads, 0, s>>>(codes, exps, T, K, padded, (_Float16*)Y);
-  else values_kernel<<<grid, kThreads, 0, s>>>(codes, exps, T, K, padded, (float*)Y);
+  const unsigned grid = grid_for(T * cdiv(K, 8));
+  if (out == Dt::BF16) values_kernel<<<grid, kThreads, 0, s>>>(codes, exps, T, K, (uint16_t*)Y);
+  else if (out == Dt::F16) values_kernel<<<grid, kThreads, 0, s>>>(codes, exps, T, K, (_Float16*)Y);
+  else values_kernel<<<grid, kThreads, 0, s>>>(codes, exps, T, K, (float*)Y);
   return hipGetLastError();
 }
 

@@ -127,8 +127,9 @@ def test_binding_checks_lists():
 
 
 def test_4_bit_size_queries(lib):
-    assert S.slope_mxfp4_row_bytes(0) == (0, 0) and S.slope_mxfp4_row_bytes(1) == (64, 4)
-    assert S.slope_mxfp4_row_bytes(128) == (64, 4) and S.slope_mxfp4_row_bytes(4999) == (40 * 64, 160)
+    assert S.slope_mxfp4_row_bytes(0) == (0, 0) and S.slope_mxfp4_row_bytes(1) == (64, 16)
+    assert S.slope_mxfp4_row_bytes(128) == (64, 16) and S.slope_mxfp4_row_bytes(4999) == (40 * 64, 160)
+    assert S.slope_mxfp4_row_bytes(513) == (5 * 64, 32)
     assert S.slope_packed_sparse_mxfp4_bytes(27648, 9216) == 432 * 72 * 3328
     assert S.slope_packed_sparse_mxfp4_bytes(300, 272) == 5 * 3 * 3328 and S.slope_packed_sparse_mxfp4_bytes(0, 16) == 0
     for rows, cols in [(4, 8), (4, (1 << 21) + 16), (-1, 16), ((1 << 22) + 1, 16)]:
@@ -148,7 +149,7 @@ def test_4_bit_refusals(lib):
     v = lambda dt=BF16, c=FAKE, e=FAKE, T=4, K=64, o=FAKE: lib.slope_mxfp4_values(dt, c, e, T, K, o, None)
     for f in (q, v):
         assert f(dt=3) == -1 and f(T=-1) == -1 and f(K=-1) == -1 and f(c=None) == -1 and f(e=None) == -1
-        assert f(c=FAKE + 8) == -3 and f(e=FAKE + 2) == -3
+        assert f(c=FAKE + 8) == -3 and f(e=FAKE + 4) == -3
         assert f(T=(1 << 22) + 1) == -6 and f(K=(1 << 22) + 1) == -6
     assert q(X=None) == -1 and q(X=FAKE + 1) == -3 and q(dt=F32, X=FAKE + 2) == -3
     assert v(o=None) == -1 and v(o=FAKE + 1) == -3 and v(dt=F32, o=FAKE + 2) == -3
@@ -164,7 +165,7 @@ def test_4_bit_refusals(lib):
         lib.slope_spmm_mxfp4_packed(dt, c, e, T, K, w, nb, N, Y, None)
     assert y(dt=3) == -1 and y(c=None) == -1 and y(e=None) == -1 and y(w=None) == -1 and y(Y=None) == -1
     assert y(T=-1) == -1 and y(K=-1) == -1 and y(N=-1) == -1 and y(nb=-1) == -1
-    assert y(c=FAKE + 8) == -3 and y(e=FAKE + 1) == -3 and y(w=FAKE + 4) == -3 and y(Y=FAKE + 8) == -3
+    assert y(c=FAKE + 8) == -3 and y(e=FAKE + 8) == -3 and y(w=FAKE + 4) == -3 and y(Y=FAKE + 8) == -3
     assert y(K=24) == -2 and y(N=66) == -2
     assert y(T=(1 << 22) + 1) == -6 and y(N=(1 << 22) + 4) == -6 and y(K=(1 << 21) + 16) == -6
     assert y(nb=3327) == -4
@@ -172,7 +173,7 @@ def test_4_bit_refusals(lib):
 
 def test_binding_checks_4_bit_tensors():
     u8 = torch.uint8
-    x, c, e = torch.zeros(3, 40), torch.zeros(3, 64, dtype=u8), torch.zeros(3, 4, dtype=u8)
+    x, c, e = torch.zeros(3, 40), torch.zeros(3, 64, dtype=u8), torch.zeros(3, 16, dtype=u8)
     with pytest.raises(ValueError, match="GPU memory"):
         S.slope_quantize_mxfp4(x, c, e)
     with pytest.raises(ValueError, match="two dimensions"):
