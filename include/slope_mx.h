@@ -36,7 +36,8 @@ extern "C" {
  *          after 20 random bits are added below the last bit kept (stochastic
  *          rounding); a positive v never becomes zero
  * and with an infinity or a NaN in the block its scale is 255 and its codes are 0.
- * The weights' update uses the moments before they are rounded.
+ * The weights' update uses the moments before they are rounded, with a square root and a
+ * reciprocal within a unit in the last place each (and correctly rounded for eps near 0).
  * The random bits of value j of tensor i are those of a 32-bit word: m takes bits
  * 31..12, v bits 19..0.  With r = low 32 bits of j / 8 and z_i the low 32 bits of
  * SplitMix64 (Steele, Lea and Flood, 2014) at state seed + i * 0x9E3779B97F4A7C15,

@@ -129,10 +129,8 @@ _SIGS_INT8 = {
 EXPORTED_SYMBOLS_INT8 = tuple(_SIGS_INT8)
 
 # include/slope_mx.h
-_P_I32, _P_VP = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(_vp)
 _SIGS_MX = {
-    "slope_adamw_multi": (_i32, [_i32, _i64, _P_I32, _P_I32, _P_VP, _P_VP, _P_VP, _P_VP, _P_VP, _P_VP, _P_I64, _P_HP,
-                                 ctypes.c_uint64, _vp]),
+    "slope_adamw_multi": (_i32, [_i32, _i64, *[_vp] * 9, _P_HP, ctypes.c_uint64, _vp]),
     "slope_adamw_moments": (_i32, [_i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
     "slope_mxfp4_row_bytes": (_i32, [_i64, _P_I64, _P_I64]),
     "slope_quantize_mxfp4": (_i32, [_i32, _vp, _i64, _i64, _vp, _vp, _vp]),
@@ -748,27 +746,41 @@ def slope_adamw_multi(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps
     if not len(grads) == len(m) == len(v) == len(mes) == len(ves) == count:
         raise ValueError("the lists must have the same length")
     dev, mdt = params[0].get_device(), _u8 if eight else _f32t
-    sizes = []
+    words = [[] for _ in range(6 if eight else 4)]     # addresses of each list, one array for all of them
+    to_p, to_g, to_m, to_v = (w.append for w in words[:4])
+    sizes, codes = [], []
     for i in range(count):
         p, g, a, b = params[i], grads[i], m[i], v[i]
         n = p.numel()
-        if not (g.numel() == a.numel() == b.numel() == n and a.dtype is mdt and b.dtype is mdt and p.dtype in _CODES
-                and g.dtype in _CODES and p.is_contiguous() and g.is_contiguous() and a.is_contiguous()
-                and b.is_contiguous() and p.get_device() == g.get_device() == a.get_device() == b.get_device() == dev):
+        pc, gc = _CODES.get(p.dtype), _CODES.get(g.dtype)
+        if not (g.numel() == n and a.numel() == n and b.numel() == n and a.dtype is mdt and b.dtype is mdt
+                and pc is not None and gc is not None and p.is_contiguous() and g.is_contiguous() and a.is_contiguous()
+                and b.is_contiguous() and p.get_device() == dev and g.get_device() == dev and a.get_device() == dev
+                and b.get_device() == dev):
             _multi_refuse(i, p, g, a, b, mes[i] if eight else None, ves[i] if eight else None, dev, mdt)
         if eight:
             x, y = mes[i], ves[i]
-            if not (x.numel() == y.numel() == -(-n // MX_BLOCK) and x.dtype is _u8 and y.dtype is _u8
-                    and x.is_contiguous() and y.is_contiguous() and x.get_device() == y.get_device() == dev):
+            k = -(-n // MX_BLOCK)
+            if not (x.numel() == k and y.numel() == k and x.dtype is _u8 and y.dtype is _u8 and x.is_contiguous()
+                    and y.is_contiguous() and x.get_device() == dev and y.get_device() == dev):
                 _multi_refuse(i, p, g, a, b, x, y, dev, mdt)
+            words[4].append(x.data_ptr())
+            words[5].append(y.data_ptr())
+        to_p(p.data_ptr())
+        to_g(g.data_ptr())
+        to_m(a.data_ptr())
+        to_v(b.data_ptr())
         sizes.append(n)
-    ptrs, codes = _vp * count, ctypes.c_int32 * count
-    addresses = lambda ts: ptrs(*[t.data_ptr() for t in ts])
+        codes.append(pc)
+        codes.append(gc)
+    table = (_i64 * (count * (len(words) + 1)))(*sizes, *[a for w in words for a in w])
+    kinds = (ctypes.c_int32 * (2 * count))(*codes[0::2], *codes[1::2])
+    at, kind_at = ctypes.addressof(table), ctypes.addressof(kinds)
+    lists = [at + 8 * count * (1 + k) for k in range(len(words))]
     hp = _hp(step, lr, beta1, beta2, eps, weight_decay)
-    _on_device("slope_adamw_multi", dev, stream, 8 if eight else 32, count, codes(*[_CODES[p.dtype] for p in params]),
-               codes(*[_CODES[g.dtype] for g in grads]), addresses(params), addresses(grads), addresses(m), addresses(v),
-               addresses(mes) if eight else None, addresses(ves) if eight else None, (_i64 * count)(*sizes),
-               ctypes.byref(hp), int(seed) & (2 ** 64 - 1))
+    _on_device("slope_adamw_multi", dev, stream, 8 if eight else 32, count, kind_at, kind_at + 4 * count, *lists[:4],
+               lists[4] if eight else None, lists[5] if eight else None, at, ctypes.byref(hp),
+               int(seed) & (2 ** 64 - 1))
 
 
 def slope_adamw_moments(m, m_exp, v, v_exp, m_out=None, v_out=None, stream=None) -> None:
@@ -781,8 +793,14 @@ def slope_adamw_moments(m, m_exp, v, v_exp, m_out=None, v_out=None, stream=None)
     out = m_out if m_out is not None else v_out
     odt = _f32t if out is None else out.dtype
     blocks = -(-n // MX_BLOCK)
-    flat = lambda t, name, size, dtype: None if t is None else _arg(t.view(-1) if t.is_contiguous() else t, name, (size,),
-                                                                    dtype, d)
+
+    def flat(t, name, size, dtype):
+        if t is None:
+            return None
+        if t.dtype is dtype and t.numel() == size and t.get_device() == d and t.is_contiguous():
+            return t.data_ptr() or 256             # no elements: never dereferenced
+        return _arg(t.reshape(-1) if t.is_contiguous() else t, name, (size,), dtype, d)
+
     _on_device("slope_adamw_moments", d, stream, _code(odt), flat(m, "m", n, _u8), flat(m_exp, "m_exp", blocks, _u8),
                flat(v, "v", n, _u8), flat(v_exp, "v_exp", blocks, _u8), n, flat(m_out, "m_out", n, odt),
                flat(v_out, "v_out", n, odt))

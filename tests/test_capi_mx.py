@@ -37,8 +37,8 @@ def _multi(lib, bits=8, count=2, pdt=(BF16, F32), gdt=(BF16, F32), p=(FAKE, 2 * 
     vp = lambda a: None if a is None else (ctypes.c_void_p * len(a))(*a)
     i32 = lambda a: None if a is None else (ctypes.c_int32 * len(a))(*a)
     h = None if hp is None else ctypes.byref(S.AdamWParams(*hp))
-    return lib.slope_adamw_multi(bits, count, i32(pdt), i32(gdt), vp(p), vp(g), vp(m), vp(v), vp(me), vp(ve),
-                                 None if n is None else (ctypes.c_int64 * len(n))(*n), h, 0, None)
+    arrays = [i32(pdt), i32(gdt), vp(p), vp(g), vp(m), vp(v), vp(me), vp(ve), None if n is None else (ctypes.c_int64 * len(n))(*n)]
+    return lib.slope_adamw_multi(bits, count, *[None if a is None else ctypes.addressof(a) for a in arrays], h, 0, None)
 
 
 def test_adamw_multi_refusals(lib):

@@ -225,6 +225,34 @@ def test_special_values_stay_in_their_block():
     assert list(a.me[0][:2].cpu()) == [255, 255] and list(a.ve[0][:3].cpu()) == [255] * 3
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-15, 1e-12])
+def test_steps_with_little_eps(eps):
+    """Gradients down to where v is no normal number: every step follows the formula, and is a NaN where
+    that is 0 / 0."""
+    n, lr = 64 * 9, 2e-3
+    a = Lists([n, n], ["f32"] * 2, ["f32"] * 2, 10, True)
+    for t in a.m + a.v + a.me + a.ve:
+        t.zero_()
+    a.g[0].copy_(torch.logspace(-12, 17, n, device="cuda"))
+    a.g[1].copy_(torch.logspace(-19, -12, n, device="cuda"))
+    a.g[1][:64] = 0.0
+    for p in a.p:
+        p.zero_()
+    a.call(1, seed=1, lr=lr, eps=eps, weight_decay=0.0)
+    for p, g in zip(a.p, a.g):
+        g = g.double()
+        v = 1e-3 * g * g
+        # v is off by half a step of the subnormal numbers at most, twice (g g and 1e-3 g g), so its root
+        # relatively by 2^-149 / v; the other operations by a few units of 2^-24, counted as 2^-20
+        want = -lr * g / (g + eps)
+        bad = g == 0
+        assert torch.equal(p.isnan(), bad & (eps == 0.0))
+        ok = (p.double() - want).abs() <= want.abs() * (2.0 ** -20 + 2.0 * 2.0 ** -149 / v)
+        assert ok[~bad].all()
+        if eps:
+            assert not p[bad].any()
+
+
 def test_all_codes_and_scales_as_values():
     codes = torch.arange(256, dtype=torch.int16).to(U8).repeat(256)
     exps = torch.arange(256, dtype=torch.int16).to(U8).repeat_interleave(8)
