@@ -313,6 +313,42 @@ def test_far_scales():
     assert np.all(np.abs(host_f64(y[1:]) - want) <= (K / 64 + 17) * 2.0 ** -23 * mass + 2.0 ** -149)
 
 
+@pytest.mark.parametrize("T,K", [(100003, 1), (70001, 33), (9973, 513), (4099, 2049), (65537, 40), (1031, 20479)])
+def test_many_rows(T, K):
+    """Row numbers come from a multiplication: every row of awkward widths, in both directions."""
+    say(f"[mxfp4 rows] T={T} K={K}")
+    x = torch.arange(T, device="cuda")[:, None] * 7 + torch.arange(K, device="cuda")[None, :] * 3
+    x = ((x % 13) - 6).float().clamp(-6, 6)
+    x[x.abs() == 5] = 4.0                                              # E2M1 numbers, and every block has few others
+    codes, exps = quantize(x)
+    y = torch.full_like(x, 9.0)
+    S.slope_mxfp4_values(codes, exps, y)
+    top = 32 * (K // 32)                                               # whole blocks hold a 6 or a 4, 2^0 either way
+    assert torch.equal(x[:, :top], y[:, :top])
+    assert ((x - y).abs() <= x.abs() / 6).all()
+    z = torch.empty((T, K), dtype=torch.bfloat16, device="cuda")
+    S.slope_mxfp4_values(codes, exps, z)
+    assert torch.equal(z.float(), y)
+
+
+def test_values_of_more_items_than_a_launch_takes():
+    T, K = 524291, 16384                                               # 2^30 items of eight values are 524288 rows
+    say(f"[mxfp4_values] T={T} K={K}")
+    nc, ne = S.slope_mxfp4_row_bytes(K)
+    codes = torch.zeros((T, nc), dtype=U8, device="cuda")
+    exps = torch.full((T, ne), 127, dtype=U8, device="cuda")
+    rows = [0, 1, T // 2, 524286, 524287, 524288, 524289, T - 1]
+    c, e = quantize(torch.randn((len(rows), K), device="cuda"))
+    codes[rows], exps[rows] = c, e
+    y = torch.full((T, K), 3.0, dtype=torch.bfloat16, device="cuda")
+    S.slope_mxfp4_values(codes, exps, y)
+    want = torch.empty((len(rows), K), dtype=torch.bfloat16, device="cuda")
+    S.slope_mxfp4_values(c, e, want)
+    assert torch.equal(y[rows], want) and want.any()
+    y[rows] = 0
+    assert not y.view(torch.int16).any()
+
+
 def test_offsets_past_31_bits():
     """Codes, chunks and outputs of more than 2^31 bytes, sampled."""
     T, K, N = 300000, 16384, 64                                        # 2.46 GB of codes
