@@ -467,8 +467,8 @@ __global__ __launch_bounds__(G::THREADS, 1) void tiles_mxfp4_kernel(const uint8_
 // 1600.  One barrier a stage; a stage's reads of the weight run one stage ahead of its
 // products and the loads three.
 //
-// Measured, 8192 x 9216 x 9216 bf16: 335 to 352 us with the clock that the card holds
-// (1.87 GHz): products and barriers alone 250 to 270, without the loads 344 of 386, without the
+// Measured, 8192 x 9216 x 9216 bf16: 335 to 347 us with the clock that the card holds
+// (1.87 GHz, 51 % of the matrix rate): products and barriers alone 250 to 270, without the loads 344 of 386, without the
 // reads 331, without the products 248, without the expansion 338 (timing copies on one
 // card).  Two groups of four waves half a stage apart, one reading while the other
 // multiplies: 336 to 358; four waves of 128 x 128: 373.
@@ -633,7 +633,7 @@ __device__ __forceinline__ void woven_tile(char* lds, const uint8_t* codes, cons
       constexpr int READS = 2 * G::FT + G::FM;
 #pragma unroll
       for (int q = 0; q < READS; ++q) {
-        if (q * NM / READS != i) continue;
+        if (q * (NM - 2) / READS != i) continue;     // (all under way two products before the barrier)
         if (q < G::FT) b0[q] = *reinterpret_cast<const u32x4*>(lds + (next + b0_at) + q * 2048);
         else if (q < G::FT + G::FM) then.sa[q - G::FT] = *reinterpret_cast<const uint16_t*>(lds + (next + scale_at) + (q - G::FT) * 128);
         else then.sb[q - G::FT - G::FM] = *reinterpret_cast<const uint16_t*>(x + (q - G::FT - G::FM) * 512);
@@ -646,8 +646,11 @@ __device__ __forceinline__ void woven_tile(char* lds, const uint8_t* codes, cons
 #pragma unroll
     for (int fm = 0; fm < G::FM; ++fm) anchor(w0[fm]);
     now = then;
-    wait_lgkmcnt0();                                 // this wave's reads of the stage are complete
-    wait_older(load + 1);                            // and its share of stage s + 2 is there
+    // This wave's reads of the stage's slot, which is filled next, are complete without a wait: their
+    // values were operands of the products above, each of which is anchored before this.  What is still
+    // under way comes from the next slot.
+    compiler_fence();
+    wait_older(load + 1);                            // the wave's share of stage s + 2 is there
     barrier();
     compiler_fence();
     refill = cur;
@@ -766,28 +769,31 @@ hipError_t few_go(const Args<O>& a) {
 }
 
 // Any number of tokens.  Above 64, four kernels by their estimated time in units of a
-// stage (us for 128 k), fitted to sweeps of 65 .. 8192 tokens over 9216 -> 9216 / 27648,
-// 20480 -> 5120, 5120 -> 5120, 4096 -> 1024 and 768 -> 2304:
+// stage (us for 128 k), fitted to sweeps of 65 .. 8192 tokens over the shapes below:
 //   large   0.0103 a unit of full_width_rows' cost (100 a round of full tiles, 65 of half tiles)
 //   wide    256 x 128 tiles of four waves: 0.60 a round
-//   mid     128 x 64 tiles: 0.13 + 0.205 a tile of each compute unit, 0.35 at least
+//   mid     128 x 64 tiles: 0.13 + 0.205 a tile of each compute unit, 0.38 at least
 //   direct  the few-token kernel over groups of 64 tokens: 0.10 + 0.14 a block of 64 rows of each
 //           unit; 32 rows up to 128 such blocks (4096 -> 1024 at 512 tokens 6.6 us, with 64 8.5)
-// Measured, us (large / wide / mid / direct), the rule's choice starred:
-//   9216 -> 9216    128 tokens  47.9 /  45.3 /  26.5 /  20.0*
-//                   256         47.9 /  45.3 /  30.3*/  32.3
-//                   512         47.9 /  46.0 /  42.5*/  50.3
-//                  1000         64.0*/  82.9 /  75.8
-//                  8192        352 * / 405   / 533
-//   20480 -> 5120   256         95   /  90.9 /  54.6 /  36.2*
-//                   512         95   /  90.0 /  61.4*/  62.6
-//                  1000         95.0 /  86.4*/  91.7
-//                  2048        128 * / 173   / 172
-//   9216 -> 27648    65         53   /  40.5 /  34.0*/  37
-//                   256         53.3 /  49.7*/  75.0
-//   5120 -> 5120    256         25   /  24   /  16.3 /  13.7*
-//                  1000         27.7 /  26.4*/  27.9
-//   768 -> 2304    1000          9.8 /  10.3 /   6.7*
+// Measured, us (large / wide / mid / direct, the weight from HBM), the rule's choice starred:
+//   9216 -> 9216    128 tokens  47.8 /  45.3 /  29.2 /  20.1*
+//                   256         47.3 /  45.5 /  33.0*/  32.3
+//                   512         47.8 /  45.9 /  43.5*/  49.1
+//                  1000         61.4*/  82.2 /  77.9 /  81.3
+//                  8192        350 * / 392   / 535
+//   20480 -> 5120    65         89.4 /  81.1 /  59.3 /  26.4*
+//                   256         98.6 /  91.1 /  59.6 /  36.7*
+//                   512         96.3 /  90.4 /  68.7*/  61.7
+//                  1000         95.0 /  86.5*/  93.7 /  97.6
+//                  2048        130.6*/ 170.6 / 170.2 / 180.9
+//   9216 -> 27648    65         44.0 /  40.6 /  38.6*/  40.7
+//                   256         51.5 /  49.1*/  76.3 /  76.8
+//                   512         72.2*/  93.2 / 121.5 / 139.8
+//   5120 -> 5120    256         29.1 /  28.8 /  18.0 /  13.9*
+//                  1000         28.6 /  26.8*/  27.6 /  31.7
+//   4096 -> 1024   1000         22.6 /  21.4 /  15.3 /   9.1*
+//                  2048         23.3 /  21.7 /  16.0 /  13.8*
+//   768 -> 2304    1000          9.3 /   9.6 /   7.1*/  10.0
 // (The few-token kernel holds all of a group's scales in LDS: 64 tokens up to K = 49152.)
 template <typename O>
 hipError_t spmm_launch(const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K, const void* packed, int64_t M,
@@ -802,7 +808,7 @@ hipError_t spmm_launch(const uint8_t* codes, const uint8_t* exps, int64_t T, int
   const double large = 0.0103 * (100 * (double)cdiv(rows_full * cols, (int64_t)cus) +
                                  65 * (double)cdiv((rows - rows_full) * halves, (int64_t)cus));
   const double wide = 0.60 * (double)cdiv(rows * halves, (int64_t)cus);
-  const double mid = std::max(0.35, 0.13 + 0.205 * (double)(cdiv(M, Mid::BM) * cdiv(T, Mid::BT)) / cus);
+  const double mid = std::max(0.38, 0.13 + 0.205 * (double)(cdiv(M, Mid::BM) * cdiv(T, Mid::BT)) / cus);
   const int64_t blocks = cdiv(M, 64) * cdiv(T, 64);
   const double direct = 0.10 + 0.14 * (double)blocks / cus;
   if (fits && direct <= mid && direct <= wide && direct <= large)
