@@ -19,6 +19,7 @@ Tensor conventions (see include/slope.h):
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch
@@ -707,8 +708,12 @@ MX_BLOCK = 32               # SLOPE_MX_BLOCK
 _u8 = torch.uint8
 
 
+_numel, _data_ptr, _get_device = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.get_device
+_is_contiguous, _dtype_of = torch.Tensor.is_contiguous, operator.attrgetter("dtype")
+
+
 def _multi_refuse(i, p, g, m, v, me, ve, dev, mdt):
-    """Raises what tensor i of a list is refused for."""
+    """Raises what tensor i of a list is refused for, if it is."""
     n = p.numel()
     for name, t in (("params", p), ("grads", g), ("m", m), ("v", v), ("m_exp", me), ("v_exp", ve)):
         if t is None:
@@ -725,7 +730,6 @@ def _multi_refuse(i, p, g, m, v, me, ve, dev, mdt):
     for name, t, dtype in (("m", m, mdt), ("v", v, mdt), ("m_exp", me, _u8), ("v_exp", ve, _u8)):
         if t is not None and t.dtype is not dtype:
             raise TypeError(f"{name}[{i}] must be {dtype}, got {t.dtype}")
-    raise ValueError(f"tensor {i} of the lists is not accepted")
 
 
 def slope_adamw_multi(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, m_exp=None,
@@ -745,38 +749,28 @@ def slope_adamw_multi(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps
         raise ValueError("8-bit moments need both m_exp and v_exp")
     if not len(grads) == len(m) == len(v) == len(mes) == len(ves) == count:
         raise ValueError("the lists must have the same length")
+    # one pass over all the tensors for each question (7 tensors of 8-bit state: 22 us tensor by tensor)
+    every = [*params, *grads, *m, *v]
+    scales = [*m_exp, *v_exp] if eight else []
     dev, mdt = params[0].get_device(), _u8 if eight else _f32t
-    words = [[] for _ in range(6 if eight else 4)]     # addresses of each list, one array for all of them
-    to_p, to_g, to_m, to_v = (w.append for w in words[:4])
-    sizes, codes = [], []
-    for i in range(count):
-        p, g, a, b = params[i], grads[i], m[i], v[i]
-        n = p.numel()
-        pc, gc = _CODES.get(p.dtype), _CODES.get(g.dtype)
-        if not (g.numel() == n and a.numel() == n and b.numel() == n and a.dtype is mdt and b.dtype is mdt
-                and pc is not None and gc is not None and p.is_contiguous() and g.is_contiguous() and a.is_contiguous()
-                and b.is_contiguous() and p.get_device() == dev and g.get_device() == dev and a.get_device() == dev
-                and b.get_device() == dev):
-            _multi_refuse(i, p, g, a, b, mes[i] if eight else None, ves[i] if eight else None, dev, mdt)
-        if eight:
-            x, y = mes[i], ves[i]
-            k = -(-n // MX_BLOCK)
-            if not (x.numel() == k and y.numel() == k and x.dtype is _u8 and y.dtype is _u8 and x.is_contiguous()
-                    and y.is_contiguous() and x.get_device() == dev and y.get_device() == dev):
-                _multi_refuse(i, p, g, a, b, x, y, dev, mdt)
-            words[4].append(x.data_ptr())
-            words[5].append(y.data_ptr())
-        to_p(p.data_ptr())
-        to_g(g.data_ptr())
-        to_m(a.data_ptr())
-        to_v(b.data_ptr())
-        sizes.append(n)
-        codes.append(pc)
-        codes.append(gc)
-    table = (_i64 * (count * (len(words) + 1)))(*sizes, *[a for w in words for a in w])
-    kinds = (ctypes.c_int32 * (2 * count))(*codes[0::2], *codes[1::2])
+    sizes = list(map(_numel, every))
+    of = sizes[:count]
+    dtypes = list(map(_dtype_of, every))
+    codes = list(map(_CODES.get, dtypes[:2 * count]))
+    everything = every + scales
+    blocks = [-(-n // MX_BLOCK) for n in of]
+    if not (sizes == of * 4 and None not in codes and dtypes[2 * count:].count(mdt) == 2 * count
+            and all(map(_is_contiguous, everything)) and set(map(_get_device, everything)) == {dev}
+            and (not eight or (list(map(_numel, scales)) == blocks * 2
+                               and list(map(_dtype_of, scales)).count(_u8) == 2 * count))):
+        for i in range(count):
+            _multi_refuse(i, params[i], grads[i], m[i], v[i], mes[i] if eight else None, ves[i] if eight else None, dev,
+                          mdt)
+        raise ValueError("the lists are not accepted")
+    table = (_i64 * (len(everything) + count))(*of, *map(_data_ptr, everything))
+    kinds = (ctypes.c_int32 * (2 * count))(*codes)
     at, kind_at = ctypes.addressof(table), ctypes.addressof(kinds)
-    lists = [at + 8 * count * (1 + k) for k in range(len(words))]
+    lists = [at + 8 * count * (1 + k) for k in range(6 if eight else 4)]
     hp = _hp(step, lr, beta1, beta2, eps, weight_decay)
     _on_device("slope_adamw_multi", dev, stream, 8 if eight else 32, count, kind_at, kind_at + 4 * count, *lists[:4],
                lists[4] if eight else None, lists[5] if eight else None, at, ctypes.byref(hp),
