@@ -57,7 +57,7 @@ extern "C" {
  * the call's own: a call recorded into a graph repeats them at each replay.
  * Errors: slope_adamw's, and SLOPE_ERR_INVALID_ARG for other state_bits, count < 0
  * or two of the written tensors that share memory; SLOPE_ERR_ALIGN for a tensor not
- * aligned to its elements. */
+ * aligned to its elements; SLOPE_ERR_UNSUPPORTED for n[i] > 2^34. */
 slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* param_dt, const int32_t* grad_dt,
                                void* const* params, const void* const* grads, void* const* m, void* const* v,
                                uint8_t* const* m_exp, uint8_t* const* v_exp, const int64_t* n,
@@ -68,7 +68,7 @@ slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* par
  * hold every value exactly (bfloat16 has four significant bits to spare).  Either
  * moment may be left out: its three arguments are NULL.  Any alignment of the codes;
  * outputs need their element's.  Errors: SLOPE_ERR_INVALID_ARG for an incomplete
- * moment or none, SLOPE_ERR_UNSUPPORTED for F16 or n > 2^40. */
+ * moment or none, SLOPE_ERR_UNSUPPORTED for F16 or n > 2^34. */
 slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, const uint8_t* m_exp_or_null,
                                  const uint8_t* v_or_null, const uint8_t* v_exp_or_null, int64_t n,
                                  void* m_out_or_null, void* v_out_or_null, void* stream);

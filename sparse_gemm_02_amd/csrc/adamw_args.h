@@ -8,6 +8,7 @@
 namespace slope {
 
 constexpr int64_t kAdamwMaxElems = int64_t(1) << 40;
+constexpr int64_t kMultiMaxElems = int64_t(1) << 34;   // of a tensor, eight values a thread: below 2^32 threads
 
 // Checks AdamW hyper-parameters and derives the per-update fp32 constants.
 inline slope_status adamw_step(const slope_adamw_params* hp, AdamWStep* c) {

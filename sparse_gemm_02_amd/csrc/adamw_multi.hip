@@ -35,30 +35,31 @@ struct MultiArgs {
   int64_t n[kTensors];
   uint32_t first[kTensors];                          // first block of the tensor
   uint32_t seed[kTensors];
-  int32_t count, slices;                             // tensors; slices of a block
+  int32_t count;
 };
 static_assert(sizeof(MultiArgs) + sizeof(AdamWStep) <= 4096, "kernel arguments");
 
-// Eight values from p on, of which `left` are there (the others read as zero).
+// Eight values e .. e + 7 of the n at p (those that are not there read as zero, and e may
+// be negative).
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int64_t left, float (&out)[8]) {
-  if (left >= 8) {
-    const Pack<T, 8> x = load_pack<T, 8>(p);
+__device__ __forceinline__ void load8(const T* p, int64_t e, int64_t n, float (&out)[8]) {
+  if (e >= 0 && e + 8 <= n) {
+    const Pack<T, 8> x = load_pack<T, 8>(p + e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[i] = elem_f32(x.v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = i < left ? elem_f32(p[i]) : 0.0f;
+    for (int i = 0; i < 8; ++i) out[i] = (uint64_t)(e + i) < (uint64_t)n ? elem_f32(p[e + i]) : 0.0f;
   }
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, int64_t left, const Pack<T, 8>& x) {
-  if (left >= 8) {
-    store_pack<T, 8>(p, x);
+__device__ __forceinline__ void store8(T* p, int64_t e, int64_t n, const Pack<T, 8>& x) {
+  if (e >= 0 && e + 8 <= n) {
+    store_pack<T, 8>(p + e, x);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = x.v[i];
+      if ((uint64_t)(e + i) < (uint64_t)n) p[e + i] = x.v[i];
   }
 }
 // The eight values rounded to their format.
@@ -206,8 +207,8 @@ __device__ __forceinline__ void encode(const float (&m)[8], const float (&v)[8],
 // ---------------------------------------------------------------- the step
 // adamw_apply with the hardware's square root and reciprocal, each within a unit in the
 // last place (the moments, whose bits decide codes, are computed the same way).  With the
-// correctly rounded ones the 8-bit step is bound by the vector units: 160 million bf16
-// values 348 us, so 309 (5.25 TB/s, a copy's rate).
+// correctly rounded ones the 8-bit step of 16-bit weights is bound by the vector units:
+// 160 million bf16 values 328 us, so 308; of fp32 ones 480 either way.
 __device__ __forceinline__ float adamw_apply_fast(float p, float g, float& m, float& v, const AdamWStep& c) {
 #pragma clang fp contract(off)
   m = __builtin_fmaf(c.beta1, m, c.omb1 * g);
@@ -224,8 +225,17 @@ __device__ __forceinline__ Pack<PT, 8> step8(float (&p)[8], const float (&g)[8],
   return rounded8<PT>(p);
 }
 
-// A block takes `slices` slices of 2048 values of one tensor; a thread eight
-// values of each.  Four lanes hold a block of 32.
+// Values by which m's start is past a 32-byte border: with fp32 moments a thread's eight
+// values begin there, since tensors that follow each other in one buffer begin anywhere
+// (6 million fp32 values at an odd place 34 us, from the tensor's first value on 40; even
+// aligned tensors gained 6 %, having one test for all eight values).
+__host__ __device__ __forceinline__ int lead32(const void* m) { return (int)(reinterpret_cast<uintptr_t>(m) / 4 % 8); }
+
+// A block of threads takes 2048 values of one tensor, a thread eight of them; four lanes
+// hold a block of 32.  Bound by memory: 160 million bf16 weights and gradients with 8-bit
+// moments 292 to 308 us (10.1 bytes a value read and written, 5.3 to 5.6 TB/s; a copy
+// reaches 5.1), with fp32 moments 635 (22 bytes, 5.6).  Two or four such parts a block of
+// threads take 3 to 4 % longer from 2^24 values on and nothing less below.
 template <typename PT, typename GT, bool EIGHT, bool FAST>
 __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const MultiArgs a, const AdamWStep c0) {
   int lo = 0, hi = a.count;                          // the last tensor whose first block is not behind this one
@@ -236,75 +246,72 @@ __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const MultiArgs a
   const int64_t n = a.n[lo];
   PT* p = (PT*)a.p[lo];
   const GT* g = (const GT*)a.g[lo];
-  int64_t e = (int64_t)(blockIdx.x - a.first[lo]) * ((int64_t)a.slices * kSlice) + threadIdx.x * kPerThread;
-  for (int u = 0; u < a.slices; ++u, e += kSlice) {
-    if (e - threadIdx.x * kPerThread >= n) return;   // the same for the whole block
-    const int64_t left = n - e;
-    const int64_t at = left > 0 ? e : 0;             // lanes past the end: no access, zeros
-    float pf[8], gf[8], mf[8], vf[8];
-    load8(p + at, left, pf);
-    load8(g + at, left, gf);
-    AdamWStep c = c0;
-    if constexpr (EIGHT) {
-      uint8_t* m = (uint8_t*)a.m[lo];
-      uint8_t* v = (uint8_t*)a.v[lo];
-      const int64_t block = at / 32;
-      const uint32_t em = left > 0 ? a.me[lo][block] : 0u, ev = left > 0 ? a.ve[lo][block] : 0u;
-      decode_m(load_codes(m + at, left), em, mf);
-      decode_v(load_codes(v + at, left), ev, vf);
-      if (ev == (uint32_t)kBadExp) c.beta2 = nan_f32();   // every v of the block is a NaN
-      const Pack<PT, 8> np = step8<PT, FAST>(pf, gf, mf, vf, c);
-      if (left < 8) {                                // nothing is there: no part of the block's largest
+  int64_t e = (int64_t)(blockIdx.x - a.first[lo]) * kSlice + threadIdx.x * kPerThread;
+  float pf[8], gf[8], mf[8], vf[8];
+  AdamWStep c = c0;
+  if constexpr (EIGHT) {
+    load8(p, e, n, pf);
+    load8(g, e, n, gf);
+    const int64_t left = n - e, at = left > 0 ? e : 0, block = at / 32;   // lanes past the end: no access, zeros
+    uint8_t* m = (uint8_t*)a.m[lo];
+    uint8_t* v = (uint8_t*)a.v[lo];
+    const uint32_t em = left > 0 ? a.me[lo][block] : 0u, ev = left > 0 ? a.ve[lo][block] : 0u;
+    decode_m(load_codes(m + at, left), em, mf);
+    decode_v(load_codes(v + at, left), ev, vf);
+    if (ev == (uint32_t)kBadExp) c.beta2 = nan_f32();   // every v of the block is a NaN
+    const Pack<PT, 8> np = step8<PT, FAST>(pf, gf, mf, vf, c);
+    if (left < 8) {                                  // nothing is there: no part of the block's largest
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i >= left) mf[i] = vf[i] = 0.0f;
-      }
-      const uint32_t nm = scale_byte(__float_as_uint(block_max(mf)), kTopM);
-      const uint32_t nv = scale_byte(__float_as_uint(block_max(vf)), kTopV);
-      u32x2 cm, cv;
-      encode(mf, vf, nm, nv, Noise((uint32_t)(e / 8), a.seed[lo]), cm, cv);
-      if (left > 0) {
-        store_codes(m + at, left, cm);
-        store_codes(v + at, left, cv);
-        if (threadIdx.x % 4 == 0) {
-          a.me[lo][block] = (uint8_t)nm;
-          a.ve[lo][block] = (uint8_t)nv;
-        }
-      }
-      store8(p + at, left, np);
-    } else {
-      float* m = (float*)a.m[lo];
-      float* v = (float*)a.v[lo];
-      load8(m + at, left, mf);
-      load8(v + at, left, vf);
-      const Pack<PT, 8> np = step8<PT, FAST>(pf, gf, mf, vf, c);
-      store8(m + at, left, rounded8<float>(mf));
-      store8(v + at, left, rounded8<float>(vf));
-      store8(p + at, left, np);
+      for (int i = 0; i < 8; ++i)
+        if (i >= left) mf[i] = vf[i] = 0.0f;
     }
+    const uint32_t nm = scale_byte(__float_as_uint(block_max(mf)), kTopM);
+    const uint32_t nv = scale_byte(__float_as_uint(block_max(vf)), kTopV);
+    u32x2 cm, cv;
+    encode(mf, vf, nm, nv, Noise((uint32_t)(e / 8), a.seed[lo]), cm, cv);
+    if (left > 0) {
+      store_codes(m + at, left, cm);
+      store_codes(v + at, left, cv);
+      if (threadIdx.x % 4 == 0) {
+        a.me[lo][block] = (uint8_t)nm;
+        a.ve[lo][block] = (uint8_t)nv;
+      }
+    }
+    store8(p, e, n, np);
+  } else {
+    float* m = (float*)a.m[lo];
+    float* v = (float*)a.v[lo];
+    e -= lead32(m);
+    load8(p, e, n, pf);
+    load8(g, e, n, gf);
+    load8(m, e, n, mf);
+    load8(v, e, n, vf);
+    const Pack<PT, 8> np = step8<PT, FAST>(pf, gf, mf, vf, c);
+    store8(m, e, n, rounded8<float>(mf));
+    store8(v, e, n, rounded8<float>(vf));
+    store8(p, e, n, np);
   }
 }
 
-// The values that 8-bit codes stand for.  n values, each thread eight of one moment.
+// The values that 8-bit codes stand for.  n values, each thread eight of one moment:
+// 160 million of both as bf16 163 us, 5.9 TB/s (178 with blocks that loop).
 template <typename O, bool V>
 __device__ __forceinline__ void values8(const uint8_t* codes, const uint8_t* exps, int64_t n, O* out) {
-  const int64_t stride = (int64_t)gridDim.x * kSlice;
-  for (int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kPerThread; e < n; e += stride) {
-    const int64_t left = n - e;
-    const uint32_t b = exps[e / 32];
-    const u32x2 w = load_codes(codes + e, left);
-    float f[8];
-    if constexpr (V) {
-      decode_v(w, b, f);
-      if (b == (uint32_t)kBadExp) {
+  const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kPerThread, left = n - e;
+  if (left <= 0) return;
+  const uint32_t b = exps[e / 32];
+  const u32x2 w = load_codes(codes + e, left);
+  float f[8];
+  if constexpr (V) {
+    decode_v(w, b, f);
+    if (b == (uint32_t)kBadExp) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = nan_f32();
-      }
-    } else {
-      decode_m(w, b, f);
+      for (int i = 0; i < 8; ++i) f[i] = nan_f32();
     }
-    store8(out + e, left, rounded8<O>(f));
+  } else {
+    decode_m(w, b, f);
   }
+  store8(out, e, n, rounded8<O>(f));
 }
 template <typename O>
 __global__ __launch_bounds__(kThreads) void moments_kernel(const uint8_t* __restrict__ m, const uint8_t* __restrict__ me,
@@ -353,12 +360,9 @@ hipError_t launch_adamw_multi(bool eight, const AdamWTensors& t, const AdamWStep
     for (int64_t i = 0; i < t.count; ++i)
       if (t.param_dt[i] == pd && t.grad_dt[i] == gd) total += t.n[i];
     if (total == 0) continue;
-    // few values: a slice a block, so that they spread over the device
-    const int64_t slices = total >= (int64_t)1 << 24 ? 4 : 1;
     MultiArgs a;
     int64_t blocks = 0;
     a.count = 0;
-    a.slices = (int32_t)slices;
     auto flush = [&]() {
       if (a.count == 0) return hipSuccess;
       const hipError_t e = launch_one((Dt)pd, (Dt)gd, eight, fast, a, (unsigned)blocks, c, s);
@@ -366,10 +370,11 @@ hipError_t launch_adamw_multi(bool eight, const AdamWTensors& t, const AdamWStep
       blocks = 0;
       return e;
     };
-    constexpr int64_t kMaxBlocks = int64_t(1) << 30;
+    constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;   // below 2^32 threads
+    static_assert(kMultiMaxElems / kSlice + 1 <= kMaxBlocks, "a tensor's blocks");
     for (int64_t i = 0; i < t.count; ++i) {
       if (t.param_dt[i] != pd || t.grad_dt[i] != gd || t.n[i] == 0) continue;
-      const int64_t need = cdiv(t.n[i], slices * kSlice);
+      const int64_t need = cdiv(t.n[i] + (eight ? 0 : lead32(t.m[i])), kSlice);
       if (a.count == kTensors || blocks + need > kMaxBlocks) {
         const hipError_t e = flush();
         if (e != hipSuccess) return e;
@@ -395,7 +400,7 @@ hipError_t launch_adamw_multi(bool eight, const AdamWTensors& t, const AdamWStep
 hipError_t launch_adamw_moments(Dt out, const uint8_t* m, const uint8_t* me, const uint8_t* v, const uint8_t* ve,
                                 int64_t n, void* mo, void* vo, hipStream_t s) {
   if (n == 0) return hipSuccess;
-  const dim3 grid((unsigned)std::min<int64_t>(cdiv(n, kSlice), 4096), 2);
+  const dim3 grid((unsigned)cdiv(n, kSlice), 2);
   if (out == Dt::BF16)
     moments_kernel<uint16_t><<<grid, kThreads, 0, s>>>(m, me, v, ve, n, (uint16_t*)mo, (uint16_t*)vo);
   else

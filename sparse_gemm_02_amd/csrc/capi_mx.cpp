@@ -65,7 +65,7 @@ slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* par
     };
     for (int64_t i = 0; i < count; ++i) {
       if (!dt_ok(param_dt[i]) || !dt_ok(grad_dt[i]) || n[i] < 0) return SLOPE_ERR_INVALID_ARG;
-      if (n[i] > slope::kAdamwMaxElems) return SLOPE_ERR_UNSUPPORTED;
+      if (n[i] > slope::kMultiMaxElems) return SLOPE_ERR_UNSUPPORTED;
       if (n[i] == 0) continue;
       const int64_t e = size_of(param_dt[i]);
       SLOPE_TRY(ptr(params[i], true, (unsigned)e));
@@ -99,7 +99,7 @@ slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, c
   if (in_m % 3 || in_v % 3 || in_m + in_v == 0) return SLOPE_ERR_INVALID_ARG;
   SLOPE_TRY(ptr(m_out_or_null, false, (unsigned)size_of(out_dt)));
   SLOPE_TRY(ptr(v_out_or_null, false, (unsigned)size_of(out_dt)));
-  if (out_dt == SLOPE_F16 || n > slope::kAdamwMaxElems) return SLOPE_ERR_UNSUPPORTED;
+  if (out_dt == SLOPE_F16 || n > slope::kMultiMaxElems) return SLOPE_ERR_UNSUPPORTED;
   if (m_out_or_null && m_out_or_null == v_out_or_null && n > 0) return SLOPE_ERR_INVALID_ARG;
   return from_hip(slope::launch_adamw_moments((Dt)out_dt, m_or_null, m_exp_or_null, v_or_null, v_exp_or_null, n,
                                               m_out_or_null, v_out_or_null, (hipStream_t)stream));
