@@ -127,18 +127,25 @@ slope_status slope_packed_sparse_mxfp4_bytes(int64_t rows, int64_t cols, int64_t
 slope_status slope_pack_sparse_mxfp4(slope_dtype dt, const void* values, const uint32_t* meta, int64_t rows,
                                      int64_t cols, void* packed, int64_t packed_bytes, void* stream);
 
+/* Bytes of device workspace that make slope_spmm_mxfp4_packed fastest: partial sums of up
+ * to eight parts of K where T <= 64 tokens of a long K meet few outputs (20480 -> 5120 at 64),
+ * 0 elsewhere.  Host-only; errors as the product's. */
+slope_status slope_spmm_mxfp4_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t* bytes);
+
 /* The 2:4 sparse product on 4-bit floating point:
  *   Y [T, N] = Xq [T, K] . W_q^T
  * of the values that the codes stand for; codes, exps from slope_quantize_mxfp4, packed_w
  * from slope_pack_sparse_mxfp4 of W_s (rows N, cols K), or of W_dp^T (rows K, cols N)
  * with dY's codes, for dX.  float32 sums (the matrix instruction's; which order depends on the
- * sizes), rounded once to out_dt (BF16, F16 or F32).  Any T; Y is overwritten, K = 0 gives 0.
- * No adapter term (slope_lowrank_add adds it).  Y needs 16-byte alignment.  Errors:
- * SLOPE_ERR_SHAPE unless K % 16 == 0 and N % 4 == 0; SLOPE_ERR_UNSUPPORTED for K >
+ * sizes and the workspace), rounded once to out_dt (BF16, F16 or F32).  Any T; Y is
+ * overwritten, K = 0 gives 0.  No adapter term (slope_lowrank_add adds it).  Y needs 16-byte
+ * alignment.  workspace: NULL, or device memory (16-byte aligned, scratch) of any size: of
+ * less than slope_spmm_mxfp4_workspace_bytes(T, K, N) bytes the call uses what helps it.
+ * Errors: SLOPE_ERR_SHAPE unless K % 16 == 0 and N % 4 == 0; SLOPE_ERR_UNSUPPORTED for K >
  * SLOPE_MXFP4_MAX_COLS; SLOPE_ERR_WORKSPACE if packed_w is short. */
 slope_status slope_spmm_mxfp4_packed(slope_dtype out_dt, const uint8_t* codes, const uint8_t* exps, int64_t T,
                                      int64_t K, const void* packed_w, int64_t packed_w_bytes, int64_t N, void* Y,
-                                     void* stream);
+                                     void* workspace_or_null, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,7 @@ Tensor conventions (see include/slope.h):
 from __future__ import annotations
 
 import ctypes
+import functools
 import operator
 import os
 
@@ -41,7 +42,8 @@ __all__ = [
     "slope_packed_sparse_i8_bytes", "slope_pack_sparse_i8", "slope_spmm_i8_packed", "slope_spmm_i8_decode",
     "I8_DECODE_MAX_TOKENS", "I8_MAX_COLS", "EXPORTED_SYMBOLS_INT8",
     "slope_adamw_multi", "slope_adamw_moments", "slope_mxfp4_row_bytes", "slope_quantize_mxfp4", "slope_mxfp4_values",
-    "slope_packed_sparse_mxfp4_bytes", "slope_pack_sparse_mxfp4", "slope_spmm_mxfp4_packed", "MX_BLOCK", "EXPORTED_SYMBOLS_MX",
+    "slope_packed_sparse_mxfp4_bytes", "slope_pack_sparse_mxfp4",
+    "slope_spmm_mxfp4_workspace_bytes", "slope_spmm_mxfp4_packed", "MX_BLOCK", "EXPORTED_SYMBOLS_MX",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -138,7 +140,8 @@ _SIGS_MX = {
     "slope_mxfp4_values": (_i32, [_i32, _vp, _vp, _i64, _i64, _vp, _vp]),
     "slope_packed_sparse_mxfp4_bytes": (_i32, [_i64, _i64, _P_I64]),
     "slope_pack_sparse_mxfp4": (_i32, [_i32, _vp, _vp, _i64, _i64, _vp, _i64, _vp]),
-    "slope_spmm_mxfp4_packed": (_i32, [_i32, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp]),
+    "slope_spmm_mxfp4_workspace_bytes": (_i32, [_i64, _i64, _i64, _P_I64]),
+    "slope_spmm_mxfp4_packed": (_i32, [_i32, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp]),
 }
 EXPORTED_SYMBOLS_MX = tuple(_SIGS_MX)
 
@@ -846,12 +849,27 @@ def slope_pack_sparse_mxfp4(values, meta, rows, cols, packed, stream=None) -> No
                _arg(meta, "meta", (rows, (cols // 4 + 7) // 8), torch.int32, d), rows, cols, pp, pb)
 
 
-def slope_spmm_mxfp4_packed(codes, exps, K, packed_w, N, Y, stream=None) -> None:
-    """Y [T, N] = Xq . W_q^T on 4-bit rows of K values and a 2:4 weight's 4-bit chunks, any T."""
+def slope_spmm_mxfp4_workspace_bytes(T: int, K: int, N: int) -> int:
+    b = ctypes.c_int64()
+    _check("slope_spmm_mxfp4_workspace_bytes", library().slope_spmm_mxfp4_workspace_bytes(T, K, N, ctypes.byref(b)))
+    return b.value
+
+
+_spmm_mxfp4_workspace = functools.lru_cache(maxsize=4096)(slope_spmm_mxfp4_workspace_bytes)
+
+
+def slope_spmm_mxfp4_packed(codes, exps, K, packed_w, N, Y, workspace=None, stream=None) -> None:
+    """Y [T, N] = Xq . W_q^T on 4-bit rows of K values and a 2:4 weight's 4-bit chunks, any T.  On the
+    current stream and without a workspace the call takes one of slope_spmm_mxfp4_workspace_bytes."""
     T = _rows(codes, "codes")[0]
     d = codes.get_device()
     pp, pb = _buffer(packed_w, "packed_w", d)
     nc, ne = _mxfp4_width(K)
     odt = Y.dtype
-    _on_device("slope_spmm_mxfp4_packed", d, stream, _code(odt), _arg(codes, "codes", (T, nc), _u8, d),
-               _arg(exps, "exps", (T, ne), _u8, d), T, K, pp, pb, N, _arg(Y, "Y", (T, N), odt, d))
+    args = (_code(odt), _arg(codes, "codes", (T, nc), _u8, d), _arg(exps, "exps", (T, ne), _u8, d), T, K, pp, pb, N,
+            _arg(Y, "Y", (T, N), odt, d))
+    if workspace is None and stream is None and 1 < T <= 64 and d >= 0:
+        need = _spmm_mxfp4_workspace(T, K, N)
+        if need:
+            workspace = torch.empty(need, dtype=_u8, device=codes.device)
+    _on_device("slope_spmm_mxfp4_packed", d, stream, *args, *_buffer(workspace, "workspace", d))

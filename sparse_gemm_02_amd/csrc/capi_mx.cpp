@@ -154,18 +154,28 @@ slope_status slope_pack_sparse_mxfp4(slope_dtype dt, const void* values, const u
   return from_hip(slope::launch_pack_sparse_mxfp4((Dt)dt, values, meta, rows, cols, packed, (hipStream_t)stream));
 }
 
+slope_status slope_spmm_mxfp4_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t* bytes) {
+  if (!bytes || T < 0 || K < 0 || N < 0) return SLOPE_ERR_INVALID_ARG;
+  if (K % 16 || N % 4) return SLOPE_ERR_SHAPE;
+  if (!in_range(T) || !in_range(N) || K > SLOPE_MXFP4_MAX_COLS) return SLOPE_ERR_UNSUPPORTED;
+  *bytes = slope::spmm_mxfp4_scratch_bytes(T, K, N);
+  return SLOPE_OK;
+}
+
 slope_status slope_spmm_mxfp4_packed(slope_dtype out_dt, const uint8_t* codes, const uint8_t* exps, int64_t T,
                                      int64_t K, const void* packed_w, int64_t packed_w_bytes, int64_t N, void* Y,
-                                     void* stream) {
-  if (!dt_ok(out_dt) || T < 0 || K < 0 || N < 0 || packed_w_bytes < 0) return SLOPE_ERR_INVALID_ARG;
+                                     void* workspace_or_null, int64_t workspace_bytes, void* stream) {
+  if (!dt_ok(out_dt) || T < 0 || K < 0 || N < 0 || packed_w_bytes < 0 || workspace_bytes < 0) return SLOPE_ERR_INVALID_ARG;
   SLOPE_TRY(ptr(codes, true));
   SLOPE_TRY(ptr(exps, true));
   SLOPE_TRY(ptr(packed_w, true));
   SLOPE_TRY(ptr(Y, true));
+  SLOPE_TRY(ptr(workspace_or_null, false));
   if (K % 16 || N % 4) return SLOPE_ERR_SHAPE;
   if (!in_range(T) || !in_range(N) || K > SLOPE_MXFP4_MAX_COLS) return SLOPE_ERR_UNSUPPORTED;
   if (packed_w_bytes < slope::packed_sparse_mxfp4_bytes(N, K)) return SLOPE_ERR_WORKSPACE;
-  return from_hip(slope::launch_spmm_mxfp4((Dt)out_dt, codes, exps, T, K, packed_w, N, Y, (hipStream_t)stream));
+  return from_hip(slope::launch_spmm_mxfp4((Dt)out_dt, codes, exps, T, K, packed_w, N, Y, workspace_or_null, workspace_bytes,
+                                           (hipStream_t)stream));
 }
 
 }  // extern "C"

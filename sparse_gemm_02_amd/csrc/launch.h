@@ -244,7 +244,8 @@ hipError_t launch_mxfp4_values(Dt out, const uint8_t* codes, const uint8_t* exps
                                hipStream_t s);
 hipError_t launch_pack_sparse_mxfp4(Dt dt, const void* values, const uint32_t* meta, int64_t M, int64_t K, void* packed,
                                     hipStream_t s);
+int64_t spmm_mxfp4_scratch_bytes(int64_t T, int64_t K, int64_t M);   // that make a call fastest (it takes fewer, or none)
 hipError_t launch_spmm_mxfp4(Dt out, const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K, const void* packed,
-                             int64_t M, void* Y, hipStream_t s);
+                             int64_t M, void* Y, void* scratch, int64_t scratch_bytes, hipStream_t s);
 
 }  // namespace slope

@@ -55,13 +55,16 @@ struct Args {
   const char* packed;
   int M, T, stages;
   O* Y;
+  float* scratch;                                    // of the parts of a split call
+  int64_t scratch_bytes;
   hipStream_t s;
 };
 
 // ---------------------------------------------------------------- few tokens
 // T <= 64: the weight's stream from HBM is the cost.  A block owns 32 FM rows and all
 // of K; its W waves take pairs of stages in turn, and their sums are added through LDS in
-// a fixed order, so one launch makes the output and nothing is scratch.  The weight
+// a fixed order, so one launch makes the output and nothing is scratch, unless the call is
+// split (below).  The weight
 // goes straight from memory into registers.  X, which every block reads (from L2), comes
 // as whole 128-byte lines, eight lanes a token, and passes through the wave's own piece
 // of LDS.  Its scales come to LDS at the start, all of them: loaded pair by pair they
@@ -81,7 +84,10 @@ struct DecodeA {
 // R loads of eight tokens bring a pair's X rows; D pairs are in flight.  No barrier in
 // the loop, since no wave reads another's piece of LDS.  Lanes of columns t >= T read a
 // row that is there (their sums are not stored).
-template <int R, int FM, int D, int W, int WPS, typename O>
+//
+// SPLIT: blocks z take a part of K each, whole groups of four stages, and write their sums
+// to Y + z T M.
+template <int R, int FM, int D, int W, int WPS, bool SPLIT, typename O>
 __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t* __restrict__ codes,
                                                                         const uint8_t* __restrict__ exps,
                                                                         const char* __restrict__ packed, int M, int T,
@@ -91,6 +97,9 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
   const int64_t t0 = (int64_t)blockIdx.y * (8 * R);  // the block's tokens (all of them up to 64)
+  const int groups = (stages + 3) / 4, z = SPLIT ? blockIdx.z : 0, parts = SPLIT ? gridDim.z : 1;
+  const int g0 = SPLIT ? groups * z / parts : 0, span = SPLIT ? groups * (z + 1) / parts - g0 : groups;
+  if constexpr (SPLIT) Y += (int64_t)z * T * M;
   const int row_c = stages * 64, row_s = (stages + 3) / 4 * 16;
   codes += t0 * row_c;
   exps += t0 * row_s;
@@ -118,16 +127,17 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t
     DecodeA<FM> a[2];
     u32x4 x[R];
   };
-  const int pairs = (stages + 1) / 2;
+  const int p0 = 2 * g0, p1 = z + 1 < parts ? p0 + 2 * span : (stages + 1) / 2;   // the block's pairs
+  const int last = 2 * p1 < stages ? 2 * p1 : stages;
   auto load_x = [&](Set& f, int pair) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) f.x[j] = load16(rx, pair < pairs ? x_src[j] + pair * 128 : kOutOfRange);
+    for (int j = 0; j < R; ++j) f.x[j] = load16(rx, pair < p1 ? x_src[j] + pair * 128 : kOutOfRange);
   };
   auto load_a = [&](Set& f, int pair) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int at = 2 * pair + u;
-      const uint32_t c = at < stages ? (uint32_t)at * kMxChunkBytes : kOutOfRange;   // beyond: zero codes
+      const uint32_t c = at < last ? (uint32_t)at * kMxChunkBytes : kOutOfRange;   // beyond: zero codes
 #pragma unroll
       for (int fm = 0; fm < FM; ++fm) {
         f.a[u].a[fm] = load16(ra, c + (h * kMxRows + row[fm]) * 16);
@@ -151,7 +161,7 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t
     }
 #pragma unroll
     for (int ft = 0; ft < FT; ++ft) {
-      const u32x2 w = scales[pair * (8 * R) + t_at[ft]];
+      const u32x2 w = scales[(pair - p0) * (8 * R) + t_at[ft]];
       sb[ft] = u32x2{w[0] >> (16 * h), w[1] >> (16 * h)};
     }
     compiler_fence();                                // the wave's LDS operations run in order: no wait, no barrier
@@ -183,16 +193,19 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t
     compiler_fence();                                // the next step's writes stay behind these reads
   };
   Set f[D];
-  // pair p's 8 bytes of token t at (p * 8R + t) * 8: reads without bank conflicts (rows of
+  // pair p0 + p's 8 bytes of token t at (p * 8R + t) * 8: reads without bank conflicts (rows of
   // a multiple of 256 bytes, as they come, would all lie in the same banks)
-  const int per_row = row_s / 16, all = T * per_row;
+  const int all = T * span;
   for (int i0 = threadIdx.x; i0 < all; i0 += 4 * 64 * W) {
     u32x4 v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = load16(rs, (i0 + j * 64 * W) * 16);   // past the end: zeros
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * 64 * W;
+      v[j] = load16(rs, SPLIT ? i / span * row_s + (g0 + i % span) * 16 : i * 16);   // past the last row: zeros
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * 64 * W, t = i / per_row, c = i - t * per_row;
+      const int i = i0 + j * 64 * W, t = i / span, c = i - t * span;
       u32x2* to = reinterpret_cast<u32x2*>(lds + W * XB) + 2 * c * (8 * R) + t;
       if (i < all) {
         to[0] = u32x2{v[j][0], v[j][1]};
@@ -202,14 +215,14 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t
   }
 #pragma unroll
   for (int d = 0; d < D; ++d) {
-    load_x(f[d], wave + d * W);
-    load_a(f[d], wave + d * W);
+    load_x(f[d], p0 + wave + d * W);
+    load_a(f[d], p0 + wave + d * W);
   }
   __syncthreads();                                   // (the first pairs are waited for next anyway)
-  for (int p = wave; p < pairs; p += D * W) {
+  for (int p = p0 + wave; p < p1; p += D * W) {
 #pragma unroll
     for (int d = 0; d < D; ++d)
-      if (p + d * W < pairs) step(f[d], p + d * W);
+      if (p + d * W < p1) step(f[d], p + d * W);
   }
   // the waves' sums: the upper half of them hands its own to the lower half first
   constexpr int HALF = W / 2, ALL = FM * FT * 256;
@@ -251,17 +264,42 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t
 // LDS of the largest form for so many tokens: eight waves' X rows, and all of the scales.
 int64_t decode_lds(int tokens, int64_t stages) { return 1024 * tokens + cdiv(stages, 4) * 16 * tokens; }
 
-template <int R, int FM, int D, int W, int WPS, typename O>
-hipError_t decode_go(const Args<O>& a) {
+template <int R, int FM, int D, int W, int WPS, bool SPLIT, typename O>
+hipError_t decode_launch(const Args<O>& a, int parts) {
   constexpr int FT = R > 4 ? 2 : 1, SUMS = W * FM * FT * 2048;
   static_assert(W <= 8, "decode_lds");
   static LdsLimit limit;
-  auto kern = decode_mxfp4_kernel<R, FM, D, W, WPS, O>;
+  auto kern = decode_mxfp4_kernel<R, FM, D, W, WPS, SPLIT, O>;
   const hipError_t e = limit.set((const void*)kern, kLdsBytes);
   if (e != hipSuccess) return e;
-  const int lds = std::max(W * R * 1024 + (int)cdiv(a.stages, 4) * 128 * R, SUMS);   // X rows and scales; sums
-  kern<<<dim3((unsigned)cdiv(a.M, 32 * FM), (unsigned)cdiv(a.T, 8 * R)), 64 * W, lds, a.s>>>(
+  const int lds = std::max(W * R * 1024 + (int)cdiv(cdiv(a.stages, 4), parts) * 128 * R, SUMS);   // X rows and scales; sums
+  kern<<<dim3((unsigned)cdiv(a.M, 32 * FM), (unsigned)cdiv(a.T, 8 * R), parts), 64 * W, lds, a.s>>>(
       a.codes, a.exps, a.packed, a.M, a.T, a.stages, a.Y);
+  return hipGetLastError();
+}
+template <int R, int FM, int D, int W, int WPS, typename O>
+hipError_t decode_go(const Args<O>& a) {
+  return decode_launch<R, FM, D, W, WPS, false>(a, 1);
+}
+
+// The parts' sums added in order and rounded: n4 groups of four outputs.
+template <typename O>
+__global__ __launch_bounds__(256) void join_kernel(const f32x4* __restrict__ sums, int64_t n4, int parts,
+                                                   O* __restrict__ Y) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  f32x4 v = sums[i];
+  for (int z = 1; z < parts; ++z) v += sums[z * n4 + i];
+  const float y[4] = {v[0], v[1], v[2], v[3]};
+  store4<O>(Y + 4 * i, y);
+}
+template <int R, int FM, int D, int W, int WPS, typename O>
+hipError_t split_go(const Args<O>& a, int parts) {
+  const Args<float> p{a.codes, a.exps, a.packed, a.M, a.T, a.stages, a.scratch, nullptr, 0, a.s};
+  const hipError_t e = decode_launch<R, FM, D, W, WPS, true>(p, parts);
+  if (e != hipSuccess) return e;
+  const int64_t n4 = (int64_t)a.T * a.M / 4;
+  join_kernel<O><<<(unsigned)cdiv(n4, 256), 256, 0, a.s>>>((const f32x4*)a.scratch, n4, parts, a.Y);
   return hipGetLastError();
 }
 
@@ -739,33 +777,75 @@ hipError_t large_go(const Args<O>& a, int64_t rows_full) {
 }
 
 // Up to 64 tokens.  64 rows a block draw X half as often as 32, and 32 spread better over
-// the compute units: whichever gives a unit less to take in (rows of weight, 0.41 bytes a value,
-// and tokens, 0.53, of its blocks).  us, 64 rows / 32 rows:
-//   9216 -> 27648    1 token 20.1 / 20.6   16: 21.1 / 23.0   64: 29.2 / 47
-//   5120 -> 20480            11.1 / 10.6       11.9 / 11.4       17.6 / 22.1
-//   9216 -> 9216              9.7 / 10.1       10.8 / 11.5       16.0 / 21.3
-//   20480 -> 5120            14.7 / 10.5       17.6 / 12.7       28.2 / 22.0
+// the compute units; parts of K spread them too, and cost a second launch and their sums.
+// A unit takes in 48 bytes a nanosecond of rows of weight (0.41 bytes a value) and tokens
+// (0.53), and all of them 5800 of weight: whichever is estimated to take the least.
+// us, 64 rows / 32 rows / 64 rows in parts, the weight from HBM:
+//   9216 -> 27648    1 token 20.1 / 20.6          16: 21.1 / 23.0          64: 29.2 / 43
+//   5120 -> 20480            11.1 / 10.6              11.9 / 11.4              17.6 / 22.1
+//   9216 -> 9216              9.7 / 10.1              10.8 / 11.5              16.1 / 21.5 / 16.6 (3)
+//   20480 -> 5120            14.7 / 10.5 / 12.2 (3)   17.6 / 12.8 / 13.0 (3)   28.9 / 22.5 / 17.6 (3)
+//   36864 -> 9216            26.5 / 30.6 / 28.5 (3)   31.2 / 39.5 / 30.1 (3)   49.6 / 68.5 / 41.1 (3)
+// Two parts of 160 or 288 blocks won nothing anywhere: units that get two do all the work.
 // Waves and pairs in flight as measured best: two blocks a unit want four waves (5120 -> 20480 at
 // 16 tokens 11.9 us, with eight 13.4), one wants eight (9216 -> 9216 at 16 10.8, with four 12.9).
+// (More pairs of weight in flight, 128 rows a block and the scales' loads behind the first pairs'
+// won nothing.)
+struct FewPlan {
+  bool wide, one;                                    // 64 rows a block; a block a compute unit at most
+  int parts;
+};
+FewPlan few_plan(int64_t T, int64_t M, int64_t stages, int64_t most_parts) {
+  const int64_t cus = compute_units();
+  const double k = 128.0 * (double)stages, sums = 4.0 * (double)T * (double)M, stream = k * (double)M * 0.41 / 5.8e6;
+  auto intake = [&](int64_t rows, int64_t parts) {
+    return k * (double)cdiv(cdiv(M, rows) * parts, cus) / (double)parts * ((double)rows * 0.41 + 0.53 * (double)T) / 48e3;
+  };
+  const double wide = intake(64, 1), narrow = intake(32, 1);
+  FewPlan plan{wide <= narrow, cdiv(M, wide <= narrow ? 64 : 32) <= cus, 1};
+  double least = std::max(std::min(wide, narrow), stream);
+  for (int parts = 2; parts <= most_parts; ++parts) {
+    const double us = std::max(intake(64, parts), stream) + 3.0 + 2.0 * parts * sums / 5e6;   // and the sums' way to memory and back
+    if (us < 0.9 * least) {                          // (what parts win by less may be lost)
+      least = us;
+      plan = FewPlan{true, cdiv(M, 64) * parts <= cus, parts};
+    }
+  }
+  return plan;
+}
+constexpr int64_t kMostParts = 8;
+// Parts of one call: whole groups of four stages, and the scratch holds their sums.
+int64_t most_parts(int64_t T, int64_t M, int64_t stages, int64_t scratch_bytes) {
+  return std::max<int64_t>(1, std::min({kMostParts, cdiv(stages, 4), scratch_bytes / (4 * T * M)}));
+}
+// A group of tokens' X rows and a part's scales fit LDS (64 tokens: parts up to K = 49152).
+bool few_fits(int64_t T, int64_t stages, int64_t parts) {
+  const int tokens = T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  return decode_lds(tokens, cdiv(cdiv(stages, 4), parts) * 4) <= kLdsBytes;
+}
+
 template <typename O>
-hipError_t few_go(const Args<O>& a) {
-  const int64_t cus = compute_units(), b2 = cdiv(a.M, 64), b1 = cdiv(a.M, 32);
-  const double x = 0.53 * (double)a.T;
-  const bool wide = (double)cdiv(b2, cus) * (64 * 0.41 + x) <= (double)cdiv(b1, cus) * (32 * 0.41 + x);
-  const bool one = (wide ? b2 : b1) <= cus;
+hipError_t few_go(const Args<O>& a, const FewPlan& f) {
+  if (f.parts > 1) {
+    if (a.T <= 8) return split_go<1, 2, 1, 8, 4, O>(a, f.parts);
+    if (a.T <= 16) return f.one ? split_go<2, 2, 1, 8, 4, O>(a, f.parts) : split_go<2, 2, 1, 4, 4, O>(a, f.parts);
+    if (a.T <= 32) return f.one ? split_go<4, 2, 1, 8, 4, O>(a, f.parts) : split_go<4, 2, 1, 4, 4, O>(a, f.parts);
+    return f.one ? split_go<8, 2, 1, 8, 2, O>(a, f.parts) : split_go<8, 2, 1, 4, 2, O>(a, f.parts);
+  }
   if (a.T <= 8) {
-    if (wide) return decode_go<1, 2, 1, 8, 4, O>(a);
-    return one ? decode_go<1, 1, 2, 8, 4, O>(a) : decode_go<1, 1, 1, 8, 4, O>(a);
+    if (f.wide) return decode_go<1, 2, 1, 8, 4, O>(a);
+    return f.one ? decode_go<1, 1, 2, 8, 4, O>(a) : decode_go<1, 1, 1, 8, 4, O>(a);
   }
   if (a.T <= 16) {
-    if (!wide) return decode_go<2, 1, 1, 8, 4, O>(a);
-    return one ? decode_go<2, 2, 1, 8, 4, O>(a) : decode_go<2, 2, 1, 4, 4, O>(a);
+    if (!f.wide) return decode_go<2, 1, 1, 8, 4, O>(a);
+    return f.one ? decode_go<2, 2, 1, 8, 4, O>(a) : decode_go<2, 2, 1, 4, 4, O>(a);
   }
   if (a.T <= 32) {
-    if (!wide) return decode_go<4, 1, 1, 8, 4, O>(a);
-    return one ? decode_go<4, 2, 1, 8, 4, O>(a) : decode_go<4, 2, 1, 4, 4, O>(a);
+    if (!f.wide) return decode_go<4, 1, 1, 8, 4, O>(a);
+    return f.one ? decode_go<4, 2, 1, 8, 4, O>(a) : decode_go<4, 2, 1, 4, 4, O>(a);
   }
-  return wide ? decode_go<8, 2, 1, 4, 2, O>(a) : decode_go<8, 1, 1, 8, 2, O>(a);
+  if (!f.wide) return decode_go<8, 1, 1, 8, 2, O>(a);
+  return f.one ? decode_go<8, 2, 1, 8, 2, O>(a) : decode_go<8, 2, 1, 4, 2, O>(a);
 }
 
 // Any number of tokens.  Above 64, four kernels by their estimated time in units of a
@@ -794,14 +874,15 @@ hipError_t few_go(const Args<O>& a) {
 //   4096 -> 1024   1000         22.6 /  21.4 /  15.3 /   9.1*
 //                  2048         23.3 /  21.7 /  16.0 /  13.8*
 //   768 -> 2304    1000          9.3 /   9.6 /   7.1*/  10.0
-// (The few-token kernel holds all of a group's scales in LDS: 64 tokens up to K = 49152.)
 template <typename O>
 hipError_t spmm_launch(const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K, const void* packed, int64_t M,
-                       void* Y, hipStream_t s) {
-  const Args<O> a{codes, exps, (const char*)packed, (int)M, (int)T, (int)cdiv(K, kMxCols), (O*)Y, s};
-  const int tokens = T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64;
-  const bool fits = decode_lds(tokens, a.stages) <= kLdsBytes && cdiv(T, 64) <= 65535;   // (and a grid's second dimension)
-  if (T <= 64) return fits ? few_go<O>(a) : mid_go<O>(a);
+                       void* Y, void* scratch, int64_t scratch_bytes, hipStream_t s) {
+  const Args<O> a{codes, exps, (const char*)packed, (int)M, (int)T, (int)cdiv(K, kMxCols), (O*)Y, (float*)scratch, scratch_bytes, s};
+  if (T <= 64) {
+    const FewPlan plan = few_plan(T, M, a.stages, scratch ? most_parts(T, M, a.stages, scratch_bytes) : 1);
+    return few_fits(T, a.stages, plan.parts) ? few_go<O>(a, plan) : mid_go<O>(a);
+  }
+  const bool fits = few_fits(T, a.stages, 1) && cdiv(T, 64) <= 65535;   // (and a grid's second dimension)
   const double cus = (double)compute_units();
   const int64_t rows = cdiv(M, 256), cols = cdiv(T, 256), halves = cdiv(T, 128);
   const int64_t rows_full = full_width_rows(rows, cols, halves, (int64_t)cus);
@@ -819,13 +900,20 @@ hipError_t spmm_launch(const uint8_t* codes, const uint8_t* exps, int64_t T, int
 
 }  // namespace
 
+int64_t spmm_mxfp4_scratch_bytes(int64_t T, int64_t K, int64_t M) {
+  if (T == 0 || T > 64 || K == 0 || M == 0) return 0;
+  const int64_t stages = cdiv(K, kMxCols);
+  const int parts = few_plan(T, M, stages, most_parts(T, M, stages, INT64_MAX)).parts;
+  return parts > 1 && few_fits(T, stages, parts) ? parts * 4 * T * M : 0;
+}
+
 hipError_t launch_spmm_mxfp4(Dt out, const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K, const void* packed,
-                             int64_t M, void* Y, hipStream_t s) {
+                             int64_t M, void* Y, void* scratch, int64_t scratch_bytes, hipStream_t s) {
   if (T == 0 || M == 0) return hipSuccess;
   if (K == 0) return launch_fill_zero(out, Y, T * M, s);
-  if (out == Dt::BF16) return spmm_launch<uint16_t>(codes, exps, T, K, packed, M, Y, s);
-  if (out == Dt::F16) return spmm_launch<_Float16>(codes, exps, T, K, packed, M, Y, s);
-  return spmm_launch<float>(codes, exps, T, K, packed, M, Y, s);
+  if (out == Dt::BF16) return spmm_launch<uint16_t>(codes, exps, T, K, packed, M, Y, scratch, scratch_bytes, s);
+  if (out == Dt::F16) return spmm_launch<_Float16>(codes, exps, T, K, packed, M, Y, scratch, scratch_bytes, s);
+  return spmm_launch<float>(codes, exps, T, K, packed, M, Y, scratch, scratch_bytes, s);
 }
 
 }  // namespace slope

@@ -161,14 +161,30 @@ def test_4_bit_refusals(lib):
     assert p(vals=FAKE + 2) == -3 and p(meta=FAKE + 4) == -3 and p(out=FAKE + 8) == -3
     assert p(cols=24) == -2 and p(dt=F32) == -6 and p(cols=(1 << 21) + 16) == -6 and p(rows=(1 << 22) + 1) == -6
     assert p(nb=3327) == -4
-    y = lambda dt=BF16, c=FAKE, e=FAKE, T=4, K=64, w=FAKE, nb=big, N=64, Y=FAKE: \
-        lib.slope_spmm_mxfp4_packed(dt, c, e, T, K, w, nb, N, Y, None)
+    y = lambda dt=BF16, c=FAKE, e=FAKE, T=4, K=64, w=FAKE, nb=big, N=64, Y=FAKE, ws=None, wb=0: \
+        lib.slope_spmm_mxfp4_packed(dt, c, e, T, K, w, nb, N, Y, ws, wb, None)
     assert y(dt=3) == -1 and y(c=None) == -1 and y(e=None) == -1 and y(w=None) == -1 and y(Y=None) == -1
     assert y(T=-1) == -1 and y(K=-1) == -1 and y(N=-1) == -1 and y(nb=-1) == -1
     assert y(c=FAKE + 8) == -3 and y(e=FAKE + 8) == -3 and y(w=FAKE + 4) == -3 and y(Y=FAKE + 8) == -3
     assert y(K=24) == -2 and y(N=66) == -2
     assert y(T=(1 << 22) + 1) == -6 and y(N=(1 << 22) + 4) == -6 and y(K=(1 << 21) + 16) == -6
-    assert y(nb=3327) == -4
+    assert y(nb=3327) == -4 and y(wb=-1) == -1 and y(ws=FAKE + 8, wb=64) == -3
+
+
+def test_product_workspace_sizes(lib):
+    """Parts of K for few tokens of a long K and few outputs: whole float32 [T, N] arrays, eight at most."""
+    size = S.slope_spmm_mxfp4_workspace_bytes
+    for T, K, N in [(64, 20480, 5120), (61, 20480, 5120), (64, 36864, 9216), (33, 65536, 64)]:
+        parts, rest = divmod(size(T, K, N), 4 * T * N)
+        assert rest == 0 and 2 <= parts <= 8, (T, K, N)
+    for T, K, N in [(0, 64, 64), (4, 0, 64), (4, 64, 0), (65, 20480, 5120), (1, 9216, 27648), (64, 9216, 27648), (64, 16, 4),
+                    (64, 1 << 21, 4)]:
+        assert size(T, K, N) == 0, (T, K, N)
+    b = ctypes.c_int64()
+    f = lambda T=4, K=64, N=64, p=ctypes.byref(b): lib.slope_spmm_mxfp4_workspace_bytes(T, K, N, p)
+    assert f(T=-1) == -1 and f(K=-1) == -1 and f(N=-1) == -1 and f(p=None) == -1
+    assert f(K=24) == -2 and f(N=66) == -2
+    assert f(T=(1 << 22) + 1) == -6 and f(N=(1 << 22) + 4) == -6 and f(K=(1 << 21) + 16) == -6
 
 
 def test_binding_checks_4_bit_tensors():

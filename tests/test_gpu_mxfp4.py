@@ -256,7 +256,37 @@ def test_product(T, K, N, out):
     assert torch.equal(run(codes, exps, K, packed, N, out), y)         # the same sums again
 
 
-@pytest.mark.parametrize("T,K,N", SHAPES)
+SPLIT = [(2, 65552, 260), (9, 32768, 132), (16, 40960, 516), (17, 24592, 68), (32, 20480, 516), (33, 16400, 1028),
+         (61, 20480, 1540), (64, 20368, 300), (64, 65552, 64), (40, 131072, 4), (64, 36864, 9216)]
+
+
+@pytest.mark.parametrize("T,K,N", SPLIT)
+@pytest.mark.parametrize("out", list(DT))
+def test_product_in_parts(T, K, N, out):
+    """Every number of parts that a workspace may hold, and a workspace that holds none."""
+    if K * N > 1 << 27 and out != "bf16":
+        pytest.skip("one large case is enough")
+    say(f"[spmm_mxfp4 parts] T={T} K={K} N={N} {out}")
+    need = S.slope_spmm_mxfp4_workspace_bytes(T, K, N)
+    assert need >= 2 * 4 * T * N
+    packed, codes, exps, meta, v = product_case(T, K, N, out, T + K + N, "f16" if out == "f16" else "bf16")
+    xv = torch.empty((T, K), device="cuda")
+    S.slope_mxfp4_values(codes, exps, xv)
+    rows = np.unique(np.concatenate([np.arange(0, N, 1 + N // 100), np.arange(N - 4, N)]))
+    want, mass = oracle.spmm_mxfp4(host_f64(xv), dense_weight(v, meta, K, rows))
+    bound = (K / 64 + 17) * 2.0 ** -23 * mass + HALF_STEP[out] * np.abs(want) + (2.0 ** -25 if out == "f16" else 0)
+    for size in sorted({0, 4 * T * N, *range(2 * 4 * T * N, need + 1, 4 * T * N), need, need + 4096}):
+        ws = torch.full((size + GUARD,), 0xA5, dtype=U8, device="cuda")
+        y = torch.full((T, N), 7.0, dtype=DT[out], device="cuda")
+        S.slope_spmm_mxfp4_packed(codes, exps, K, packed, N, y, workspace=ws[:size])
+        torch.cuda.synchronize()
+        bad = np.abs(host_f64(y)[:, rows] - want) > bound
+        assert not bad.any(), (size, np.argwhere(bad)[:3])
+        assert (ws[size:] == 0xA5).all()
+    assert torch.equal(run(codes, exps, K, packed, N, out), y)         # what the call takes by itself
+
+
+@pytest.mark.parametrize("T,K,N", SHAPES + SPLIT[:-1])
 def test_product_of_small_integers_is_exact(T, K, N):
     """Codes of 0 and +-1 with equal scales: every partial sum is an integer below 2^24."""
     rng = np.random.default_rng(T * K + N)
