@@ -237,7 +237,9 @@ class SparseAdamW(torch.optim.Optimizer):
         for group in self.param_groups:
             b1, b2 = group["betas"]
             hp = dict(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"], weight_decay=group["weight_decay"])
-            lists = {}                               # by step number and device: parameters without a gradient sit steps out
+            # by step number and device (parameters without a gradient sit steps out), and parameters that
+            # share their memory after each other
+            lists, turns = {}, {}
             for p in group["params"]:
                 if p.grad is None:
                     continue
@@ -250,8 +252,10 @@ class SparseAdamW(torch.optim.Optimizer):
                                                     layer.out_features, layer.in_features, layer.packed_s,
                                                     layer.packed_dpT, st["step"], **hp)
                 else:
-                    lists.setdefault((st["step"], p.device), []).append((p, g, st))
-            for (t, _), each in lists.items():
+                    at = (p.data_ptr(), p.device)
+                    turns[at] = turn = turns.get(at, -1) + 1 if p.numel() else 0
+                    lists.setdefault((st["step"], p.device, turn), []).append((p, g, st))
+            for (t, _, _), each in lists.items():
                 ps, gs, sts = zip(*each)
                 take = lambda name: [st[name] for st in sts]
                 eight = {} if self.state_bits == 32 else dict(m_exp=take("exp_avg_exp"), v_exp=take("exp_avg_sq_exp"),

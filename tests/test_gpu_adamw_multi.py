@@ -253,6 +253,25 @@ def test_steps_with_little_eps(eps):
             assert not p[bad].any()
 
 
+def test_parameters_that_share_memory_take_turns():
+    """Two parameters over the same weight, as tied heads are: two steps after each other, as calls would take them."""
+    w = torch.randn(777, device="cuda")
+    own = [torch.nn.Parameter(torch.randn(33, device="cuda")), torch.nn.Parameter(torch.empty(0, device="cuda"))]
+    p, q = torch.nn.Parameter(w), torch.nn.Parameter(w)
+    assert p.data_ptr() == q.data_ptr()
+    grads = [torch.randn_like(t) for t in (p, q, *own)]
+    want = w.clone()
+    for g in grads[:2]:
+        S.slope_adamw(want, g, torch.zeros(777, device="cuda"), torch.zeros(777, device="cuda"), 1, 1e-2)
+    holder = torch.nn.Module()
+    holder.ps = torch.nn.ParameterList([p, q, *own])
+    opt = SparseAdamW([holder], lr=1e-2)
+    for t, g in zip((p, q, *own), grads):
+        t.grad = g
+    opt.step()
+    assert torch.equal(w, want)
+
+
 def test_all_codes_and_scales_as_values():
     codes = torch.arange(256, dtype=torch.int16).to(U8).repeat(256)
     exps = torch.arange(256, dtype=torch.int16).to(U8).repeat_interleave(8)
