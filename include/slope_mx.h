@@ -56,7 +56,7 @@ extern "C" {
  * Tensors need only their element type's alignment.  The step's number and the seed are
  * the call's own: a call recorded into a graph repeats them at each replay.
  * Errors: slope_adamw's, and SLOPE_ERR_INVALID_ARG for other state_bits, count < 0
- * or two of the written tensors that share memory; SLOPE_ERR_ALIGN for a tensor not
+ * or a written tensor that shares memory with another one or a gradient; SLOPE_ERR_ALIGN for a tensor not
  * aligned to its elements; SLOPE_ERR_UNSUPPORTED for n[i] > 2^34. */
 slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* param_dt, const int32_t* grad_dt,
                                void* const* params, const void* const* grads, void* const* m, void* const* v,

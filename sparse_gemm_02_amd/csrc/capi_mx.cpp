@@ -34,11 +34,16 @@ slope_status ptr(const void* p, bool required, unsigned align = 16) {
     if (_st != SLOPE_OK) return _st;       \
   } while (0)
 
-// Whether two of the byte ranges [first, second) overlap.
-bool overlap(std::vector<std::pair<uintptr_t, uintptr_t>>& r) {
-  std::sort(r.begin(), r.end());
-  for (size_t i = 1; i < r.size(); ++i)
-    if (r[i].first < r[i - 1].second) return true;
+// Whether two of the written byte ranges [first, second) overlap, or one of them and one that is read.
+typedef std::vector<std::pair<uintptr_t, uintptr_t>> Ranges;
+bool overlap(Ranges& written, const Ranges& read) {
+  std::sort(written.begin(), written.end());
+  for (size_t i = 1; i < written.size(); ++i)
+    if (written[i].first < written[i - 1].second) return true;
+  for (const auto& r : read) {                       // the last written range that begins before its end
+    const auto w = std::lower_bound(written.begin(), written.end(), std::make_pair(r.second, uintptr_t(0)));
+    if (w != written.begin() && std::prev(w)->second > r.first) return true;
+  }
   return false;
 }
 
@@ -58,11 +63,13 @@ slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* par
   if (!param_dt || !grad_dt || !params || !grads || !m || !v || !n || (eight && (!m_exp || !v_exp)))
     return SLOPE_ERR_INVALID_ARG;
   try {
-    std::vector<std::pair<uintptr_t, uintptr_t>> written;
+    Ranges written, read;
     written.reserve((size_t)count * (eight ? 5 : 3));
-    auto writes = [&](const void* p, int64_t bytes) {
-      written.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes);
+    read.reserve((size_t)count);
+    auto range = [](const void* p, int64_t bytes) {
+      return std::make_pair(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes);
     };
+    auto writes = [&](const void* p, int64_t bytes) { written.push_back(range(p, bytes)); };
     for (int64_t i = 0; i < count; ++i) {
       if (!dt_ok(param_dt[i]) || !dt_ok(grad_dt[i]) || n[i] < 0) return SLOPE_ERR_INVALID_ARG;
       if (n[i] > slope::kMultiMaxElems) return SLOPE_ERR_UNSUPPORTED;
@@ -73,6 +80,7 @@ slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* par
       SLOPE_TRY(ptr(m[i], true, eight ? 1 : 4));
       SLOPE_TRY(ptr(v[i], true, eight ? 1 : 4));
       writes(params[i], n[i] * e);
+      read.push_back(range(grads[i], n[i] * size_of(grad_dt[i])));
       writes(m[i], n[i] * (eight ? 1 : 4));
       writes(v[i], n[i] * (eight ? 1 : 4));
       if (eight) {
@@ -83,7 +91,7 @@ slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* par
         writes(v_exp[i], blocks);
       }
     }
-    if (overlap(written)) return SLOPE_ERR_INVALID_ARG;
+    if (overlap(written, read)) return SLOPE_ERR_INVALID_ARG;
   } catch (const std::bad_alloc&) {
     return SLOPE_ERR_HIP;
   }

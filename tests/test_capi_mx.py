@@ -70,6 +70,8 @@ def test_adamw_multi_refuses_tensors_that_share_memory(lib):
     assert f(me=(9 * FAKE, 9 * FAKE + 1)) == -1 and f(ve=(9 * FAKE, 12 * FAKE)) == -1
     assert f(bits=32, m=(5 * FAKE, 5 * FAKE + 252)) == -1
     assert f(m=(FAKE, 6 * FAKE)) == -1                               # a moment over a weight
+    assert f(g=(FAKE, 4 * FAKE)) == -1 and f(g=(3 * FAKE, 2 * FAKE + 124)) == -1   # a gradient over a weight
+    assert f(g=(7 * FAKE - 126, 4 * FAKE)) == -1                     # the last value of a gradient over a moment
 
 
 def test_adamw_moments_refusals(lib):

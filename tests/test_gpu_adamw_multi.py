@@ -149,7 +149,7 @@ def test_many_tensors_take_several_launches(eight):
     a.guards_whole()
 
 
-def test_large_lists_take_several_slices_a_block():
+def test_large_lists():
     n = (1 << 24) + 5                                                # four slices a block from 2^24 values on
     a = Lists([n, 3000], ["bf16", "bf16"], ["bf16", "bf16"], 4, True)
     before = a.bits()
