@@ -808,6 +808,7 @@ def _mxfp4_width(K):
     return 64 * -(-K // 128), 16 * -(-K // 512)
 
 
+@functools.lru_cache(maxsize=4096)
 def slope_mxfp4_row_bytes(K: int):
     """(bytes of codes, bytes of scales) of one row of K 4-bit values."""
     c, e = ctypes.c_int64(), ctypes.c_int64()

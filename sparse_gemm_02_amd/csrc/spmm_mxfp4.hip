@@ -282,14 +282,21 @@ hipError_t decode_go(const Args<O>& a) {
   return decode_launch<R, FM, D, W, WPS, false>(a, 1);
 }
 
-// The parts' sums added in order and rounded: n4 groups of four outputs.
+constexpr int kMostParts = 8;
+
+// The parts' sums added in order and rounded: n4 groups of four outputs.  All parts are
+// loaded before the first sum.
 template <typename O>
 __global__ __launch_bounds__(256) void join_kernel(const f32x4* __restrict__ sums, int64_t n4, int parts,
                                                    O* __restrict__ Y) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n4) return;
-  f32x4 v = sums[i];
-  for (int z = 1; z < parts; ++z) v += sums[z * n4 + i];
+  f32x4 part[kMostParts];
+#pragma unroll
+  for (int z = 0; z < kMostParts; ++z) part[z] = z < parts ? sums[z * n4 + i] : f32x4{};
+  f32x4 v = part[0];
+#pragma unroll
+  for (int z = 1; z < kMostParts; ++z) v += part[z];
   const float y[4] = {v[0], v[1], v[2], v[3]};
   store4<O>(Y + 4 * i, y);
 }
@@ -813,10 +820,9 @@ FewPlan few_plan(int64_t T, int64_t M, int64_t stages, int64_t most_parts) {
   }
   return plan;
 }
-constexpr int64_t kMostParts = 8;
 // Parts of one call: whole groups of four stages, and the scratch holds their sums.
 int64_t most_parts(int64_t T, int64_t M, int64_t stages, int64_t scratch_bytes) {
-  return std::max<int64_t>(1, std::min({kMostParts, cdiv(stages, 4), scratch_bytes / (4 * T * M)}));
+  return std::max<int64_t>(1, std::min({(int64_t)kMostParts, cdiv(stages, 4), scratch_bytes / (4 * T * M)}));
 }
 // A group of tokens' X rows and a part's scales fit LDS (64 tokens: parts up to K = 49152).
 bool few_fits(int64_t T, int64_t stages, int64_t parts) {
