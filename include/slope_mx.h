@@ -119,7 +119,7 @@ slope_status slope_packed_sparse_mxfp4_bytes(int64_t rows, int64_t cols, int64_t
  *              first and the second kept code of its groups of four, nibble g for group g
  *   positions  at 2048 + ((b / 2) * 64 + r) * 8 + (b % 2) * 4: a word whose nibble g has
  *              the bits of group g's kept positions
- *   scales     at 3072 + r * 4 + b: one byte
+ *   scales     at 3 * 1024 + r * 4 + b: one byte
  * Rows past `rows` and columns past `cols` have codes and scales 0.  packed: caller-owned,
  * at least slope_packed_sparse_mxfp4_bytes(rows, cols) bytes, overwritten.  Errors:
  * SLOPE_ERR_UNSUPPORTED for F32 or cols > SLOPE_MXFP4_MAX_COLS, SLOPE_ERR_SHAPE if cols %

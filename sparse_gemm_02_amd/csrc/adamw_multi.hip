@@ -227,8 +227,7 @@ __device__ __forceinline__ Pack<PT, 8> step8(float (&p)[8], const float (&g)[8],
 
 // Values by which m's start is past a 32-byte border: with fp32 moments a thread's eight
 // values begin there, since tensors that follow each other in one buffer begin anywhere
-// (6 million fp32 values at an odd place 34 us, from the tensor's first value on 40; even
-// aligned tensors gained 6 %, having one test for all eight values).
+// (6 million fp32 values at an odd place 34 us, from the tensor's first value on 40).
 __host__ __device__ __forceinline__ int lead32(const void* m) { return (int)(reinterpret_cast<uintptr_t>(m) / 4 % 8); }
 
 // A block of threads takes 2048 values of one tensor, a thread eight of them; four lanes

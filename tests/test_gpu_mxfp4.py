@@ -187,7 +187,7 @@ def chunks_reference(codes, exps, meta, rows, cols):
             at = ((b4 // 2) * 64 + rr)
             chunk[at * 16 + (b4 % 2) * 8:][:8] = np.array([first, second], "<u4").view(np.uint8)
             chunk[2048 + at * 8 + (b4 % 2) * 4:][:4] = np.array([kept], "<u4").view(np.uint8)
-            chunk[3072 + rr * 4 + b4] = exps[r, b]
+            chunk[3 * 1024 + rr * 4 + b4] = exps[r, b]
     return out.reshape(-1)
 
 
