@@ -497,9 +497,8 @@ def test_a_model_trained_with_8_bit_moments_and_served_in_4_bits():
     assert np.all(np.abs(host_f64(dx) - want) <= 2.0 ** -23 * (D / 64 + 17) * mass + 2.0 ** -8 * np.abs(want))
 
 
-@pytest.mark.parametrize("T", [1, 40, 300])
-def test_captured_and_on_another_stream(T):
-    K, N = 1040, 772
+@pytest.mark.parametrize("T,K,N", [(1, 1040, 772), (40, 1040, 772), (300, 1040, 772), (64, 20480, 516)])
+def test_captured_and_on_another_stream(T, K, N):
     packed, codes, exps, meta, v = product_case(T, K, N, "bf16", T)
     x = [torch.randn((T, K), device="cuda").bfloat16() for _ in range(3)]
     eager = []
@@ -523,6 +522,9 @@ def test_captured_and_on_another_stream(T):
     for i in (0, 1, 2, 1):
         xin.copy_(x[i])
         y.fill_(float("nan"))
+        with torch.cuda.stream(side):                                  # (parts take a workspace each: another call beside it)
+            other = torch.empty_like(y)
+            S.slope_spmm_mxfp4_packed(codes, exps, K, packed, N, other)
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, eager[i])
