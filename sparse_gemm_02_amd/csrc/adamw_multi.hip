@@ -13,6 +13,7 @@
 // thousandth of itself a step, and codes lie an eighth apart, so v would stand
 // still; rounded this way its expectation follows the exact average.
 #include <algorithm>
+#include <type_traits>
 
 #include "adamw.h"
 #include "adamw_args.h"
@@ -39,12 +40,29 @@ struct MultiArgs {
 };
 static_assert(sizeof(MultiArgs) + sizeof(AdamWStep) <= 4096, "kernel arguments");
 
+// Eight elements of one or two bytes past the caches' usual order (NT): what they hold is
+// not used again before it would be displaced.  A wave's access covers whole lines; fp32 ones,
+// two accesses a lane with every second 16 bytes, lose by it (2^27 fp32 values 674 -> 740 us).
+template <typename V>
+__device__ __forceinline__ Pack<V, 8> load_nt(const V* p) {
+  typedef uint32_t Words __attribute__((ext_vector_type(2 * sizeof(V)), aligned(1)));
+  const Words w = __builtin_nontemporal_load(reinterpret_cast<const Words*>(p));
+  return __builtin_bit_cast(Pack<V, 8>, w);
+}
+template <typename V>
+__device__ __forceinline__ void store_nt(V* p, const Pack<V, 8>& x) {
+  typedef uint32_t Words __attribute__((ext_vector_type(2 * sizeof(V)), aligned(1)));
+  __builtin_nontemporal_store(__builtin_bit_cast(Words, x), reinterpret_cast<Words*>(p));
+}
+
 // Eight values e .. e + 7 of the n at p (those that are not there read as zero, and e may
 // be negative).
-template <typename T>
+template <bool NT, typename T>
 __device__ __forceinline__ void load8(const T* p, int64_t e, int64_t n, float (&out)[8]) {
   if (e >= 0 && e + 8 <= n) {
-    const Pack<T, 8> x = load_pack<T, 8>(p + e);
+    Pack<T, 8> x;
+    if constexpr (NT && sizeof(T) < 4) x = load_nt(p + e);
+    else x = load_pack<T, 8>(p + e);
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[i] = elem_f32(x.v[i]);
   } else {
@@ -52,10 +70,11 @@ __device__ __forceinline__ void load8(const T* p, int64_t e, int64_t n, float (&
     for (int i = 0; i < 8; ++i) out[i] = (uint64_t)(e + i) < (uint64_t)n ? elem_f32(p[e + i]) : 0.0f;
   }
 }
-template <typename T>
+template <bool NT, typename T>
 __device__ __forceinline__ void store8(T* p, int64_t e, int64_t n, const Pack<T, 8>& x) {
   if (e >= 0 && e + 8 <= n) {
-    store_pack<T, 8>(p + e, x);
+    if constexpr (NT && sizeof(T) < 4) store_nt(p + e, x);
+    else store_pack<T, 8>(p + e, x);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -83,9 +102,12 @@ __device__ __forceinline__ Pack<T, 8> rounded8(const float (&in)[8]) {
     return __builtin_bit_cast(Pack<T, 8>, w);
   }
 }
+template <bool NT>
 __device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int64_t left) {
   if (left >= 8) {
-    const Pack<uint8_t, 8> x = load_pack<uint8_t, 8>(p);
+    Pack<uint8_t, 8> x;
+    if constexpr (NT) x = load_nt(p);
+    else x = load_pack<uint8_t, 8>(p);
     return __builtin_bit_cast(u32x2, x);
   }
   u32x2 w = {0u, 0u};
@@ -94,9 +116,12 @@ __device__ __forceinline__ u32x2 load_codes(const uint8_t* p, int64_t left) {
     if (i < left) w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
   return w;
 }
+template <bool NT>
 __device__ __forceinline__ void store_codes(uint8_t* p, int64_t left, u32x2 w) {
   if (left >= 8) {
-    store_pack<uint8_t, 8>(p, __builtin_bit_cast(Pack<uint8_t, 8>, w));
+    const auto x = __builtin_bit_cast(Pack<uint8_t, 8>, w);
+    if constexpr (NT) store_nt(p, x);
+    else store_pack<uint8_t, 8>(p, x);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -235,7 +260,7 @@ __host__ __device__ __forceinline__ int lead32(const void* m) { return (int)(rei
 // moments 292 to 308 us (10.1 bytes a value read and written, 5.3 to 5.6 TB/s; a copy
 // reaches 5.1), with fp32 moments 635 (22 bytes, 5.6).  Two or four such parts a block of
 // threads take 3 to 4 % longer from 2^24 values on and nothing less below.
-template <typename PT, typename GT, bool EIGHT, bool FAST>
+template <typename PT, typename GT, bool EIGHT, bool FAST, bool NT>
 __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const MultiArgs a, const AdamWStep c0) {
   int lo = 0, hi = a.count;                          // the last tensor whose first block is not behind this one
   while (hi - lo > 1) {
@@ -249,14 +274,14 @@ __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const MultiArgs a
   float pf[8], gf[8], mf[8], vf[8];
   AdamWStep c = c0;
   if constexpr (EIGHT) {
-    load8(p, e, n, pf);
-    load8(g, e, n, gf);
+    load8<NT>(p, e, n, pf);
+    load8<NT>(g, e, n, gf);
     const int64_t left = n - e, at = left > 0 ? e : 0, block = at / 32;   // lanes past the end: no access, zeros
     uint8_t* m = (uint8_t*)a.m[lo];
     uint8_t* v = (uint8_t*)a.v[lo];
     const uint32_t em = left > 0 ? a.me[lo][block] : 0u, ev = left > 0 ? a.ve[lo][block] : 0u;
-    decode_m(load_codes(m + at, left), em, mf);
-    decode_v(load_codes(v + at, left), ev, vf);
+    decode_m(load_codes<NT>(m + at, left), em, mf);
+    decode_v(load_codes<NT>(v + at, left), ev, vf);
     if (ev == (uint32_t)kBadExp) c.beta2 = nan_f32();   // every v of the block is a NaN
     const Pack<PT, 8> np = step8<PT, FAST>(pf, gf, mf, vf, c);
     if (left < 8) {                                  // nothing is there: no part of the block's largest
@@ -269,37 +294,37 @@ __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const MultiArgs a
     u32x2 cm, cv;
     encode(mf, vf, nm, nv, Noise((uint32_t)(e / 8), a.seed[lo]), cm, cv);
     if (left > 0) {
-      store_codes(m + at, left, cm);
-      store_codes(v + at, left, cv);
+      store_codes<NT>(m + at, left, cm);
+      store_codes<NT>(v + at, left, cv);
       if (threadIdx.x % 4 == 0) {
         a.me[lo][block] = (uint8_t)nm;
         a.ve[lo][block] = (uint8_t)nv;
       }
     }
-    store8(p, e, n, np);
+    store8<NT>(p, e, n, np);
   } else {
     float* m = (float*)a.m[lo];
     float* v = (float*)a.v[lo];
     e -= lead32(m);
-    load8(p, e, n, pf);
-    load8(g, e, n, gf);
-    load8(m, e, n, mf);
-    load8(v, e, n, vf);
+    load8<NT>(p, e, n, pf);
+    load8<NT>(g, e, n, gf);
+    load8<NT>(m, e, n, mf);
+    load8<NT>(v, e, n, vf);
     const Pack<PT, 8> np = step8<PT, FAST>(pf, gf, mf, vf, c);
-    store8(m, e, n, rounded8<float>(mf));
-    store8(v, e, n, rounded8<float>(vf));
-    store8(p, e, n, np);
+    store8<NT>(m, e, n, rounded8<float>(mf));
+    store8<NT>(v, e, n, rounded8<float>(vf));
+    store8<NT>(p, e, n, np);
   }
 }
 
 // The values that 8-bit codes stand for.  n values, each thread eight of one moment:
-// 160 million of both as bf16 163 us, 5.9 TB/s (178 with blocks that loop).
-template <typename O, bool V>
+// 160 million of both as bf16 158 us, 6.2 TB/s (178 with blocks that loop, 163 without NT).
+template <typename O, bool V, bool NT>
 __device__ __forceinline__ void values8(const uint8_t* codes, const uint8_t* exps, int64_t n, O* out) {
   const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kPerThread, left = n - e;
   if (left <= 0) return;
   const uint32_t b = exps[e / 32];
-  const u32x2 w = load_codes(codes + e, left);
+  const u32x2 w = load_codes<NT>(codes + e, left);
   float f[8];
   if constexpr (V) {
     decode_v(w, b, f);
@@ -310,33 +335,42 @@ __device__ __forceinline__ void values8(const uint8_t* codes, const uint8_t* exp
   } else {
     decode_m(w, b, f);
   }
-  store8(out, e, n, rounded8<O>(f));
+  store8<NT>(out, e, n, rounded8<O>(f));
 }
-template <typename O>
+template <typename O, bool NT>
 __global__ __launch_bounds__(kThreads) void moments_kernel(const uint8_t* __restrict__ m, const uint8_t* __restrict__ me,
                                                            const uint8_t* __restrict__ v, const uint8_t* __restrict__ ve,
                                                            int64_t n, O* __restrict__ mo, O* __restrict__ vo) {
-  if (blockIdx.y == 0 && mo) values8<O, false>(m, me, n, mo);
-  if (blockIdx.y == 1 && vo) values8<O, true>(v, ve, n, vo);
+  if (blockIdx.y == 0 && mo) values8<O, false, NT>(m, me, n, mo);
+  if (blockIdx.y == 1 && vo) values8<O, true, NT>(v, ve, n, vo);
 }
 
+// Above this many values a call's tensors pass the last-level cache (256 MB) before anything reads
+// them again.  8-bit moments, bf16, 2^25 values 68.5 us, so 64.7; 2^27: 247 and 235 (fp32 weights 393
+// and 370); 7 million fp16 values that stay there, and their moments read out next: 28.7, so 29.8.
+constexpr int64_t kStreams = int64_t(1) << 25;
+
+struct Form {
+  bool eight, fast, nt;
+};
 template <typename PT, typename GT>
-hipError_t go(bool eight, bool fast, const MultiArgs& a, unsigned blocks, const AdamWStep& c, hipStream_t s) {
-  if (fast) adamw_multi_kernel<PT, GT, true, true><<<blocks, kThreads, 0, s>>>(a, c);
-  else if (eight) adamw_multi_kernel<PT, GT, true, false><<<blocks, kThreads, 0, s>>>(a, c);
-  else adamw_multi_kernel<PT, GT, false, false><<<blocks, kThreads, 0, s>>>(a, c);
+hipError_t go(const Form& f, const MultiArgs& a, unsigned blocks, const AdamWStep& c, hipStream_t s) {
+  if (!f.eight) adamw_multi_kernel<PT, GT, false, false, false><<<blocks, kThreads, 0, s>>>(a, c);
+  else if (!f.fast) adamw_multi_kernel<PT, GT, true, false, false><<<blocks, kThreads, 0, s>>>(a, c);
+  else if (!f.nt) adamw_multi_kernel<PT, GT, true, true, false><<<blocks, kThreads, 0, s>>>(a, c);
+  else adamw_multi_kernel<PT, GT, true, true, true><<<blocks, kThreads, 0, s>>>(a, c);
   return hipGetLastError();
 }
 template <typename PT>
-hipError_t go_grad(Dt g, bool eight, bool fast, const MultiArgs& a, unsigned blocks, const AdamWStep& c, hipStream_t s) {
-  if (g == Dt::BF16) return go<PT, uint16_t>(eight, fast, a, blocks, c, s);
-  if (g == Dt::F16) return go<PT, _Float16>(eight, fast, a, blocks, c, s);
-  return go<PT, float>(eight, fast, a, blocks, c, s);
+hipError_t go_grad(Dt g, const Form& f, const MultiArgs& a, unsigned blocks, const AdamWStep& c, hipStream_t s) {
+  if (g == Dt::BF16) return go<PT, uint16_t>(f, a, blocks, c, s);
+  if (g == Dt::F16) return go<PT, _Float16>(f, a, blocks, c, s);
+  return go<PT, float>(f, a, blocks, c, s);
 }
-hipError_t launch_one(Dt p, Dt g, bool eight, bool fast, const MultiArgs& a, unsigned blocks, const AdamWStep& c, hipStream_t s) {
-  if (p == Dt::BF16) return go_grad<uint16_t>(g, eight, fast, a, blocks, c, s);
-  if (p == Dt::F16) return go_grad<_Float16>(g, eight, fast, a, blocks, c, s);
-  return go_grad<float>(g, eight, fast, a, blocks, c, s);
+hipError_t launch_one(Dt p, Dt g, const Form& f, const MultiArgs& a, unsigned blocks, const AdamWStep& c, hipStream_t s) {
+  if (p == Dt::BF16) return go_grad<uint16_t>(g, f, a, blocks, c, s);
+  if (p == Dt::F16) return go_grad<_Float16>(g, f, a, blocks, c, s);
+  return go_grad<float>(g, f, a, blocks, c, s);
 }
 
 // 32 bits for tensor i of a call (SplitMix64 of Steele, Lea and Flood, 2014).
@@ -359,12 +393,13 @@ hipError_t launch_adamw_multi(bool eight, const AdamWTensors& t, const AdamWStep
     for (int64_t i = 0; i < t.count; ++i)
       if (t.param_dt[i] == pd && t.grad_dt[i] == gd) total += t.n[i];
     if (total == 0) continue;
+    const Form form{eight, fast, total >= kStreams};
     MultiArgs a;
     int64_t blocks = 0;
     a.count = 0;
     auto flush = [&]() {
       if (a.count == 0) return hipSuccess;
-      const hipError_t e = launch_one((Dt)pd, (Dt)gd, eight, fast, a, (unsigned)blocks, c, s);
+      const hipError_t e = launch_one((Dt)pd, (Dt)gd, form, a, (unsigned)blocks, c, s);
       a.count = 0;
       blocks = 0;
       return e;
@@ -400,10 +435,13 @@ hipError_t launch_adamw_moments(Dt out, const uint8_t* m, const uint8_t* me, con
                                 int64_t n, void* mo, void* vo, hipStream_t s) {
   if (n == 0) return hipSuccess;
   const dim3 grid((unsigned)cdiv(n, kSlice), 2);
-  if (out == Dt::BF16)
-    moments_kernel<uint16_t><<<grid, kThreads, 0, s>>>(m, me, v, ve, n, (uint16_t*)mo, (uint16_t*)vo);
-  else
-    moments_kernel<float><<<grid, kThreads, 0, s>>>(m, me, v, ve, n, (float*)mo, (float*)vo);
+  auto put = [&](auto* m_to, auto* v_to) {
+    using O = std::remove_pointer_t<decltype(m_to)>;
+    if (n >= kStreams) moments_kernel<O, true><<<grid, kThreads, 0, s>>>(m, me, v, ve, n, m_to, v_to);
+    else moments_kernel<O, false><<<grid, kThreads, 0, s>>>(m, me, v, ve, n, m_to, v_to);
+  };
+  if (out == Dt::BF16) put((uint16_t*)mo, (uint16_t*)vo);
+  else put((float*)mo, (float*)vo);
   return hipGetLastError();
 }
 

@@ -85,14 +85,17 @@ struct DecodeA {
 // the loop, since no wave reads another's piece of LDS.  Lanes of columns t >= T read a
 // row that is there (their sums are not stored).
 //
+// NT: a large weight's loads do not displace what the caches hold (decode_launch).
+//
 // SPLIT: blocks z take a part of K each, whole groups of four stages, and write their sums
 // to Y + z T M.
-template <int R, int FM, int D, int W, int WPS, bool SPLIT, typename O>
+template <int R, int FM, int D, int W, int WPS, bool SPLIT, bool NT, typename O>
 __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t* __restrict__ codes,
                                                                         const uint8_t* __restrict__ exps,
                                                                         const char* __restrict__ packed, int M, int T,
                                                                         int stages, O* __restrict__ Y) {
   constexpr int FT = R > 4 ? 2 : 1, XB = R * 1024;   // LDS bytes of a pair's X rows
+  constexpr int AUX = NT ? 2 : 0;                    // the loads' cache policy: non-temporal
   constexpr int PER = kMxRows / (32 * FM);           // blocks a chunk
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5;
@@ -140,10 +143,10 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t
       const uint32_t c = at < last ? (uint32_t)at * kMxChunkBytes : kOutOfRange;   // beyond: zero codes
 #pragma unroll
       for (int fm = 0; fm < FM; ++fm) {
-        f.a[u].a[fm] = load16(ra, c + (h * kMxRows + row[fm]) * 16);
+        f.a[u].a[fm] = __builtin_amdgcn_raw_buffer_load_b128(ra, c + (h * kMxRows + row[fm]) * 16, 0, AUX);
         f.a[u].kept[fm] = __builtin_bit_cast(
-            u32x2, __builtin_amdgcn_raw_buffer_load_b64(ra, c + kMxMaskAt + (h * kMxRows + row[fm]) * 8, 0, 0));
-        f.a[u].s[fm] = __builtin_amdgcn_raw_buffer_load_b32(ra, c + kMxScaleAt + row[fm] * 4, 0, 0);
+            u32x2, __builtin_amdgcn_raw_buffer_load_b64(ra, c + kMxMaskAt + (h * kMxRows + row[fm]) * 8, 0, AUX));
+        f.a[u].s[fm] = __builtin_amdgcn_raw_buffer_load_b32(ra, c + kMxScaleAt + row[fm] * 4, 0, AUX);
       }
     }
   };
@@ -264,18 +267,29 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t
 // LDS of the largest form for so many tokens: eight waves' X rows, and all of the scales.
 int64_t decode_lds(int tokens, int64_t stages) { return 1024 * tokens + cdiv(stages, 4) * 16 * tokens; }
 
+// A weight of at least 64 MB, read once by a call of up to 64 tokens, is not expected in the 256 MB
+// last-level cache at the next call, and its lines leave X's where they are.  us, from HBM and (a
+// single weight, called again and again) from the cache, without NT / with it:
+//   9216 -> 27648, 105 MB   1 token 20.5 / 18.8 and 17.2 / 17.5   64: 29.5 / 27.5 and 21.9 / 26.8
+//   9216 -> 9216, 35 MB              9.9 /  9.1 and  7.3 /  7.7       16.1 / 14.9 and 12.2 / 13.5
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
+
 template <int R, int FM, int D, int W, int WPS, bool SPLIT, typename O>
 hipError_t decode_launch(const Args<O>& a, int parts) {
   constexpr int FT = R > 4 ? 2 : 1, SUMS = W * FM * FT * 2048;
   static_assert(W <= 8, "decode_lds");
-  static LdsLimit limit;
-  auto kern = decode_mxfp4_kernel<R, FM, D, W, WPS, SPLIT, O>;
-  const hipError_t e = limit.set((const void*)kern, kLdsBytes);
-  if (e != hipSuccess) return e;
   const int lds = std::max(W * R * 1024 + (int)cdiv(cdiv(a.stages, 4), parts) * 128 * R, SUMS);   // X rows and scales; sums
-  kern<<<dim3((unsigned)cdiv(a.M, 32 * FM), (unsigned)cdiv(a.T, 8 * R), parts), 64 * W, lds, a.s>>>(
-      a.codes, a.exps, a.packed, a.M, a.T, a.stages, a.Y);
-  return hipGetLastError();
+  auto go = [&](auto kern, LdsLimit& limit) {
+    const hipError_t e = limit.set((const void*)kern, kLdsBytes);
+    if (e != hipSuccess) return e;
+    kern<<<dim3((unsigned)cdiv(a.M, 32 * FM), (unsigned)cdiv(a.T, 8 * R), parts), 64 * W, lds, a.s>>>(
+        a.codes, a.exps, a.packed, a.M, a.T, a.stages, a.Y);
+    return hipGetLastError();
+  };
+  static LdsLimit once, streams;
+  if (a.T <= 64 && cdiv(a.M, kMxRows) * a.stages * kMxChunkBytes >= kStreamBytes)
+    return go(decode_mxfp4_kernel<R, FM, D, W, WPS, SPLIT, true, O>, streams);
+  return go(decode_mxfp4_kernel<R, FM, D, W, WPS, SPLIT, false, O>, once);
 }
 template <int R, int FM, int D, int W, int WPS, typename O>
 hipError_t decode_go(const Args<O>& a) {

@@ -149,8 +149,43 @@ def test_many_tensors_take_several_launches(eight):
     a.guards_whole()
 
 
+@pytest.mark.parametrize("dt,gdt,shift", [("bf16", "bf16", 0), ("f16", "f32", 1), ("f32", "f16", 3), ("bf16", "f32", 2)])
+def test_lists_past_the_cache(dt, gdt, shift):
+    """From 2^25 values on 8-bit moments and 16-bit tensors are accessed non-temporally.  A tensor's first
+    blocks do not depend on the rest of it, and moments not on eps (near 0 the accesses are ordinary ones)."""
+    sizes = [1, 31, (1 << 25) + 77, 2049]
+    say(f"[adamw_multi] {dt} {gdt} {shift}")
+    a, b, c = (Lists(sizes, [dt] * 4, [gdt] * 4, 6, True, shift) for _ in range(3))
+    a.call(3, seed=5)
+    b.call(3, seed=5, eps=1e-15)
+    short = 1 << 24
+    for x in (c.p, c.g, c.m, c.v):
+        x[2] = x[2][:short]
+    for x in (c.me, c.ve):
+        x[2] = x[2][:short // 32]
+    c.call(3, seed=5)
+    torch.cuda.synchronize()
+    for x in (a, b, c):
+        for raw, at, n in x.buffers:
+            rest = torch.cat([raw[:at], raw[at + n:]]).view(U8)
+            assert (rest == 0x5A).all()
+    for i in range(4):
+        for x, y in ((a.m, b.m), (a.v, b.v), (a.me, b.me), (a.ve, b.ve)):
+            assert torch.equal(x[i], y[i])
+        for x, y in ((a.p, c.p), (a.m, c.m), (a.v, c.v), (a.me, c.me), (a.ve, c.ve)):
+            assert torch.equal(x[i][:y[i].numel()], y[i])
+    mo, vo = (torch.empty(sizes[2], dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    S.slope_adamw_moments(a.m[2], a.me[2], a.v[2], a.ve[2], mo, vo)
+    for at in (0, short, sizes[2] - 77):
+        n = min(32 * 100, sizes[2] - at)
+        m2, v2 = (torch.empty(n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        cut = lambda t, k: t[2][at // k:-(-(at + n) // k)].clone()
+        S.slope_adamw_moments(cut(a.m, 1), cut(a.me, 32), cut(a.v, 1), cut(a.ve, 32), m2, v2)
+        assert torch.equal(mo[at:at + n], m2) and torch.equal(vo[at:at + n], v2)
+
+
 def test_large_lists():
-    n = (1 << 24) + 5                                                # four slices a block from 2^24 values on
+    n = (1 << 24) + 5
     a = Lists([n, 3000], ["bf16", "bf16"], ["bf16", "bf16"], 4, True)
     before = a.bits()
     a.call(2, seed=77)

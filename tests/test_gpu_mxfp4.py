@@ -307,6 +307,30 @@ def test_product_of_small_integers_is_exact(T, K, N):
     assert np.array_equal(host_f64(y), xi @ w.T)
 
 
+@pytest.mark.parametrize("K,N", [(16384, 10308), (36864, 5060)])
+def test_large_weights_take_the_values_of_small_ones(K, N):
+    """Weights of more than 64 MB, whose loads few tokens make non-temporal, against the same rows in small
+    weights.  Integers: every order of the sums is exact."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    vt = (torch.randint(0, 2, (N, K // 2), device="cuda", generator=g) * 2 - 1).bfloat16()
+    nib = torch.tensor([4, 8, 12, 9, 13, 14], device="cuda")[torch.randint(0, 6, (N, K // 32, 8), device="cuda", generator=g)]
+    meta = (nib << (4 * torch.arange(8, device="cuda"))).sum(-1).to(torch.int32)
+    nb = S.slope_packed_sparse_mxfp4_bytes(N, K)
+    assert nb >= 64 << 20
+    packed = torch.empty(nb, dtype=U8, device="cuda")
+    S.slope_pack_sparse_mxfp4(vt, meta, N, K, packed)
+    for T in (1, 8, 9, 16, 17, 30, 33, 64):
+        say(f"[spmm_mxfp4 large weight] T={T} K={K} N={N}")
+        xi = torch.randint(-1, 2, (T, K), device="cuda", generator=g).float()
+        xi[:, ::32] = 1.0
+        codes, exps = quantize(xi)
+        y = run(codes, exps, K, packed, N, "f32")
+        for at in range(0, N, 1280):                                   # 20 chunks of rows
+            n, row = min(1280, N - at), K // 128 * 3328
+            part = packed[at // 64 * row:(at + n + 63) // 64 * row]
+            assert torch.equal(run(codes, exps, K, part, n, "f32"), y[:, at:at + n])
+
+
 def test_blocks_without_values_reach_their_outputs_only():
     T, K, N = 70, 512, 200
     for t in (1, 40, T):
