@@ -257,8 +257,8 @@ __host__ __device__ __forceinline__ int lead32(const void* m) { return (int)(rei
 
 // A block of threads takes 2048 values of one tensor, a thread eight of them; four lanes
 // hold a block of 32.  Bound by memory: 160 million bf16 weights and gradients with 8-bit
-// moments 292 to 308 us (10.1 bytes a value read and written, 5.3 to 5.6 TB/s; a copy
-// reaches 5.1), with fp32 moments 635 (22 bytes, 5.6).  Two or four such parts a block of
+// moments 278 us (10.1 bytes a value read and written, 5.9 TB/s; a copy reaches 5.1), with
+// fp32 moments 609 (22 bytes, 5.8).  Two or four such parts a block of
 // threads take 3 to 4 % longer from 2^24 values on and nothing less below.
 template <typename PT, typename GT, bool EIGHT, bool FAST, bool NT>
 __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const MultiArgs a, const AdamWStep c0) {
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const MultiArgs a
 }
 
 // The values that 8-bit codes stand for.  n values, each thread eight of one moment:
-// 160 million of both as bf16 158 us, 6.2 TB/s (178 with blocks that loop, 163 without NT).
+// 160 million of both as bf16 156 us, 6.2 TB/s (178 with blocks that loop, 163 without NT).
 template <typename O, bool V, bool NT>
 __device__ __forceinline__ void values8(const uint8_t* codes, const uint8_t* exps, int64_t n, O* out) {
   const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kPerThread, left = n - e;
@@ -345,17 +345,19 @@ __global__ __launch_bounds__(kThreads) void moments_kernel(const uint8_t* __rest
   if (blockIdx.y == 1 && vo) values8<O, true, NT>(v, ve, n, vo);
 }
 
-// Above this many values a call's tensors pass the last-level cache (256 MB) before anything reads
+// From these many values on a call's tensors pass the last-level cache (256 MB) before anything reads
 // them again.  8-bit moments, bf16, 2^25 values 68.5 us, so 64.7; 2^27: 247 and 235 (fp32 weights 393
-// and 370); 7 million fp16 values that stay there, and their moments read out next: 28.7, so 29.8.
-constexpr int64_t kStreams = int64_t(1) << 25;
+// and 370); 7 million fp16 values that stay there, and their moments read out next: 28.7, so 29.8.  fp32
+// moments, bf16 weights, 2^24: 71.4 and 67.1; 2^27: 533 and 506.
+constexpr int64_t streams_from(bool eight) { return int64_t(1) << (eight ? 25 : 24); }
 
 struct Form {
   bool eight, fast, nt;
 };
 template <typename PT, typename GT>
 hipError_t go(const Form& f, const MultiArgs& a, unsigned blocks, const AdamWStep& c, hipStream_t s) {
-  if (!f.eight) adamw_multi_kernel<PT, GT, false, false, false><<<blocks, kThreads, 0, s>>>(a, c);
+  if (!f.eight && !f.nt) adamw_multi_kernel<PT, GT, false, false, false><<<blocks, kThreads, 0, s>>>(a, c);
+  else if (!f.eight) adamw_multi_kernel<PT, GT, false, false, true><<<blocks, kThreads, 0, s>>>(a, c);
   else if (!f.fast) adamw_multi_kernel<PT, GT, true, false, false><<<blocks, kThreads, 0, s>>>(a, c);
   else if (!f.nt) adamw_multi_kernel<PT, GT, true, true, false><<<blocks, kThreads, 0, s>>>(a, c);
   else adamw_multi_kernel<PT, GT, true, true, true><<<blocks, kThreads, 0, s>>>(a, c);
@@ -393,7 +395,7 @@ hipError_t launch_adamw_multi(bool eight, const AdamWTensors& t, const AdamWStep
     for (int64_t i = 0; i < t.count; ++i)
       if (t.param_dt[i] == pd && t.grad_dt[i] == gd) total += t.n[i];
     if (total == 0) continue;
-    const Form form{eight, fast, total >= kStreams};
+    const Form form{eight, fast, total >= streams_from(eight)};
     MultiArgs a;
     int64_t blocks = 0;
     a.count = 0;
@@ -437,7 +439,7 @@ hipError_t launch_adamw_moments(Dt out, const uint8_t* m, const uint8_t* me, con
   const dim3 grid((unsigned)cdiv(n, kSlice), 2);
   auto put = [&](auto* m_to, auto* v_to) {
     using O = std::remove_pointer_t<decltype(m_to)>;
-    if (n >= kStreams) moments_kernel<O, true><<<grid, kThreads, 0, s>>>(m, me, v, ve, n, m_to, v_to);
+    if (n >= streams_from(true)) moments_kernel<O, true><<<grid, kThreads, 0, s>>>(m, me, v, ve, n, m_to, v_to);
     else moments_kernel<O, false><<<grid, kThreads, 0, s>>>(m, me, v, ve, n, m_to, v_to);
   };
   if (out == Dt::BF16) put((uint16_t*)mo, (uint16_t*)vo);

@@ -149,6 +149,20 @@ def test_many_tensors_take_several_launches(eight):
     a.guards_whole()
 
 
+@pytest.mark.parametrize("dt,gdt,shift", [("bf16", "bf16", 0), ("f16", "f32", 5), ("f32", "bf16", 3)])
+def test_32_bit_lists_past_the_cache(dt, gdt, shift):
+    """From 2^24 values on the 16-bit tensors are accessed non-temporally: still slope_adamw's bits."""
+    sizes = [33, (1 << 24) + 13, 2049]
+    say(f"[adamw_multi 32] {dt} {gdt} {shift}")
+    a, b = (Lists(sizes, [dt] * 3, [gdt] * 3, 8, False, at) for at in (shift, 0))   # (slope_adamw wants 16-byte addresses)
+    a.call(5)
+    for p, g, m, v in zip(b.p, b.g, b.m, b.v):
+        S.slope_adamw(p, g, m, v, 5, **HP)
+    torch.cuda.synchronize()
+    a.guards_whole()
+    assert all(torch.equal(s, t) for x, y in zip((a.p, a.m, a.v), (b.p, b.m, b.v)) for s, t in zip(x, y))
+
+
 @pytest.mark.parametrize("dt,gdt,shift", [("bf16", "bf16", 0), ("f16", "f32", 1), ("f32", "f16", 3), ("bf16", "f32", 2)])
 def test_lists_past_the_cache(dt, gdt, shift):
     """From 2^25 values on 8-bit moments and 16-bit tensors are accessed non-temporally.  A tensor's first
