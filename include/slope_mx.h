@@ -63,6 +63,20 @@ slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* par
                                uint8_t* const* m_exp, uint8_t* const* v_exp, const int64_t* n,
                                const slope_adamw_params* hp, uint64_t seed, void* stream);
 
+/* slope_adamw_double_prune_packed with 8-bit moments: one step on the compressed values of
+ * W_s, whose new values are written in place and into W_s's tile chunks, and the double
+ * prune of the updated W_s into W_dp^T's.  Values, codes and scales are bitwise those of
+ * slope_adamw_multi on a list of this one tensor (m, v [N, K/2] codes, m_exp, v_exp [N * K / 64]
+ * scales, the same seed), the chunks those of slope_pack_sparse and
+ * slope_double_prune_packed of the new values.  dt BF16 or F16; grad_dt BF16, F16 or F32.
+ * m_exp and v_exp may have any address.  Errors: those of slope_adamw_double_prune_packed,
+ * and SLOPE_ERR_SHAPE unless K % 64 == 0 (the blocks of moments lie in one row). */
+slope_status slope_adamw8_double_prune_packed(slope_dtype dt, slope_dtype grad_dt, void* values_s, const uint32_t* meta_s,
+                                              const void* dW_values, uint8_t* m, uint8_t* m_exp, uint8_t* v, uint8_t* v_exp,
+                                              int64_t N, int64_t K, const slope_adamw_params* hp, uint64_t seed,
+                                              void* packed_s, int64_t packed_s_bytes, void* packed_dpT,
+                                              int64_t packed_dpT_bytes, void* stream);
+
 /* The values of 8-bit moments (code * 2^E; NaN where the scale is 255): m, v codes
  * [n], m_exp, v_exp scales [ceil(n / 32)], outputs [n] in out_dt: BF16 or F32, both
  * hold every value exactly (bfloat16 has four significant bits to spare).  Either

@@ -41,7 +41,7 @@ __all__ = [
     "slope_rmsnorm", "slope_rmsnorm_bwd_workspace_bytes", "slope_rmsnorm_bwd", "slope_quantize_rows_i8",
     "slope_packed_sparse_i8_bytes", "slope_pack_sparse_i8", "slope_spmm_i8_packed", "slope_spmm_i8_decode",
     "I8_DECODE_MAX_TOKENS", "I8_MAX_COLS", "EXPORTED_SYMBOLS_INT8",
-    "slope_adamw_multi", "slope_adamw_moments", "slope_mxfp4_row_bytes", "slope_quantize_mxfp4", "slope_mxfp4_values",
+    "slope_adamw_multi", "slope_adamw8_double_prune_packed", "slope_adamw_moments", "slope_mxfp4_row_bytes", "slope_quantize_mxfp4", "slope_mxfp4_values",
     "slope_packed_sparse_mxfp4_bytes", "slope_pack_sparse_mxfp4",
     "slope_spmm_mxfp4_workspace_bytes", "slope_spmm_mxfp4_packed", "MX_BLOCK", "EXPORTED_SYMBOLS_MX",
 ]
@@ -134,6 +134,8 @@ EXPORTED_SYMBOLS_INT8 = tuple(_SIGS_INT8)
 # include/slope_mx.h
 _SIGS_MX = {
     "slope_adamw_multi": (_i32, [_i32, _i64, *[_vp] * 9, _P_HP, ctypes.c_uint64, _vp]),
+    "slope_adamw8_double_prune_packed": (_i32, [_i32, _i32, *[_vp] * 7, _i64, _i64, _P_HP, ctypes.c_uint64, _vp, _i64,
+                                                _vp, _i64, _vp]),
     "slope_adamw_moments": (_i32, [_i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
     "slope_mxfp4_row_bytes": (_i32, [_i64, _P_I64, _P_I64]),
     "slope_quantize_mxfp4": (_i32, [_i32, _vp, _i64, _i64, _vp, _vp, _vp]),
@@ -778,6 +780,22 @@ def slope_adamw_multi(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps
     _on_device("slope_adamw_multi", dev, stream, 8 if eight else 32, count, kind_at, kind_at + 4 * count, *lists[:4],
                lists[4] if eight else None, lists[5] if eight else None, at, ctypes.byref(hp),
                int(seed) & (2 ** 64 - 1))
+
+
+def slope_adamw8_double_prune_packed(values_s, meta_s, dW_values, m, m_exp, v, v_exp, N, K, packed_s, packed_dpT, step,
+                                     lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, seed=0, stream=None) -> None:
+    """slope_adamw_multi with 8-bit moments on the compressed values of W_s (in place, and inside its
+    tile chunks packed_s), then the double prune of the updated W_s into the tile chunks packed_dpT."""
+    n, d = N * K // 2, values_s.get_device()
+    flat = lambda t, name, size, dtype: _arg(t.reshape(-1) if t.is_contiguous() else t, name, (size,), dtype, d)
+    vdt, gdt = values_s.dtype, dW_values.dtype
+    ps, pb = _buffer(packed_s, "packed_s", d)
+    qs, qb = _buffer(packed_dpT, "packed_dpT", d)
+    hp = _hp(step, lr, beta1, beta2, eps, weight_decay)
+    _on_device("slope_adamw8_double_prune_packed", d, stream, _code(vdt), _code(gdt), flat(values_s, "values_s", n, vdt),
+               flat(meta_s, "meta_s", N * -(-K // 32), torch.int32), flat(dW_values, "dW_values", n, gdt),
+               flat(m, "m", n, _u8), flat(m_exp, "m_exp", -(-n // MX_BLOCK), _u8), flat(v, "v", n, _u8),
+               flat(v_exp, "v_exp", -(-n // MX_BLOCK), _u8), N, K, ctypes.byref(hp), int(seed) & (2 ** 64 - 1), ps, pb, qs, qb)
 
 
 def slope_adamw_moments(m, m_exp, v, v_exp, m_out=None, v_out=None, stream=None) -> None:

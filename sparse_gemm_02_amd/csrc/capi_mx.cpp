@@ -17,6 +17,7 @@ using slope::Dt;
 
 namespace {
 
+constexpr int64_t kPackedMaxCols = 1 << 21;   // of 16-bit tile chunks
 bool in_range(int64_t v) { return v >= 0 && v <= SLOPE_MAX_DIM; }
 bool dt_ok(int d) { return d == SLOPE_F32 || d == SLOPE_BF16 || d == SLOPE_F16; }
 int64_t size_of(int d) { return d == SLOPE_F32 ? 4 : 2; }
@@ -97,6 +98,29 @@ slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* par
   }
   const slope::AdamWTensors t{count, param_dt, grad_dt, params, grads, m, v, m_exp, v_exp, n};
   return from_hip(slope::launch_adamw_multi(eight, t, c, seed, (hipStream_t)stream));
+}
+
+slope_status slope_adamw8_double_prune_packed(slope_dtype dt, slope_dtype grad_dt, void* values_s, const uint32_t* meta_s,
+                                              const void* dW_values, uint8_t* m, uint8_t* m_exp, uint8_t* v, uint8_t* v_exp,
+                                              int64_t N, int64_t K, const slope_adamw_params* hp, uint64_t seed,
+                                              void* packed_s, int64_t packed_s_bytes, void* packed_dpT,
+                                              int64_t packed_dpT_bytes, void* stream) {
+  if (!dt_ok(dt) || !dt_ok(grad_dt) || N < 0 || K < 0 || packed_s_bytes < 0 || packed_dpT_bytes < 0)
+    return SLOPE_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)values_s, (const void*)meta_s, dW_values, (const void*)m, (const void*)v, (const void*)packed_s,
+                        (const void*)packed_dpT})
+    SLOPE_TRY(ptr(p, true));
+  SLOPE_TRY(ptr(m_exp, true, 1));
+  SLOPE_TRY(ptr(v_exp, true, 1));
+  slope::AdamWStep c;
+  SLOPE_TRY(slope::adamw_step(hp, &c));
+  if (dt == SLOPE_F32) return SLOPE_ERR_UNSUPPORTED;   // 16-bit values only
+  if (N % 16 || K % 64) return SLOPE_ERR_SHAPE;        // a block of moments lies in one row
+  if (K > kPackedMaxCols || N > kPackedMaxCols) return SLOPE_ERR_UNSUPPORTED;
+  if (packed_s_bytes < slope::packed_sparse_bytes(N, K) || packed_dpT_bytes < slope::packed_sparse_bytes(K, N))
+    return SLOPE_ERR_WORKSPACE;
+  return from_hip(slope::launch_adamw8_double_prune_packed((Dt)dt, (Dt)grad_dt, values_s, meta_s, dW_values, m, m_exp, v, v_exp,
+                                                           N, K, c, seed, packed_s, packed_dpT, (hipStream_t)stream));
 }
 
 slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, const uint8_t* m_exp_or_null,

@@ -232,6 +232,10 @@ struct AdamWTensors {
   const int64_t* n;
 };
 hipError_t launch_adamw_multi(bool eight, const AdamWTensors& t, const AdamWStep& c, uint64_t seed, hipStream_t s);
+hipError_t launch_adamw8_double_prune_packed(Dt dt, Dt grad, void* values_s, const uint32_t* meta_s, const void* grads,
+                                             uint8_t* m, uint8_t* me, uint8_t* v, uint8_t* ve, int64_t N, int64_t K,
+                                             const AdamWStep& c, uint64_t seed, void* packed_s, void* packed_dpT,
+                                             hipStream_t s);
 hipError_t launch_adamw_moments(Dt out, const uint8_t* m, const uint8_t* me, const uint8_t* v, const uint8_t* ve,
                                 int64_t n, void* mo, void* vo, hipStream_t s);
 

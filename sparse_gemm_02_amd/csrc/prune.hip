@@ -6,9 +6,12 @@
 // Footprint" section keeps each as two 16-bit values plus indices per group of
 // four.  Selection rule: the two largest magnitudes, equal magnitudes to the
 // lower position, NaN above every number.
+#include <type_traits>
+
 #include "adamw.h"
 #include "common.h"
 #include "launch.h"
+#include "moments8.h"
 
 namespace slope {
 
@@ -497,6 +500,11 @@ __global__ __launch_bounds__(kThreads) void double_prune_kernel(const E* __restr
 // conflicts.
 constexpr int DW_T = 128, DW_PITCH = 68;  // tile edge; LDS row pitch in 32-bit words
 
+struct Codes8 {                           // 8-bit moments and their blocks' scales
+  uint8_t *m, *me, *v, *ve;
+  uint32_t seed;
+};
+
 
 
 //
@@ -511,7 +519,13 @@ constexpr int DW_T = 128, DW_PITCH = 68;  // tile edge; LDS row pitch in 32-bit 
 // two.  The grid then covers whole 256-row chunks, rows past K written as 0.
 // UPD with PK also rewrites the updated values inside W_s's tile chunks
 // (pk_s, which holds W_s packed: the mask is static, so only values change).
-template <bool UPD, typename GT, bool H = false, bool PK = false>
+//
+// MOM: the moments are fp32 (0), or 8-bit codes (q; 2: with the hardware's root
+// and reciprocal, moments8.h).  A thread's eight values are a run of codes, and where K % 64
+// == 0 four neighbouring lanes hold a block of 32.  20480 x 5120 bf16 186 us (4.2 TB/s of
+// what it reads and writes; 5120 x 5120 41), where the step and the two passes over its
+// result by themselves take 219 (61), and fp32 moments here 289 (57).
+template <bool UPD, typename GT, bool H = false, bool PK = false, int MOM = 0>
 __global__ __launch_bounds__(kThreads) void double_prune_wide_kernel(uint16_t* vals, const uint32_t* __restrict__ meta,
                                                                     int64_t N, int64_t K,
                                                                     uint16_t* __restrict__ out_vals,
@@ -521,7 +535,7 @@ __global__ __launch_bounds__(kThreads) void double_prune_wide_kernel(uint16_t* v
                                                                     char* __restrict__ pk_s,
                                                                     const GT* __restrict__ grads,
                                                                     float* __restrict__ m, float* __restrict__ v,
-                                                                    AdamWStep hp) {
+                                                                    const Codes8 q8, AdamWStep hp) {
   __shared__ __attribute__((aligned(16))) uint32_t tile[DW_T * DW_PITCH];
   const int tid = threadIdx.x;
   // Workgroups are dealt to the eight XCDs in turn; give each XCD a contiguous
@@ -547,7 +561,8 @@ __global__ __launch_bounds__(kThreads) void double_prune_wide_kernel(uint16_t* v
   uint32_t nibs[4];
   int64_t el[4];
   bool ok[4];
-  float gf[UPD ? 4 : 1][8], mf[UPD ? 4 : 1][8], vf[UPD ? 4 : 1][8];
+  float gf[UPD ? 4 : 1][8], mf[UPD && !MOM ? 4 : 1][8], vf[UPD && !MOM ? 4 : 1][8];
+  Run8 run[MOM ? 4 : 1];
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
     const int64_t row = n0 + it * 32 + (tid >> 3);
@@ -558,8 +573,13 @@ __global__ __launch_bounds__(kThreads) void double_prune_wide_kernel(uint16_t* v
     nibs[it] = meta[rowc * in_wpr + (kcc >> 5)] >> (16 * (c & 1));
     if constexpr (UPD) {
       load8_f32(grads + el[it], gf[it]);
-      load8_f32(m + el[it], mf[it]);
-      load8_f32(v + el[it], vf[it]);
+      if constexpr (MOM) {
+        run[it] = Run8{*reinterpret_cast<const u32x2*>(q8.m + el[it]), *reinterpret_cast<const u32x2*>(q8.v + el[it]),
+                       q8.me[el[it] / 32], q8.ve[el[it] / 32]};
+      } else {
+        load8_f32(m + el[it], mf[it]);
+        load8_f32(v + el[it], vf[it]);
+      }
     }
   }
   // byte selectors (v_perm_b32 of a group's word with itself) giving the two
@@ -582,20 +602,40 @@ __global__ __launch_bounds__(kThreads) void double_prune_wide_kernel(uint16_t* v
     if constexpr (UPD) {
       typedef Fmt16<H> F;
       u32x4 nw;
+      if constexpr (MOM) {
+        typedef std::conditional_t<H, _Float16, uint16_t> E;
+        float pf[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = adamw_apply(F::to_f32((uint16_t)(w4[it][i] & 0xFFFFu)), gf[it][2 * i], mf[it][2 * i],
-                                     vf[it][2 * i], hp);
-        const float hi = adamw_apply(F::to_f32((uint16_t)(w4[it][i] >> 16)), gf[it][2 * i + 1], mf[it][2 * i + 1],
-                                     vf[it][2 * i + 1], hp);
-        nw[i] = (uint32_t)F::from_f32(lo) | ((uint32_t)F::from_f32(hi) << 16);
+        for (int i = 0; i < 4; ++i) {
+          pf[2 * i] = F::to_f32((uint16_t)(w4[it][i] & 0xFFFFu));
+          pf[2 * i + 1] = F::to_f32((uint16_t)(w4[it][i] >> 16));
+        }
+        nw = __builtin_bit_cast(u32x4, (update8<E, MOM == 2>(pf, gf[it], run[it], 8, hp, Noise((uint32_t)(el[it] / 8), q8.seed))));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float lo = adamw_apply(F::to_f32((uint16_t)(w4[it][i] & 0xFFFFu)), gf[it][2 * i], mf[it][2 * i],
+                                       vf[it][2 * i], hp);
+          const float hi = adamw_apply(F::to_f32((uint16_t)(w4[it][i] >> 16)), gf[it][2 * i + 1], mf[it][2 * i + 1],
+                                       vf[it][2 * i + 1], hp);
+          nw[i] = (uint32_t)F::from_f32(lo) | ((uint32_t)F::from_f32(hi) << 16);
+        }
       }
       w4[it] = nw;
       if (ok[it]) {
         const int64_t e = el[it];
         *reinterpret_cast<u32x4*>(vals + e) = nw;
-        store8_f32(m + e, mf[it]);
-        store8_f32(v + e, vf[it]);
+        if constexpr (MOM) {
+          *reinterpret_cast<u32x2*>(q8.m + e) = run[it].m;
+          *reinterpret_cast<u32x2*>(q8.v + e) = run[it].v;
+          if (c % 4 == 0) {
+            q8.me[e / 32] = (uint8_t)run[it].em;
+            q8.ve[e / 32] = (uint8_t)run[it].ev;
+          }
+        } else {
+          store8_f32(m + e, mf[it]);
+          store8_f32(v + e, vf[it]);
+        }
         if constexpr (PK) {                           // the same granule of W_s's chunk row
           const int64_t row = n0 + r;
           const int rs = (int)(row % kPackRows), gs = (int)((kc % kPackCols) / 16);
@@ -754,8 +794,27 @@ hipError_t dp_wide(uint16_t* vals, const uint32_t* meta, int64_t N, int64_t K, u
   const int64_t ktiles = PK ? cdiv(K, kPackRows) * (kPackRows / DW_T) : cdiv(K, DW_T);
   dim3 g((unsigned)ktiles, (unsigned)cdiv(N, DW_T));
   double_prune_wide_kernel<UPD, GT, H, PK><<<g, kThreads, 0, s>>>(vals, meta, N, K, out_vals, out_meta, out_mask,
-                                                                 pk_dpT, pk_s, (const GT*)grads, m, v, c);
+                                                                 pk_dpT, pk_s, (const GT*)grads, m, v, Codes8{}, c);
   return hipGetLastError();
+}
+
+template <typename GT, bool H>
+hipError_t dp_wide8(uint16_t* vals, const uint32_t* meta, const void* grads, const Codes8& q, int64_t N, int64_t K,
+                    const AdamWStep& c, char* pk_s, char* pk_dpT, hipStream_t s) {
+  const dim3 g((unsigned)(cdiv(K, kPackRows) * (kPackRows / DW_T)), (unsigned)cdiv(N, DW_T));
+  auto go = [&](auto kern) {
+    kern<<<g, kThreads, 0, s>>>(vals, meta, N, K, nullptr, nullptr, nullptr, pk_dpT, pk_s, (const GT*)grads, nullptr, nullptr,
+                                q, c);
+    return hipGetLastError();
+  };
+  return fast_step(c) ? go(double_prune_wide_kernel<true, GT, H, true, 2>) : go(double_prune_wide_kernel<true, GT, H, true, 1>);
+}
+template <bool H>
+hipError_t dp_wide8_grad(Dt grad, uint16_t* vals, const uint32_t* meta, const void* grads, const Codes8& q, int64_t N,
+                         int64_t K, const AdamWStep& c, char* pk_s, char* pk_dpT, hipStream_t s) {
+  if (grad == Dt::BF16) return dp_wide8<uint16_t, H>(vals, meta, grads, q, N, K, c, pk_s, pk_dpT, s);
+  if (grad == Dt::F16) return dp_wide8<_Float16, H>(vals, meta, grads, q, N, K, c, pk_s, pk_dpT, s);
+  return dp_wide8<float, H>(vals, meta, grads, q, N, K, c, pk_s, pk_dpT, s);
 }
 
 template <bool UPD, bool H, bool PK>
@@ -864,6 +923,17 @@ hipError_t launch_adamw_double_prune_packed(Dt dt, Dt grad, void* values_s, cons
   if (N == 0 || K == 0) return hipSuccess;
   return dp_wide_dt<true, true>(dt, grad, values_s, meta_s, N, K, nullptr, nullptr, nullptr, packed_dpT, packed_s,
                                 grads, m, v, c, s);
+}
+
+hipError_t launch_adamw8_double_prune_packed(Dt dt, Dt grad, void* values_s, const uint32_t* meta_s, const void* grads,
+                                             uint8_t* m, uint8_t* me, uint8_t* v, uint8_t* ve, int64_t N, int64_t K,
+                                             const AdamWStep& c, uint64_t seed, void* packed_s, void* packed_dpT,
+                                             hipStream_t s) {
+  if (N == 0 || K == 0) return hipSuccess;
+  const Codes8 q{m, me, v, ve, tensor_seed(seed, 0)};
+  if (dt == Dt::F16)
+    return dp_wide8_grad<true>(grad, (uint16_t*)values_s, meta_s, grads, q, N, K, c, (char*)packed_s, (char*)packed_dpT, s);
+  return dp_wide8_grad<false>(grad, (uint16_t*)values_s, meta_s, grads, q, N, K, c, (char*)packed_s, (char*)packed_dpT, s);
 }
 
 }  // namespace slope

@@ -31,8 +31,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import (I8_DECODE_MAX_TOKENS, MX_BLOCK, slope_adamw_double_prune_packed, slope_adamw_moments,
-               slope_adamw_multi, slope_double_prune_packed,
+from . import (I8_DECODE_MAX_TOKENS, MX_BLOCK, slope_adamw8_double_prune_packed, slope_adamw_double_prune_packed,
+               slope_adamw_moments, slope_adamw_multi, slope_double_prune_packed,
                slope_lowrank_add, slope_lowrank_grads_packed, slope_lowrank_grads_workspace_bytes,
                slope_lowrank_workspace_bytes, slope_masked_wgrad_packed, slope_pack_sparse, slope_pack_sparse_i8,
                slope_pack_tokens, slope_packed_sparse_bytes, slope_packed_sparse_i8_bytes, slope_packed_tokens_bytes,
@@ -187,10 +187,10 @@ class SparseAdamW(torch.optim.Optimizer):
     norm weights) take one launch together.
 
     state_bits=8: both moments as 8-bit codes with a scale for each 32 values
-    (slope_adamw_multi; a quarter of the fp32 moments' memory), rounded
-    stochastically with random bits from `seed` and the step; all parameters take
-    one launch together, and the layers' operands are re-derived from the new
-    values.  `moments(p)` gives them as values.
+    (a quarter of the fp32 moments' memory), rounded stochastically with random
+    bits from `seed` and the step; launches as above, but layers whose width is no
+    multiple of 64 step with the other parameters and their operands are re-derived.
+    `moments(p)` gives the moments as values.
 
     A step recorded into a graph repeats its step number (and random bits)."""
 
@@ -247,7 +247,13 @@ class SparseAdamW(torch.optim.Optimizer):
                 st["step"] += 1
                 g = p.grad.contiguous()
                 layer = self._layer_of.get(p)
-                if layer is not None and self.state_bits == 32:
+                if layer is not None and self.state_bits == 8 and layer.in_features % 64 == 0:
+                    slope_adamw8_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_exp"], st["exp_avg_sq"],
+                                                     st["exp_avg_sq_exp"], layer.out_features, layer.in_features,
+                                                     layer.packed_s, layer.packed_dpT, st["step"],
+                                                     seed=(self.seed << 40) + (done << 32) + st["step"], **hp)
+                    done += 1
+                elif layer is not None and self.state_bits == 32:
                     slope_adamw_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_sq"],
                                                     layer.out_features, layer.in_features, layer.packed_s,
                                                     layer.packed_dpT, st["step"], **hp)

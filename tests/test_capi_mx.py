@@ -74,6 +74,25 @@ def test_adamw_multi_refuses_tensors_that_share_memory(lib):
     assert f(g=(7 * FAKE - 126, 4 * FAKE)) == -1                     # the last value of a gradient over a moment
 
 
+def test_adamw8_double_prune_refusals(lib):
+    names = ("vals", "meta", "dw", "m", "me", "v", "ve", "ps", "pd")
+    def f(dt=BF16, gdt=BF16, N=64, K=128, hp=(1e-3, 0.9, 0.999, 1e-8, 0.01, 1), pb=1 << 40, qb=1 << 40, **k):
+        a = {n: k.get(n, (i + 1) * FAKE) for i, n in enumerate(names)}
+        h = None if hp is None else ctypes.byref(S.AdamWParams(*hp))
+        return lib.slope_adamw8_double_prune_packed(dt, gdt, a["vals"], a["meta"], a["dw"], a["m"], a["me"], a["v"], a["ve"],
+                                                    N, K, h, 0, a["ps"], pb, a["pd"], qb, None)
+    for n in names:
+        assert f(**{n: None}) == -1, n
+        if n not in ("me", "ve"):                                    # (scales may lie anywhere)
+            assert f(**{n: 20 * FAKE + 8}) == -3, n
+    assert f(dt=3) == -1 and f(gdt=7) == -1 and f(N=-1) == -1 and f(K=-1) == -1 and f(pb=-1) == -1 and f(qb=-1) == -1
+    assert f(hp=None) == -1 and f(hp=(1e-3, 0.9, 0.999, 1e-8, 0.01, 0)) == -1
+    assert f(dt=F32) == -6 and f(N=(1 << 21) + 16) == -6 and f(K=(1 << 21) + 64) == -6
+    assert f(N=24) == -2 and f(K=96) == -2 and f(K=48) == -2
+    assert f(pb=100) == -4 and f(qb=100) == -4
+    assert f(N=0) == 0 and f(K=0) == 0
+
+
 def test_adamw_moments_refusals(lib):
     f = lambda dt=BF16, m=FAKE, me=2 * FAKE, v=3 * FAKE, ve=4 * FAKE, n=64, mo=5 * FAKE, vo=6 * FAKE: \
         lib.slope_adamw_moments(dt, m, me, v, ve, n, mo, vo, None)

@@ -149,6 +149,42 @@ def test_many_tensors_take_several_launches(eight):
     a.guards_whole()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("gdt", list(DT))
+@pytest.mark.parametrize("N,K", [(16, 64), (48, 192), (272, 320), (528, 1024), (1040, 64), (144, 2112)])
+def test_fused_with_the_double_prune(N, K, dt, gdt):
+    """Values, codes and scales of slope_adamw_multi, chunks of the packing calls, byte for byte."""
+    say(f"[adamw8_double_prune] N={N} K={K} {dt} {gdt}")
+    from sparse_gemm_02_amd import slope_packed_sparse_bytes
+    n, words = N * K // 2, -(-K // 32)
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    nib = torch.tensor([4, 8, 12, 9, 13, 14], device="cuda")[torch.randint(0, 6, (N, words, 8), device="cuda", generator=g)]
+    meta = (nib << (4 * torch.arange(8, device="cuda"))).sum(-1).to(torch.int32)
+    a, b = (Lists([n], [dt], [gdt], 10 * N + K, True) for _ in range(2))
+    for x in (a, b):
+        x.g[0][n // 3] = float("nan")
+        x.me[0][1], x.ve[0][2 % blocks(n)] = 255, 255
+    packs = []
+    for x in (a, b):
+        ps = torch.full((slope_packed_sparse_bytes(N, K) + 64,), 0xA5, dtype=U8, device="cuda")
+        pd = torch.full((slope_packed_sparse_bytes(K, N) + 64,), 0xA5, dtype=U8, device="cuda")
+        S.slope_pack_sparse(x.p[0].view(N, K // 2), meta, N, K, ps)
+        packs.append((ps, pd))
+    for step, eps in ((1, 1e-8), (2, 1e-15), (3, 1e-8)):
+        hp = {**HP, "eps": eps}
+        S.slope_adamw8_double_prune_packed(a.p[0].view(N, K // 2), meta, a.g[0], a.m[0], a.me[0], a.v[0], a.ve[0], N, K,
+                                           *packs[0], step, seed=90 + step, **hp)
+        b.call(step, seed=90 + step, eps=eps)
+        S.slope_pack_sparse(b.p[0].view(N, K // 2), meta, N, K, packs[1][0])
+        S.slope_double_prune_packed(b.p[0].view(N, K // 2), meta, N, K, packs[1][1])
+        torch.cuda.synchronize()
+        for x, y in zip((a.p, a.m, a.v, a.me, a.ve), (b.p, b.m, b.v, b.me, b.ve)):
+            assert torch.equal(x[0].view(U8), y[0].view(U8))
+        assert all(torch.equal(s, t) for s, t in zip(*packs))
+        assert all((t[-64:] == 0xA5).all() for t in packs[0])
+    a.guards_whole()
+
+
 @pytest.mark.parametrize("dt,gdt,shift", [("bf16", "bf16", 0), ("f16", "f32", 5), ("f32", "bf16", 3)])
 def test_32_bit_lists_past_the_cache(dt, gdt, shift):
     """From 2^24 values on the 16-bit tensors are accessed non-temporally: still slope_adamw's bits."""
@@ -445,14 +481,16 @@ def test_optimizer_with_8_bits_trains_a_layer():
         torch.cuda.synchronize()
         if skip is not None:
             assert torch.equal(skip.detach(), kept)
-        # one list for each step number: the norm's own number lags by one after it sat out
+        # the layer's weight by itself (with its operands), then one list for each step number: the norm's
+        # own number lags by one after it sat out
         for p in params:
             p0, g, st = before[p]
             if g is None:
                 continue
             t = opt.state[p]["step"]
-            lists = [[q for q in order if before[q][1] is not None and opt.state[q]["step"] == k]
-                     for k in dict.fromkeys(opt.state[q]["step"] for q in order if before[q][1] is not None)]
+            rest = [q for q in order if before[q][1] is not None and q is not layer.values]
+            lists = [[layer.values]] + [[q for q in rest if opt.state[q]["step"] == k]
+                                        for k in dict.fromkeys(opt.state[q]["step"] for q in rest)]
             which = next(i for i, l in enumerate(lists) if any(q is p for q in l))
             place = next(i for i, q in enumerate(lists[which]) if q is p)
             n = p.numel()
