@@ -18,10 +18,12 @@ Tensor conventions (see include/slope.h):
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import operator
 import os
+import struct
 
 import torch
 
@@ -133,7 +135,7 @@ EXPORTED_SYMBOLS_INT8 = tuple(_SIGS_INT8)
 
 # include/slope_mx.h
 _SIGS_MX = {
-    "slope_adamw_multi": (_i32, [_i32, _i64, *[_vp] * 9, _P_HP, ctypes.c_uint64, _vp]),
+    "slope_adamw_multi": (_i32, [_i32, _i64, *[_vp] * 10, ctypes.c_uint64, _vp]),
     "slope_adamw8_double_prune_packed": (_i32, [_i32, _i32, *[_vp] * 7, _i64, _i64, _P_HP, ctypes.c_uint64, _vp, _i64,
                                                 _vp, _i64, _vp]),
     "slope_adamw_moments": (_i32, [_i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp]),
@@ -717,6 +719,9 @@ _numel, _data_ptr, _get_device = torch.Tensor.numel, torch.Tensor.data_ptr, torc
 _is_contiguous, _dtype_of = torch.Tensor.is_contiguous, operator.attrgetter("dtype")
 
 
+_HP_PACK = struct.Struct("=dddddq").pack            # AdamWParams' bytes, made faster
+
+
 def _multi_refuse(i, p, g, m, v, me, ve, dev, mdt):
     """Raises what tensor i of a list is refused for, if it is."""
     n = p.numel()
@@ -763,22 +768,20 @@ def slope_adamw_multi(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps
     dtypes = list(map(_dtype_of, every))
     codes = list(map(_CODES.get, dtypes[:2 * count]))
     everything = every + scales
-    blocks = [-(-n // MX_BLOCK) for n in of]
     if not (sizes == of * 4 and None not in codes and dtypes[2 * count:].count(mdt) == 2 * count
             and all(map(_is_contiguous, everything)) and set(map(_get_device, everything)) == {dev}
-            and (not eight or (list(map(_numel, scales)) == blocks * 2
+            and (not eight or (list(map(_numel, scales)) == [-(-n // MX_BLOCK) for n in of] * 2
                                and list(map(_dtype_of, scales)).count(_u8) == 2 * count))):
         for i in range(count):
             _multi_refuse(i, params[i], grads[i], m[i], v[i], mes[i] if eight else None, ves[i] if eight else None, dev,
                           mdt)
         raise ValueError("the lists are not accepted")
-    table = (_i64 * (len(everything) + count))(*of, *map(_data_ptr, everything))
-    kinds = (ctypes.c_int32 * (2 * count))(*codes)
-    at, kind_at = ctypes.addressof(table), ctypes.addressof(kinds)
-    lists = [at + 8 * count * (1 + k) for k in range(6 if eight else 4)]
-    hp = _hp(step, lr, beta1, beta2, eps, weight_decay)
-    _on_device("slope_adamw_multi", dev, stream, 8 if eight else 32, count, kind_at, kind_at + 4 * count, *lists[:4],
-               lists[4] if eight else None, lists[5] if eight else None, at, ctypes.byref(hp),
+    of += map(_data_ptr, everything)
+    table, kinds = array.array("q", of), array.array("i", codes)
+    at, kind_at, size = table.buffer_info()[0], kinds.buffer_info()[0], 8 * count
+    _on_device("slope_adamw_multi", dev, stream, 8 if eight else 32, count, kind_at, kind_at + 4 * count, at + size,
+               at + 2 * size, at + 3 * size, at + 4 * size, at + 5 * size if eight else None,
+               at + 6 * size if eight else None, at, _HP_PACK(lr, beta1, beta2, eps, weight_decay, int(step)),
                int(seed) & (2 ** 64 - 1))
 
 
@@ -821,6 +824,13 @@ def slope_adamw_moments(m, m_exp, v, v_exp, m_out=None, v_out=None, stream=None)
                flat(v_out, "v_out", n, odt))
 
 
+def _own(t, name):
+    """Address of a contiguous tensor that the other arguments go by."""
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() or 256                     # no elements: never dereferenced
+
+
 def _mxfp4_width(K):
     """(bytes of codes, bytes of scales) of a row of K values."""
     return 64 * -(-K // 128), 16 * -(-K // 512)
@@ -837,20 +847,20 @@ def slope_mxfp4_row_bytes(K: int):
 def slope_quantize_mxfp4(X, codes, exps, stream=None) -> None:
     """4-bit codes [T, code bytes] and scales [T, scale bytes] (slope_mxfp4_row_bytes)
     of the rows of X [T, K]."""
-    T, K = shape = _rows(X, "X")
+    T, K = _rows(X, "X")
     d = X.get_device()
     nc, ne = _mxfp4_width(K)
-    _on_device("slope_quantize_mxfp4", d, stream, _code(X.dtype), _arg(X, "X", shape, X.dtype, d), T, K,
+    _on_device("slope_quantize_mxfp4", d, stream, _code(X.dtype), _own(X, "X"), T, K,
                _arg(codes, "codes", (T, nc), _u8, d), _arg(exps, "exps", (T, ne), _u8, d))
 
 
 def slope_mxfp4_values(codes, exps, out, stream=None) -> None:
     """out [T, K] <- the values of 4-bit rows."""
-    T, K = shape = _rows(out, "out")
+    T, K = _rows(out, "out")
     d = out.get_device()
     nc, ne = _mxfp4_width(K)
     _on_device("slope_mxfp4_values", d, stream, _code(out.dtype), _arg(codes, "codes", (T, nc), _u8, d),
-               _arg(exps, "exps", (T, ne), _u8, d), T, K, _arg(out, "out", shape, out.dtype, d))
+               _arg(exps, "exps", (T, ne), _u8, d), T, K, _own(out, "out"))
 
 
 def slope_packed_sparse_mxfp4_bytes(rows: int, cols: int) -> int:
