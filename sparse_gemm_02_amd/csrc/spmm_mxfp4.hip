@@ -267,7 +267,7 @@ __global__ __launch_bounds__(64 * W, WPS) void decode_mxfp4_kernel(const uint8_t
 // LDS of the largest form for so many tokens: eight waves' X rows, and all of the scales.
 int64_t decode_lds(int tokens, int64_t stages) { return 1024 * tokens + cdiv(stages, 4) * 16 * tokens; }
 
-// A weight of at least 64 MB, read once by a call of up to 64 tokens, is not expected in the 256 MB
+// A weight of at least 64 MB, read once by a call, is not expected in the 256 MB
 // last-level cache at the next call, and its lines leave X's where they are.  us, from HBM and (a
 // single weight, called again and again) from the cache, without NT / with it:
 //   9216 -> 27648, 105 MB   1 token 20.5 / 18.8 and 17.2 / 17.5   64: 29.5 / 27.5 and 21.9 / 26.8
@@ -287,7 +287,7 @@ hipError_t decode_launch(const Args<O>& a, int parts) {
     return hipGetLastError();
   };
   static LdsLimit once, streams;
-  if (a.T <= 64 && cdiv(a.M, kMxRows) * a.stages * kMxChunkBytes >= kStreamBytes)
+  if (a.T <= 8 * R && cdiv(a.M, kMxRows) * a.stages * kMxChunkBytes >= kStreamBytes)
     return go(decode_mxfp4_kernel<R, FM, D, W, WPS, SPLIT, true, O>, streams);
   return go(decode_mxfp4_kernel<R, FM, D, W, WPS, SPLIT, false, O>, once);
 }
@@ -799,37 +799,52 @@ hipError_t large_go(const Args<O>& a, int64_t rows_full) {
 
 // Up to 64 tokens.  64 rows a block draw X half as often as 32, and 32 spread better over
 // the compute units; parts of K spread them too, and cost a second launch and their sums.
-// A unit takes in 48 bytes a nanosecond of rows of weight (0.41 bytes a value) and tokens
-// (0.53), and all of them 5800 of weight: whichever is estimated to take the least.
-// us, 64 rows / 32 rows / 64 rows in parts, the weight from HBM:
-//   9216 -> 27648    1 token 20.1 / 20.6          16: 21.1 / 23.0          64: 29.2 / 43
-//   5120 -> 20480            11.1 / 10.6              11.9 / 11.4              17.6 / 22.1
-//   9216 -> 9216              9.7 / 10.1              10.8 / 11.5              16.1 / 21.5 / 16.6 (3)
-//   20480 -> 5120            14.7 / 10.5 / 12.2 (3)   17.6 / 12.8 / 13.0 (3)   28.9 / 22.5 / 17.6 (3)
-//   36864 -> 9216            26.5 / 30.6 / 28.5 (3)   31.2 / 39.5 / 30.1 (3)   49.6 / 68.5 / 41.1 (3)
-// Two parts of 160 or 288 blocks won nothing anywhere: units that get two do all the work.
+// A unit takes in 48 bytes a nanosecond of rows of weight (0.41 bytes a value) and tokens (0.53),
+// and all of them 6400 of weight: what is estimated to take the least.  Parts have to win a tenth,
+// over blocks of 32 rows a little more, which do better than estimated.  us, 64 rows / 32 rows / 64 rows in parts, the weight from HBM:
+//   9216 -> 27648    1 token 18.7 / 20.4          16: 19.1 / 21.7          64: 27.9 / 42.2
+//   5120 -> 20480            12.1 / 10.4              11.7 / 11.3              17.5 / 22.0
+//   9216 -> 9216              9.8 / 10.1              10.8 / 11.6              16.0 / 21.4 / 18.3 (3)
+//   20480 -> 5120            14.5 / 10.3 / 12.1 (3)   17.5 / 12.6 / 12.8 (3)   28.3 / 22.3 / 17.7 (3)
+//   20480 -> 2560            13.7 /  9.3 /  9.4 (4)   16.4 / 11.6 / 10.0 (4)   26.1 / 20.8 / 13.9 (4)
+//   16384 -> 6144            12.8 /  9.8 / 12.1 (2)   14.9 / 11.2 / 12.7 (4)   22.6 / 18.0 / 17.9 (2)
+//   36864 -> 9216            25.5 / 28.0 / 26.3 (3)   30.2 / 37.9 / 27.2 (3)   47.2 / 67.4 / 40.9 (3)
 // Waves and pairs in flight as measured best: two blocks a unit want four waves (5120 -> 20480 at
 // 16 tokens 11.9 us, with eight 13.4), one wants eight (9216 -> 9216 at 16 10.8, with four 12.9).
 // (More pairs of weight in flight, 128 rows a block and the scales' loads behind the first pairs'
 // won nothing.)
+//
+// Of so long a K that 64 tokens' scales do not fit LDS (from 49153 on) a block has fewer tokens,
+// or a part of K.
 struct FewPlan {
+  int tokens;                                        // of a block: 8, 16, 32 or 64; 0: they fit no block
   bool wide, one;                                    // 64 rows a block; a block a compute unit at most
   int parts;
 };
+int group_of(int64_t T) { return T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 FewPlan few_plan(int64_t T, int64_t M, int64_t stages, int64_t most_parts) {
-  const int64_t cus = compute_units();
-  const double k = 128.0 * (double)stages, sums = 4.0 * (double)T * (double)M, stream = k * (double)M * 0.41 / 5.8e6;
-  auto intake = [&](int64_t rows, int64_t parts) {
-    return k * (double)cdiv(cdiv(M, rows) * parts, cus) / (double)parts * ((double)rows * 0.41 + 0.53 * (double)T) / 48e3;
+  const int64_t cus = compute_units(), groups = cdiv(stages, 4);
+  const double k = 128.0 * (double)stages, sums = 4.0 * (double)T * (double)M, stream = k * (double)M * 0.41 / 6.4e6;
+  auto intake = [&](int64_t rows, int64_t tokens, int64_t parts) {
+    const double a_unit = (double)cdiv(cdiv(M, rows) * cdiv(T, tokens) * parts, cus) / (double)parts;
+    return k * a_unit * ((double)rows * 0.41 + 0.53 * (double)std::min(T, tokens)) / 48e3;
   };
-  const double wide = intake(64, 1), narrow = intake(32, 1);
-  FewPlan plan{wide <= narrow, cdiv(M, wide <= narrow ? 64 : 32) <= cus, 1};
-  double least = std::max(std::min(wide, narrow), stream);
+  int tokens = group_of(T);
+  while (tokens && decode_lds(tokens, stages) > kLdsBytes) tokens = tokens > 8 ? tokens / 2 : 0;
+  FewPlan plan{tokens, false, false, 1};
+  double least = 1e30;
+  if (tokens) {
+    const double wide = intake(64, tokens, 1), narrow = intake(32, tokens, 1);
+    plan.wide = wide <= narrow;
+    plan.one = cdiv(M, plan.wide ? 64 : 32) * cdiv(T, tokens) <= cus;
+    least = std::max(plan.wide ? wide : 0.94 * narrow, stream);
+  }
+  tokens = group_of(T);
   for (int parts = 2; parts <= most_parts; ++parts) {
-    const double us = std::max(intake(64, parts), stream) + 3.0 + 2.0 * parts * sums / 5e6;   // and the sums' way to memory and back
-    if (us < 0.9 * least) {                          // (what parts win by less may be lost)
+    const double us = std::max(intake(64, tokens, parts), stream) + 3.0 + 2.0 * parts * sums / 5e6;   // and the sums' way to memory and back
+    if (us < 0.9 * least && decode_lds(tokens, cdiv(groups, parts) * 4) <= kLdsBytes) {
       least = us;
-      plan = FewPlan{true, cdiv(M, 64) * parts <= cus, parts};
+      plan = FewPlan{tokens, true, cdiv(M, 64) * parts <= cus, parts};
     }
   }
   return plan;
@@ -838,29 +853,24 @@ FewPlan few_plan(int64_t T, int64_t M, int64_t stages, int64_t most_parts) {
 int64_t most_parts(int64_t T, int64_t M, int64_t stages, int64_t scratch_bytes) {
   return std::max<int64_t>(1, std::min({(int64_t)kMostParts, cdiv(stages, 4), scratch_bytes / (4 * T * M)}));
 }
-// A group of tokens' X rows and a part's scales fit LDS (64 tokens: parts up to K = 49152).
-bool few_fits(int64_t T, int64_t stages, int64_t parts) {
-  const int tokens = T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64;
-  return decode_lds(tokens, cdiv(cdiv(stages, 4), parts) * 4) <= kLdsBytes;
-}
 
 template <typename O>
 hipError_t few_go(const Args<O>& a, const FewPlan& f) {
   if (f.parts > 1) {
-    if (a.T <= 8) return split_go<1, 2, 1, 8, 4, O>(a, f.parts);
-    if (a.T <= 16) return f.one ? split_go<2, 2, 1, 8, 4, O>(a, f.parts) : split_go<2, 2, 1, 4, 4, O>(a, f.parts);
-    if (a.T <= 32) return f.one ? split_go<4, 2, 1, 8, 4, O>(a, f.parts) : split_go<4, 2, 1, 4, 4, O>(a, f.parts);
+    if (f.tokens == 8) return split_go<1, 2, 1, 8, 4, O>(a, f.parts);
+    if (f.tokens == 16) return f.one ? split_go<2, 2, 1, 8, 4, O>(a, f.parts) : split_go<2, 2, 1, 4, 4, O>(a, f.parts);
+    if (f.tokens == 32) return f.one ? split_go<4, 2, 1, 8, 4, O>(a, f.parts) : split_go<4, 2, 1, 4, 4, O>(a, f.parts);
     return f.one ? split_go<8, 2, 1, 8, 2, O>(a, f.parts) : split_go<8, 2, 1, 4, 2, O>(a, f.parts);
   }
-  if (a.T <= 8) {
+  if (f.tokens == 8) {
     if (f.wide) return decode_go<1, 2, 1, 8, 4, O>(a);
     return f.one ? decode_go<1, 1, 2, 8, 4, O>(a) : decode_go<1, 1, 1, 8, 4, O>(a);
   }
-  if (a.T <= 16) {
+  if (f.tokens == 16) {
     if (!f.wide) return decode_go<2, 1, 1, 8, 4, O>(a);
     return f.one ? decode_go<2, 2, 1, 8, 4, O>(a) : decode_go<2, 2, 1, 4, 4, O>(a);
   }
-  if (a.T <= 32) {
+  if (f.tokens == 32) {
     if (!f.wide) return decode_go<4, 1, 1, 8, 4, O>(a);
     return f.one ? decode_go<4, 2, 1, 8, 4, O>(a) : decode_go<4, 2, 1, 4, 4, O>(a);
   }
@@ -900,9 +910,9 @@ hipError_t spmm_launch(const uint8_t* codes, const uint8_t* exps, int64_t T, int
   const Args<O> a{codes, exps, (const char*)packed, (int)M, (int)T, (int)cdiv(K, kMxCols), (O*)Y, (float*)scratch, scratch_bytes, s};
   if (T <= 64) {
     const FewPlan plan = few_plan(T, M, a.stages, scratch ? most_parts(T, M, a.stages, scratch_bytes) : 1);
-    return few_fits(T, a.stages, plan.parts) ? few_go<O>(a, plan) : mid_go<O>(a);
+    return plan.tokens ? few_go<O>(a, plan) : mid_go<O>(a);
   }
-  const bool fits = few_fits(T, a.stages, 1) && cdiv(T, 64) <= 65535;   // (and a grid's second dimension)
+  const bool fits = decode_lds(64, a.stages) <= kLdsBytes && cdiv(T, 64) <= 65535;   // (and a grid's second dimension)
   const double cus = (double)compute_units();
   const int64_t rows = cdiv(M, 256), cols = cdiv(T, 256), halves = cdiv(T, 128);
   const int64_t rows_full = full_width_rows(rows, cols, halves, (int64_t)cus);
@@ -924,7 +934,7 @@ int64_t spmm_mxfp4_scratch_bytes(int64_t T, int64_t K, int64_t M) {
   if (T == 0 || T > 64 || K == 0 || M == 0) return 0;
   const int64_t stages = cdiv(K, kMxCols);
   const int parts = few_plan(T, M, stages, most_parts(T, M, stages, INT64_MAX)).parts;
-  return parts > 1 && few_fits(T, stages, parts) ? parts * 4 * T * M : 0;
+  return parts > 1 ? parts * 4 * T * M : 0;
 }
 
 hipError_t launch_spmm_mxfp4(Dt out, const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K, const void* packed,

@@ -236,7 +236,7 @@ SHAPES = [(1, 16, 4), (1, 128, 64), (3, 144, 68), (5, 4096, 260), (16, 272, 1000
           (33, 512, 2052), (48, 5120, 64), (63, 784, 516), (64, 2048, 1024), (65, 768, 2304), (100, 1024, 128),
           (129, 272, 516), (200, 2320, 300), (255, 640, 256), (300, 128, 4100), (513, 1168, 772), (1000, 768, 516),
           (2, 20480, 1028), (64, 9216, 520), (7, 1024, 8196), (600, 256, 8196),
-          (40, 65552, 68), (250, 1168, 24004), (1100, 400, 9220), (2100, 144, 9220), (1030, 16, 9216)]
+          (40, 65552, 68), (20, 327680, 8), (3, 655360, 36), (250, 1168, 24004), (1100, 400, 9220), (2100, 144, 9220), (1030, 16, 9216)]
 
 
 @pytest.mark.parametrize("T,K,N", SHAPES)
