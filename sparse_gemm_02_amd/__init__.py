@@ -824,16 +824,16 @@ def slope_adamw_moments(m, m_exp, v, v_exp, m_out=None, v_out=None, stream=None)
                flat(v_out, "v_out", n, odt))
 
 
-def _own(t, name):
-    """Address of a contiguous tensor that the other arguments go by."""
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() or 256                     # no elements: never dereferenced
-
-
-def _mxfp4_width(K):
-    """(bytes of codes, bytes of scales) of a row of K values."""
-    return 64 * -(-K // 128), 16 * -(-K // 512)
+def _rows_fit(codes, exps, other, name, T, K, d):
+    """Raises unless codes and exps are T 4-bit rows of K values on device d, and the other operand, on d, is
+    contiguous.  (One test for what fits; addresses of no elements, 0, are passed as 256: never dereferenced.)"""
+    nc, ne = 64 * -(-K // 128), 16 * -(-K // 512)
+    if not (codes.dtype is _u8 and exps.dtype is _u8 and codes.shape == (T, nc) and exps.shape == (T, ne)
+            and codes.is_contiguous() and exps.is_contiguous() and other.is_contiguous()
+            and codes.get_device() == d and exps.get_device() == d):
+        if not other.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        _arg(codes, "codes", (T, nc), _u8, d), _arg(exps, "exps", (T, ne), _u8, d)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -849,18 +849,18 @@ def slope_quantize_mxfp4(X, codes, exps, stream=None) -> None:
     of the rows of X [T, K]."""
     T, K = _rows(X, "X")
     d = X.get_device()
-    nc, ne = _mxfp4_width(K)
-    _on_device("slope_quantize_mxfp4", d, stream, _code(X.dtype), _own(X, "X"), T, K,
-               _arg(codes, "codes", (T, nc), _u8, d), _arg(exps, "exps", (T, ne), _u8, d))
+    _rows_fit(codes, exps, X, "X", T, K, d)
+    _on_device("slope_quantize_mxfp4", d, stream, _code(X.dtype), X.data_ptr() or 256, T, K, codes.data_ptr() or 256,
+               exps.data_ptr() or 256)
 
 
 def slope_mxfp4_values(codes, exps, out, stream=None) -> None:
     """out [T, K] <- the values of 4-bit rows."""
     T, K = _rows(out, "out")
     d = out.get_device()
-    nc, ne = _mxfp4_width(K)
-    _on_device("slope_mxfp4_values", d, stream, _code(out.dtype), _arg(codes, "codes", (T, nc), _u8, d),
-               _arg(exps, "exps", (T, ne), _u8, d), T, K, _own(out, "out"))
+    _rows_fit(codes, exps, out, "out", T, K, d)
+    _on_device("slope_mxfp4_values", d, stream, _code(out.dtype), codes.data_ptr() or 256, exps.data_ptr() or 256, T, K,
+               out.data_ptr() or 256)
 
 
 def slope_packed_sparse_mxfp4_bytes(rows: int, cols: int) -> int:
@@ -893,12 +893,13 @@ def slope_spmm_mxfp4_packed(codes, exps, K, packed_w, N, Y, workspace=None, stre
     T = _rows(codes, "codes")[0]
     d = codes.get_device()
     pp, pb = _buffer(packed_w, "packed_w", d)
-    nc, ne = _mxfp4_width(K)
-    odt = Y.dtype
-    args = (_code(odt), _arg(codes, "codes", (T, nc), _u8, d), _arg(exps, "exps", (T, ne), _u8, d), T, K, pp, pb, N,
-            _arg(Y, "Y", (T, N), odt, d))
+    _rows_fit(codes, exps, Y, "Y", T, K, d)
+    if Y.shape != (T, N) or Y.get_device() != d:
+        _arg(Y, "Y", (T, N), Y.dtype, d)
     if workspace is None and stream is None and 1 < T <= 64 and d >= 0:
         need = _spmm_mxfp4_workspace(T, K, N)
         if need:
             workspace = torch.empty(need, dtype=_u8, device=codes.device)
-    _on_device("slope_spmm_mxfp4_packed", d, stream, *args, *_buffer(workspace, "workspace", d))
+    wp, wb = (None, 0) if workspace is None else _buffer(workspace, "workspace", d)
+    _on_device("slope_spmm_mxfp4_packed", d, stream, _code(Y.dtype), codes.data_ptr() or 256, exps.data_ptr() or 256, T, K,
+               pp, pb, N, Y.data_ptr() or 256, wp, wb)
