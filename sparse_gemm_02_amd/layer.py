@@ -287,20 +287,41 @@ class SparseAdamW(torch.optim.Optimizer):
             return tuple(values)
         return m, v
 
+    def _moment_names(self):
+        return ("exp_avg", "exp_avg_sq") + (() if self.state_bits == 32 else ("exp_avg_exp", "exp_avg_sq_exp"))
+
     def load_state_dict(self, state_dict):
-        """As torch's, with the moments in their own formats (torch's converts a
-        parameter's floating and integer states to the parameter's format)."""
-        saved = state_dict["state"]
-        ids = [i for g in state_dict["param_groups"] for i in g["params"]]
+        """As torch's, load hooks included, with the moments in their own formats (torch's
+        converts a parameter's floating and integer states to the parameter's format)."""
         want = torch.float32 if self.state_bits == 32 else torch.uint8
-        for i in ids:
-            if i in saved and saved[i] and saved[i]["exp_avg"].dtype is not want:
-                raise ValueError(f"the saved moments are {saved[i]['exp_avg'].dtype}, the optimizer's {want}")
-        super().load_state_dict(state_dict)
-        for p, i in zip((p for g in self.param_groups for p in g["params"]), ids):
-            for k, t in saved.get(i, {}).items():
-                if isinstance(t, torch.Tensor):
-                    self.state[p][k] = t.detach().clone().to(p.device)
+        saved, ids = {}, []                          # of what the hooks before the load made of the dictionary
+
+        def last_before(_, given):
+            ids.extend(i for g in given["param_groups"] for i in g["params"])
+            saved.update((i, given["state"][i]) for i in ids if i in given["state"])
+            for st in saved.values():
+                for name in self._moment_names():
+                    kept = st[name].dtype if name in st else want
+                    if kept is not want and not (self.state_bits == 32 and kept.is_floating_point):
+                        raise ValueError(f"the saved moments are {kept}, the optimizer's {want}")
+
+        def first_after(_):
+            for p, i in zip((p for g in self.param_groups for p in g["params"]), ids):
+                for k, t in saved.get(i, {}).items():
+                    if isinstance(t, torch.Tensor):
+                        self.state[p][k] = t.detach().to(p.device, want if k in self._moment_names() else t.dtype, copy=True)
+
+        hooks = [self.register_load_state_dict_pre_hook(last_before),
+                 self.register_load_state_dict_post_hook(first_after, prepend=True)]
+        try:
+            super().load_state_dict(state_dict)
+        finally:
+            for h in hooks:
+                h.remove()
+        for i, p in enumerate(p for g in self.param_groups for p in g["params"]):
+            for name in self._moment_names():
+                if self.state.get(p) and name not in self.state[p]:
+                    raise ValueError(f"the saved state of parameter {i} has no {name}")
 
 
 def training_state_bytes(layer: SparseLinear, optimizer: SparseAdamW | None = None) -> dict:
