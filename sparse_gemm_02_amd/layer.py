@@ -27,6 +27,7 @@ and N multiples of 16 (the packed operand format).
 """
 from __future__ import annotations
 
+import operator
 from typing import NamedTuple
 
 import torch
@@ -176,6 +177,40 @@ class SparseLinear(torch.nn.Module):
         return y.reshape(*lead, self.out_features)
 
 
+_data_ptr, _nbytes = torch.Tensor.data_ptr, operator.attrgetter("nbytes")
+
+
+def _turns(ps, gs):
+    """Turns of the parameters ps of a step, whose gradients are gs.  One call's tensors may not share memory:
+    where a parameter is written that another one is or reads as its gradient, the two take turns in
+    their order, as calls for each of them would; a gradient in its own parameter's memory becomes
+    a copy in gs."""
+    turns = [0] * len(ps)
+    tensors = ps + gs
+    first = list(map(_data_ptr, tensors))
+    spans = sorted(zip(first, map(operator.add, first, map(_nbytes, tensors))))
+    starts, ends = zip(*spans)
+    if all(map(operator.le, ends, starts[1:])):      # all apart, as they nearly always are
+        return turns
+    spans = []                                       # first byte, end, parameter's number, whether it is written
+    for i, p in enumerate(ps):
+        if p.numel():
+            at = p.data_ptr()
+            if gs[i].data_ptr() < at + p.nbytes and at < gs[i].data_ptr() + gs[i].nbytes:
+                gs[i] = gs[i].clone()
+            spans += ((t.data_ptr(), t.data_ptr() + t.nbytes, i, t is p) for t in (p, gs[i]))
+    before, reached = {}, []                         # earlier ones that share memory; spans that may meet the next
+    for s in sorted(spans):
+        reached = [o for o in reached if o[1] > s[0]]
+        for o in reached:
+            if (o[3] or s[3]) and o[2] != s[2]:
+                before.setdefault(max(o[2], s[2]), []).append(min(o[2], s[2]))
+        reached.append(s)
+    for i in sorted(before):
+        turns[i] = 1 + max(turns[j] for j in before[i])
+    return turns
+
+
 class SparseAdamW(torch.optim.Optimizer):
     """AdamW for SparseLinear layers (and any other bf16 / fp16 / fp32 parameters).
 
@@ -237,41 +272,43 @@ class SparseAdamW(torch.optim.Optimizer):
         for group in self.param_groups:
             b1, b2 = group["betas"]
             hp = dict(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"], weight_decay=group["weight_decay"])
-            # by step number and device (parameters without a gradient sit steps out), and parameters that
-            # share their memory after each other
-            lists, turns = {}, {}
-            for p in group["params"]:
-                if p.grad is None:
-                    continue
-                st = self._state_of(p)
-                st["step"] += 1
-                g = p.grad.contiguous()
-                layer = self._layer_of.get(p)
-                if layer is not None and self.state_bits == 8 and layer.in_features % 64 == 0:
-                    slope_adamw8_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_exp"], st["exp_avg_sq"],
-                                                     st["exp_avg_sq_exp"], layer.out_features, layer.in_features,
-                                                     layer.packed_s, layer.packed_dpT, st["step"],
-                                                     seed=(self.seed << 40) + (done << 32) + st["step"], **hp)
-                    done += 1
-                elif layer is not None and self.state_bits == 32:
-                    slope_adamw_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_sq"],
-                                                    layer.out_features, layer.in_features, layer.packed_s,
-                                                    layer.packed_dpT, st["step"], **hp)
-                else:
-                    at = (p.data_ptr(), p.device)
-                    turns[at] = turn = turns.get(at, -1) + 1 if p.numel() else 0
-                    lists.setdefault((st["step"], p.device, turn), []).append((p, g, st))
-            for (t, _, _), each in lists.items():
-                ps, gs, sts = zip(*each)
-                take = lambda name: [st[name] for st in sts]
-                eight = {} if self.state_bits == 32 else dict(m_exp=take("exp_avg_exp"), v_exp=take("exp_avg_sq_exp"),
-                                                              seed=(self.seed << 40) + (done << 32) + t)
-                slope_adamw_multi(ps, gs, take("exp_avg"), take("exp_avg_sq"), t, **eight, **hp)
-                done += 1
-                for p in ps:
+            ps = [p for p in group["params"] if p.grad is not None]
+            gs = [p.grad.contiguous() for p in ps]
+            if not ps:
+                continue
+            turns = _turns(ps, gs)
+            # a turn's fused layers, then its lists by step number and device (parameters without a gradient sit steps out)
+            for now in range(max(turns) + 1):
+                lists = {}
+                for p, g, turn in zip(ps, gs, turns):
+                    if turn != now:
+                        continue
+                    st = self._state_of(p)
+                    st["step"] += 1
                     layer = self._layer_of.get(p)
-                    if layer is not None:
-                        layer.refresh()
+                    if layer is not None and self.state_bits == 8 and layer.in_features % 64 == 0:
+                        slope_adamw8_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_exp"], st["exp_avg_sq"],
+                                                         st["exp_avg_sq_exp"], layer.out_features, layer.in_features,
+                                                         layer.packed_s, layer.packed_dpT, st["step"],
+                                                         seed=(self.seed << 40) + (done << 32) + st["step"], **hp)
+                        done += 1
+                    elif layer is not None and self.state_bits == 32:
+                        slope_adamw_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_sq"],
+                                                        layer.out_features, layer.in_features, layer.packed_s,
+                                                        layer.packed_dpT, st["step"], **hp)
+                    else:
+                        lists.setdefault((st["step"], p.device), []).append((p, g, st))
+                for (t, _), each in lists.items():
+                    own, grads, sts = zip(*each)
+                    take = lambda name: [st[name] for st in sts]
+                    eight = {} if self.state_bits == 32 else dict(m_exp=take("exp_avg_exp"), v_exp=take("exp_avg_sq_exp"),
+                                                                  seed=(self.seed << 40) + (done << 32) + t)
+                    slope_adamw_multi(own, grads, take("exp_avg"), take("exp_avg_sq"), t, **eight, **hp)
+                    done += 1
+                    for p in own:
+                        layer = self._layer_of.get(p)
+                        if layer is not None:
+                            layer.refresh()
         return loss
 
     @torch.no_grad()

@@ -109,3 +109,112 @@ def test_a_saved_state_without_moments_is_refused(bits):
     opt = _optimizer([_parameter(), _parameter(7)], state_bits=bits)
     opt.load_state_dict(saved)
     assert len(opt.state) == 1
+
+
+# ------------------------------------------------------------------ steps
+
+class Recorded:
+    """The library's calls of a step, in order: ("list" or "layer", parameters, step, seed).  A list is refused
+    as the library refuses it; weights take a step along their gradient, so that the order shows."""
+
+    def __init__(self, monkeypatch):
+        self.calls, self.refuse = [], None
+        monkeypatch.setattr(M, "slope_adamw_multi", self._list)
+        monkeypatch.setattr(M, "slope_adamw_double_prune_packed", self._layer32)
+        monkeypatch.setattr(M, "slope_adamw8_double_prune_packed", self._layer8)
+
+    @staticmethod
+    def _span(t):
+        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+    def _list(self, ps, gs, m, v, step, m_exp=None, v_exp=None, seed=0, **hp):
+        meet = lambda a, b: max(a[0], b[0]) < min(a[1], b[1])
+        written = [self._span(t) for t in (*ps, *m, *v, *(m_exp or ()), *(v_exp or ())) if t.numel()]
+        read = [self._span(t) for t in gs if t.numel()]
+        assert not any(meet(a, b) for i, a in enumerate(written) for b in written[:i] + read), "INVALID_ARG"
+        self._step("list", ps, gs, step, seed)
+
+    def _layer32(self, p, meta, g, m, v, N, K, ps, pd, step, **hp):
+        self._step("layer", [p], [g], step, None)
+
+    def _layer8(self, p, meta, g, m, me, v, ve, N, K, ps, pd, step, seed=0, **hp):
+        self._step("layer", [p], [g], step, seed)
+
+    def _step(self, kind, ps, gs, step, seed):
+        if self.refuse is not None and any(p is self.refuse for p in ps):
+            raise ValueError("refused")
+        self.calls.append((kind, list(ps), step, seed))
+        for p, g in zip(ps, gs):
+            p.copy_(2 * p + g)
+
+
+def _layer(N=16, K=64, dtype=torch.bfloat16):
+    layer = M.SparseLinear.__new__(M.SparseLinear)
+    torch.nn.Module.__init__(layer)
+    layer.in_features, layer.out_features, layer.rank = K, N, 0
+    layer.values = torch.nn.Parameter(torch.randn(N, K // 2).to(dtype))
+    layer.meta = layer.packed_s = layer.packed_dpT = None
+    return layer
+
+
+def _in_turn(params, grads):
+    """What a call for each parameter in their order leaves in the memory that `params` are views of."""
+    for p, g in zip(params, grads):
+        p.data.copy_(2 * p.data + g)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_parameters_that_overlap_in_part_take_turns(monkeypatch, bits):
+    rec = Recorded(monkeypatch)
+    def make():
+        flat = torch.arange(96, dtype=torch.float32)
+        own = torch.arange(5, dtype=torch.float32)
+        views = [flat, own, flat[10:40], flat[30:], flat[40:41], own[4:], flat[0:0]]
+        return flat, own, [torch.nn.Parameter(v) for v in views]
+    flat, own, params = make()
+    grads = [torch.randn(p.shape) for p in params]
+    opt = _optimizer(params, state_bits=bits)
+    for p, g in zip(params, grads):
+        p.grad = g
+    opt.step()
+    want, want_own, again = make()
+    _in_turn(again, grads)
+    assert torch.equal(flat, want) and torch.equal(own, want_own)
+    # three turns: the wholes, then what overlaps them alone, then what overlaps a part of the second turn
+    assert [[next(i for i, q in enumerate(params) if q is p) for p in ps] for _, ps, _, _ in rec.calls] == [[0, 1, 6], [2, 5], [3], [4]]
+
+
+def test_gradients_that_are_weights_of_the_step(monkeypatch):
+    """A gradient over its own weight, over one that is stepped before it and over one that is stepped after it."""
+    Recorded(monkeypatch)
+    a, b, c, d = (torch.randn(33) for _ in range(4))
+    start = [t.clone() for t in (a, b, c, d)]
+    params = [torch.nn.Parameter(t) for t in (a, b, c, d)]
+    for p, g in zip(params, (a, a, d, torch.ones(33))):
+        p.grad = g
+    _optimizer(params).step()
+    a0, b0, c0, d0 = start
+    assert torch.equal(a, 2 * a0 + a0) and torch.equal(b, 2 * b0 + a) and torch.equal(c, 2 * c0 + d0) and torch.equal(d, 2 * d0 + 1)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_layers_take_turns_with_what_overlaps_them(monkeypatch, bits):
+    rec = Recorded(monkeypatch)
+    layer, other = _layer(), _layer()
+    row = torch.nn.Parameter(layer.values.data[3])
+    params = [row, layer.values, other.values, torch.nn.Parameter(torch.randn(9))]
+    start = layer.values.detach().clone()
+    opt = M.SparseAdamW([], extra_params=params, state_bits=bits)
+    opt._layer_of = {l.values: l for l in (layer, other)}
+    for p in params:
+        p.grad = torch.randn(p.shape).to(p.dtype)
+    opt.step()
+    start[3] = 2 * start[3] + row.grad
+    assert torch.equal(layer.values, 2 * start + layer.values.grad)
+    assert [kind for kind, *_ in rec.calls] == ["layer", "list", "layer"]
+    # without a common byte: the layers, then one list
+    rec.calls.clear()
+    params[0].grad = None
+    opt.state[layer.values]["step"] = 0
+    opt.step()
+    assert [(kind, len(ps)) for kind, ps, *_ in rec.calls] == [("layer", 1), ("layer", 1), ("list", 1)]
