@@ -284,20 +284,22 @@ class SparseAdamW(torch.optim.Optimizer):
                     if turn != now:
                         continue
                     st = self._state_of(p)
-                    st["step"] += 1
+                    t = int(st["step"]) + 1          # kept once the call is accepted
                     layer = self._layer_of.get(p)
                     if layer is not None and self.state_bits == 8 and layer.in_features % 64 == 0:
                         slope_adamw8_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_exp"], st["exp_avg_sq"],
                                                          st["exp_avg_sq_exp"], layer.out_features, layer.in_features,
-                                                         layer.packed_s, layer.packed_dpT, st["step"],
-                                                         seed=(self.seed << 40) + (done << 32) + st["step"], **hp)
+                                                         layer.packed_s, layer.packed_dpT, t,
+                                                         seed=(self.seed << 40) + (done << 32) + t, **hp)
                         done += 1
+                        st["step"] = t
                     elif layer is not None and self.state_bits == 32:
                         slope_adamw_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_sq"],
                                                         layer.out_features, layer.in_features, layer.packed_s,
-                                                        layer.packed_dpT, st["step"], **hp)
+                                                        layer.packed_dpT, t, **hp)
+                        st["step"] = t
                     else:
-                        lists.setdefault((st["step"], p.device), []).append((p, g, st))
+                        lists.setdefault((t, p.device), []).append((p, g, st))
                 for (t, _), each in lists.items():
                     own, grads, sts = zip(*each)
                     take = lambda name: [st[name] for st in sts]
@@ -305,7 +307,8 @@ class SparseAdamW(torch.optim.Optimizer):
                                                                   seed=(self.seed << 40) + (done << 32) + t)
                     slope_adamw_multi(own, grads, take("exp_avg"), take("exp_avg_sq"), t, **eight, **hp)
                     done += 1
-                    for p in own:
+                    for p, st in zip(own, sts):
+                        st["step"] = t
                         layer = self._layer_of.get(p)
                         if layer is not None:
                             layer.refresh()

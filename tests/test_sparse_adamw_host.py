@@ -218,3 +218,43 @@ def test_layers_take_turns_with_what_overlaps_them(monkeypatch, bits):
     opt.state[layer.values]["step"] = 0
     opt.step()
     assert [(kind, len(ps)) for kind, ps, *_ in rec.calls] == [("layer", 1), ("layer", 1), ("list", 1)]
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_refused_call_counts_no_step(monkeypatch, bits):
+    """Where the library refuses a call, the parameters' step numbers are those of the calls that it took."""
+    rec = Recorded(monkeypatch)
+    layers = [_layer(), _layer()]
+    w = torch.randn(64)
+    rest = [torch.nn.Parameter(torch.randn(9)), torch.nn.Parameter(w), torch.nn.Parameter(w[:32])]
+    params = [l.values for l in layers] + rest
+    opt = M.SparseAdamW([], extra_params=params, state_bits=bits)
+    opt._layer_of = {l.values: l for l in layers}
+    for p in params:
+        p.grad = torch.zeros_like(p)
+    steps = lambda: [opt.state[p].get("step", 0) for p in params]
+    for refuse, want in [(params[1], [1, 0, 0, 0, 0]), (rest[0], [2, 1, 0, 0, 0]), (rest[2], [3, 2, 1, 1, 0])]:
+        rec.refuse = refuse
+        with pytest.raises(ValueError, match="refused"):
+            opt.step()
+        assert steps() == want
+    rec.refuse = None
+    rec.calls.clear()
+    opt.step()
+    assert steps() == [4, 3, 2, 2, 1]
+    assert [(len(ps), t) for _, ps, t, _ in rec.calls] == [(1, 4), (1, 3), (2, 2), (1, 1)]
+
+
+def test_a_step_number_that_is_a_tensor(monkeypatch):
+    """As other optimizers' checkpoints have it: parameters of one number still take one call."""
+    rec = Recorded(monkeypatch)
+    params = [_parameter(), _parameter(7)]
+    opt = _filled(_optimizer(params))
+    saved = opt.state_dict()
+    for st in saved["state"].values():
+        st["step"] = torch.tensor(5.0)
+    opt.load_state_dict(saved)
+    for p in params:
+        p.grad = torch.zeros_like(p)
+    opt.step()
+    assert [(len(ps), t) for _, ps, t, _ in rec.calls] == [(2, 6)] and opt.state[params[0]]["step"] == 6
