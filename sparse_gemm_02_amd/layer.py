@@ -32,8 +32,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import (I8_DECODE_MAX_TOKENS, MX_BLOCK, slope_adamw8_double_prune_packed, slope_adamw_double_prune_packed,
-               slope_adamw_moments, slope_adamw_multi, slope_double_prune_packed,
+from . import (I8_DECODE_MAX_TOKENS, MX_BLOCK, slope_adamw, slope_adamw8_double_prune_packed,
+               slope_adamw_double_prune_packed, slope_adamw_moments, slope_adamw_multi, slope_double_prune_packed,
                slope_lowrank_add, slope_lowrank_grads_packed, slope_lowrank_grads_workspace_bytes,
                slope_lowrank_workspace_bytes, slope_masked_wgrad_packed, slope_pack_sparse, slope_pack_sparse_i8,
                slope_pack_tokens, slope_packed_sparse_bytes, slope_packed_sparse_i8_bytes, slope_packed_tokens_bytes,
@@ -177,6 +177,7 @@ class SparseLinear(torch.nn.Module):
         return y.reshape(*lead, self.out_features)
 
 
+_LIST_MAX = 1 << 34       # values of a tensor that slope_adamw_multi takes
 _data_ptr, _nbytes = torch.Tensor.data_ptr, operator.attrgetter("nbytes")
 
 
@@ -297,6 +298,9 @@ class SparseAdamW(torch.optim.Optimizer):
                         slope_adamw_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_sq"],
                                                         layer.out_features, layer.in_features, layer.packed_s,
                                                         layer.packed_dpT, t, **hp)
+                        st["step"] = t
+                    elif self.state_bits == 32 and p.numel() > _LIST_MAX:
+                        slope_adamw(p, g, st["exp_avg"], st["exp_avg_sq"], t, **hp)
                         st["step"] = t
                     else:
                         lists.setdefault((t, p.device), []).append((p, g, st))

@@ -258,3 +258,20 @@ def test_a_step_number_that_is_a_tensor(monkeypatch):
         p.grad = torch.zeros_like(p)
     opt.step()
     assert [(len(ps), t) for _, ps, t, _ in rec.calls] == [(2, 6)] and opt.state[params[0]]["step"] == 6
+
+
+def test_parameters_too_large_for_a_list(monkeypatch):
+    """slope_adamw_multi takes tensors of at most 2^34 values; larger ones with 32-bit moments have a call of
+    slope_adamw's each, as far as that goes.  (Tensors without memory stand for them.)"""
+    calls = []
+    monkeypatch.setattr(M, "slope_adamw_multi", lambda ps, *a, **k: calls.append([p.numel() for p in ps]))
+    monkeypatch.setattr(M, "slope_adamw", lambda p, g, m, v, step, **hp: calls.append((p.numel(), step, hp["lr"])))
+    sizes = [1 << 34, (1 << 34) + 1, 64]
+    params = [torch.nn.Parameter(torch.empty(n, dtype=torch.bfloat16, device="meta")) for n in sizes]
+    monkeypatch.setattr(M, "_turns", lambda ps, gs: [0] * len(ps))
+    opt = _optimizer(params, lr=0.5)
+    for p in params:
+        p.grad = torch.empty_like(p)
+    opt.step()
+    opt.step()
+    assert calls == [((1 << 34) + 1, 1, 0.5), [1 << 34, 64], ((1 << 34) + 1, 2, 0.5), [1 << 34, 64]]
