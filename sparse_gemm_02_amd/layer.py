@@ -212,6 +212,21 @@ def _turns(ps, gs):
     return turns
 
 
+def _list_seed(seed, number, step):
+    """The 64-bit seed of list `number` of a step.  Seeds of 24 bits with up to 256 lists a step lie
+    side by side; others are hashed first (SplitMix64 of Steele, Lea and Flood, 2014), for all of their bits to
+    count and none to meet a neighbour's."""
+    if 0 <= seed < 1 << 24 and number < 256:
+        return (seed << 40) + (number << 32) + step
+    z = seed
+    for more in (0, number):
+        z = (z + more + 0x9E3779B97F4A7C15) & 0xFFFFFFFFFFFFFFFF
+        z = (z ^ z >> 30) * 0xBF58476D1CE4E5B9 & 0xFFFFFFFFFFFFFFFF
+        z = (z ^ z >> 27) * 0x94D049BB133111EB & 0xFFFFFFFFFFFFFFFF
+        z ^= z >> 31
+    return z + step & 0xFFFFFFFFFFFFFFFF
+
+
 class SparseAdamW(torch.optim.Optimizer):
     """AdamW for SparseLinear layers (and any other bf16 / fp16 / fp32 parameters).
 
@@ -234,7 +249,7 @@ class SparseAdamW(torch.optim.Optimizer):
                  state_bits=32, seed=0):
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
-        self.state_bits, self.seed = state_bits, seed
+        self.state_bits, self.seed = state_bits, int(seed)
         modules = list(modules)
         self._layer_of = {}
         params = []
@@ -291,7 +306,7 @@ class SparseAdamW(torch.optim.Optimizer):
                         slope_adamw8_double_prune_packed(p, layer.meta, g, st["exp_avg"], st["exp_avg_exp"], st["exp_avg_sq"],
                                                          st["exp_avg_sq_exp"], layer.out_features, layer.in_features,
                                                          layer.packed_s, layer.packed_dpT, t,
-                                                         seed=(self.seed << 40) + (done << 32) + t, **hp)
+                                                         seed=_list_seed(self.seed, done, t), **hp)
                         done += 1
                         st["step"] = t
                     elif layer is not None and self.state_bits == 32:
@@ -308,7 +323,7 @@ class SparseAdamW(torch.optim.Optimizer):
                     own, grads, sts = zip(*each)
                     take = lambda name: [st[name] for st in sts]
                     eight = {} if self.state_bits == 32 else dict(m_exp=take("exp_avg_exp"), v_exp=take("exp_avg_sq_exp"),
-                                                                  seed=(self.seed << 40) + (done << 32) + t)
+                                                                  seed=_list_seed(self.seed, done, t))
                     slope_adamw_multi(own, grads, take("exp_avg"), take("exp_avg_sq"), t, **eight, **hp)
                     done += 1
                     for p, st in zip(own, sts):

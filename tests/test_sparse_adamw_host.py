@@ -275,3 +275,42 @@ def test_parameters_too_large_for_a_list(monkeypatch):
     opt.step()
     opt.step()
     assert calls == [((1 << 34) + 1, 1, 0.5), [1 << 34, 64], ((1 << 34) + 1, 2, 0.5), [1 << 34, 64]]
+
+
+# ------------------------------------------------------------------ random bits
+
+def test_seeds_of_neighbouring_optimizers_and_lists_are_apart(monkeypatch):
+    """No two of the lists of a step, of steps and of optimizers with other seeds have the same random bits:
+    300 parameters over one tensor make 300 lists."""
+    rec = Recorded(monkeypatch)
+    w = torch.zeros(4)
+    seen, first = set(), {}
+    seeds = [0, 1, 2, (1 << 24) - 1, 1 << 24, (1 << 24) + 1, 1 << 40, (1 << 64) - 1, -2]
+    for seed in seeds:
+        params = [torch.nn.Parameter(w) for _ in range(300)]
+        opt = _optimizer(params, state_bits=8, seed=seed, lr=0.0)
+        for p in params:
+            p.grad = torch.zeros(4)
+        rec.calls.clear()
+        opt.step()
+        opt.step()
+        got = [(s & (2 ** 64 - 1), t) for _, _, t, s in rec.calls]
+        assert [t for _, t in got] == [1] * 300 + [2] * 300
+        seen |= {s for s, _ in got}
+        first[seed] = [s for s, _ in got]
+    assert len(seen) == len(seeds) * 600
+    # the numbers that they always had: seeds of 24 bits, the first 256 lists of a step
+    for seed in (0, 1, 2, (1 << 24) - 1):
+        assert first[seed][:256] == [(seed << 40) + (done << 32) + 1 for done in range(256)]
+
+
+def test_layers_take_seeds_in_their_order(monkeypatch):
+    rec = Recorded(monkeypatch)
+    layers = [_layer(), _layer()]
+    params = [l.values for l in layers] + [_parameter()]
+    opt = M.SparseAdamW([], extra_params=params, state_bits=8, seed=6)
+    opt._layer_of = {l.values: l for l in layers}
+    for p in params:
+        p.grad = torch.zeros_like(p)
+    opt.step()
+    assert [s for *_, s in rec.calls] == [(6 << 40) + (done << 32) + 1 for done in range(3)]
