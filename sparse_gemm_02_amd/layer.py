@@ -346,14 +346,20 @@ class SparseAdamW(torch.optim.Optimizer):
             return tuple(values)
         return m, v
 
+    def state_dict(self):
+        """As torch's, and with 8-bit moments the seed of their random bits."""
+        state = super().state_dict()
+        return state if self.state_bits == 32 else {**state, "seed": self.seed}
+
     def _moment_names(self):
         return ("exp_avg", "exp_avg_sq") + (() if self.state_bits == 32 else ("exp_avg_exp", "exp_avg_sq_exp"))
 
     def load_state_dict(self, state_dict):
         """As torch's, load hooks included, with the moments in their own formats (torch's
-        converts a parameter's floating and integer states to the parameter's format)."""
+        converts a parameter's floating and integer states to the parameter's format), and
+        the saved seed if there is one."""
         want = torch.float32 if self.state_bits == 32 else torch.uint8
-        saved, ids = {}, []                          # of what the hooks before the load made of the dictionary
+        saved, ids, saved_seed = {}, [], []          # of what the hooks before the load made of the dictionary
 
         def last_before(_, given):
             ids.extend(i for g in given["param_groups"] for i in g["params"])
@@ -364,7 +370,10 @@ class SparseAdamW(torch.optim.Optimizer):
                     if kept is not want and not (self.state_bits == 32 and kept.is_floating_point):
                         raise ValueError(f"the saved moments are {kept}, the optimizer's {want}")
 
+            saved_seed.append(int(given.get("seed", self.seed)))
+
         def first_after(_):
+            self.seed = saved_seed[-1]
             for p, i in zip((p for g in self.param_groups for p in g["params"]), ids):
                 for k, t in saved.get(i, {}).items():
                     if isinstance(t, torch.Tensor):

@@ -314,3 +314,34 @@ def test_layers_take_seeds_in_their_order(monkeypatch):
         p.grad = torch.zeros_like(p)
     opt.step()
     assert [s for *_, s in rec.calls] == [(6 << 40) + (done << 32) + 1 for done in range(3)]
+
+
+def test_the_seed_is_part_of_a_checkpoint(monkeypatch, tmp_path):
+    """A resumed run goes on with the random bits of the uninterrupted one, whatever seed the new optimizer was
+    made with."""
+    rec = Recorded(monkeypatch)
+    p = _parameter()
+    def run(o):
+        rec.calls.clear()
+        p.grad = torch.zeros_like(p)
+        o.step()
+        return [s for *_, s in rec.calls]
+    opt = _optimizer([p], state_bits=8, seed=77)
+    run(opt)
+    torch.save(opt.state_dict(), tmp_path / "opt.pt")
+    want = run(opt)
+    assert want == [(77 << 40) + 2]
+    again = _optimizer([p], state_bits=8)
+    again.load_state_dict(torch.load(tmp_path / "opt.pt", weights_only=True))
+    assert run(again) == want and again.seed == 77
+    # a checkpoint without one leaves the optimizer's own; a hook before the load may change it
+    old = torch.load(tmp_path / "opt.pt", weights_only=True)
+    del old["seed"]
+    other = _optimizer([p], state_bits=8, seed=5)
+    other.load_state_dict(old)
+    assert run(other) == [(5 << 40) + 2]
+    other.register_load_state_dict_pre_hook(lambda _, given: {**given, "seed": 9})
+    other.load_state_dict(old)
+    assert other.seed == 9
+    # 32-bit moments take no random bits, and their checkpoints are as they were
+    assert set(_optimizer([p]).state_dict()) == {"state", "param_groups"}
