@@ -70,7 +70,8 @@ slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* par
  * scales, the same seed), the chunks those of slope_pack_sparse and
  * slope_double_prune_packed of the new values.  dt BF16 or F16; grad_dt BF16, F16 or F32.
  * m_exp and v_exp may have any address.  Errors: those of slope_adamw_double_prune_packed,
- * and SLOPE_ERR_SHAPE unless K % 64 == 0 (the blocks of moments lie in one row). */
+ * SLOPE_ERR_SHAPE unless K % 64 == 0 (the blocks of moments lie in one row), and
+ * SLOPE_ERR_INVALID_ARG for a written tensor (chunks included) that shares memory with another one. */
 slope_status slope_adamw8_double_prune_packed(slope_dtype dt, slope_dtype grad_dt, void* values_s, const uint32_t* meta_s,
                                               const void* dW_values, uint8_t* m, uint8_t* m_exp, uint8_t* v, uint8_t* v_exp,
                                               int64_t N, int64_t K, const slope_adamw_params* hp, uint64_t seed,

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 #include <utility>
 #include <vector>
@@ -36,7 +37,11 @@ slope_status ptr(const void* p, bool required, unsigned align = 16) {
   } while (0)
 
 // Whether two of the written byte ranges [first, second) overlap, or one of them and one that is read.
-typedef std::vector<std::pair<uintptr_t, uintptr_t>> Ranges;
+typedef std::pair<uintptr_t, uintptr_t> Range;
+typedef std::vector<Range> Ranges;
+Range range(const void* p, int64_t bytes) {
+  return Range(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes);
+}
 bool overlap(Ranges& written, const Ranges& read) {
   std::sort(written.begin(), written.end());
   for (size_t i = 1; i < written.size(); ++i)
@@ -46,6 +51,15 @@ bool overlap(Ranges& written, const Ranges& read) {
     if (w != written.begin() && std::prev(w)->second > r.first) return true;
   }
   return false;
+}
+// Refuses a call (of at least one value) whose written ranges overlap each other or one that is read.
+slope_status apart(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+  try {
+    Ranges w(written);
+    return overlap(w, Ranges(read)) ? SLOPE_ERR_INVALID_ARG : SLOPE_OK;
+  } catch (const std::bad_alloc&) {
+    return SLOPE_ERR_HIP;
+  }
 }
 
 }  // namespace
@@ -67,9 +81,6 @@ slope_status slope_adamw_multi(int state_bits, int64_t count, const int32_t* par
     Ranges written, read;
     written.reserve((size_t)count * (eight ? 5 : 3));
     read.reserve((size_t)count);
-    auto range = [](const void* p, int64_t bytes) {
-      return std::make_pair(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes);
-    };
     auto writes = [&](const void* p, int64_t bytes) { written.push_back(range(p, bytes)); };
     for (int64_t i = 0; i < count; ++i) {
       if (!dt_ok(param_dt[i]) || !dt_ok(grad_dt[i]) || n[i] < 0) return SLOPE_ERR_INVALID_ARG;
@@ -117,8 +128,12 @@ slope_status slope_adamw8_double_prune_packed(slope_dtype dt, slope_dtype grad_d
   if (dt == SLOPE_F32) return SLOPE_ERR_UNSUPPORTED;   // 16-bit values only
   if (N % 16 || K % 64) return SLOPE_ERR_SHAPE;        // a block of moments lies in one row
   if (K > kPackedMaxCols || N > kPackedMaxCols) return SLOPE_ERR_UNSUPPORTED;
-  if (packed_s_bytes < slope::packed_sparse_bytes(N, K) || packed_dpT_bytes < slope::packed_sparse_bytes(K, N))
-    return SLOPE_ERR_WORKSPACE;
+  const int64_t n = N * K / 2, chunks_s = slope::packed_sparse_bytes(N, K), chunks_dpT = slope::packed_sparse_bytes(K, N);
+  if (packed_s_bytes < chunks_s || packed_dpT_bytes < chunks_dpT) return SLOPE_ERR_WORKSPACE;
+  if (n == 0) return SLOPE_OK;
+  SLOPE_TRY(apart({range(values_s, 2 * n), range(m, n), range(m_exp, n / SLOPE_MX_BLOCK), range(v, n),
+                   range(v_exp, n / SLOPE_MX_BLOCK), range(packed_s, chunks_s), range(packed_dpT, chunks_dpT)},
+                  {range(meta_s, N * (K / 32) * 4), range(dW_values, n * size_of(grad_dt))}));
   return from_hip(slope::launch_adamw8_double_prune_packed((Dt)dt, (Dt)grad_dt, values_s, meta_s, dW_values, m, m_exp, v, v_exp,
                                                            N, K, c, seed, packed_s, packed_dpT, (hipStream_t)stream));
 }
