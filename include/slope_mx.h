@@ -83,7 +83,8 @@ slope_status slope_adamw8_double_prune_packed(slope_dtype dt, slope_dtype grad_d
  * hold every value exactly (bfloat16 has four significant bits to spare).  Either
  * moment may be left out: its three arguments are NULL.  Any alignment of the codes;
  * outputs need their element's.  Errors: SLOPE_ERR_INVALID_ARG for an incomplete
- * moment or none, SLOPE_ERR_UNSUPPORTED for F16 or n > 2^34. */
+ * moment or none, or an output that shares memory with another argument;
+ * SLOPE_ERR_UNSUPPORTED for F16 or n > 2^34. */
 slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, const uint8_t* m_exp_or_null,
                                  const uint8_t* v_or_null, const uint8_t* v_exp_or_null, int64_t n,
                                  void* m_out_or_null, void* v_out_or_null, void* stream);
@@ -91,7 +92,9 @@ slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, c
 /* Largest reduction width of the 4-bit product. */
 #define SLOPE_MXFP4_MAX_COLS (1 << 21)
 
-/* 4-bit floating point with a scale for 32 values.  Of each 32 consecutive values x of
+/* In the calls below outputs and workspaces share memory with no other argument (not checked).
+ *
+ * 4-bit floating point with a scale for 32 values.  Of each 32 consecutive values x of
  * a row (the last block filled up with zeros):
  *   scale  2^E, E = max(-127, e - 2), e the exponent of the largest magnitude rounded to
  *          two significant bits (ties away from zero)

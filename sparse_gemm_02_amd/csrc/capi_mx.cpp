@@ -147,7 +147,11 @@ slope_status slope_adamw_moments(slope_dtype out_dt, const uint8_t* m_or_null, c
   SLOPE_TRY(ptr(m_out_or_null, false, (unsigned)size_of(out_dt)));
   SLOPE_TRY(ptr(v_out_or_null, false, (unsigned)size_of(out_dt)));
   if (out_dt == SLOPE_F16 || n > slope::kMultiMaxElems) return SLOPE_ERR_UNSUPPORTED;
-  if (m_out_or_null && m_out_or_null == v_out_or_null && n > 0) return SLOPE_ERR_INVALID_ARG;
+  if (n == 0) return SLOPE_OK;
+  const int64_t blocks = (n + SLOPE_MX_BLOCK - 1) / SLOPE_MX_BLOCK;
+  const auto of = [](const void* p, int64_t bytes) { return range(p, p ? bytes : 0); };
+  SLOPE_TRY(apart({of(m_out_or_null, n * size_of(out_dt)), of(v_out_or_null, n * size_of(out_dt))},
+                  {of(m_or_null, n), of(m_exp_or_null, blocks), of(v_or_null, n), of(v_exp_or_null, blocks)}));
   return from_hip(slope::launch_adamw_moments((Dt)out_dt, m_or_null, m_exp_or_null, v_or_null, v_exp_or_null, n,
                                               m_out_or_null, v_out_or_null, (hipStream_t)stream));
 }

@@ -49,3 +49,25 @@ def test_fused_8_bit_step_refuses_shared_memory(lib, gdt):
             assert f(**{a: at[b]}) == INVALID, (a, b)                # the same address
             step = 1 if a in ("me", "ve") else 16
             assert f(**{a: at[b] + (size[b] - 1) // step * step}) == INVALID, (a, b)   # over its last bytes
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_moments_refuse_shared_memory(lib, dt):
+    n, e = 4096, 2 if dt == BF16 else 4
+    names = ("m", "me", "v", "ve", "mo", "vo")
+    at = {k: (i + 1) * FAKE for i, k in enumerate(names)}
+    size = dict(m=n, me=n // 32, v=n, ve=n // 32, mo=n * e, vo=n * e)
+
+    def f(n=n, **k):
+        return lib.slope_adamw_moments(dt, *[k.get(x, at[x]) for x in names[:4]], n, k.get("mo", at["mo"]), k.get("vo", at["vo"]), None)
+    for out in ("mo", "vo"):
+        for other in names:
+            if other == out:
+                continue
+            assert f(**{out: at[other]}) == INVALID, (out, other)
+            assert f(**{out: at[other] + (size[other] - 1) // e * e}) == INVALID, (out, other)   # over its last bytes
+            assert f(**{other: at[out] + size[out] - e}) == INVALID, (out, other)
+    # one moment alone: an output over its own codes
+    g = lambda mo: lib.slope_adamw_moments(dt, at["m"], at["me"], None, None, n, mo, None, None)
+    assert g(at["m"]) == INVALID and g(at["m"] + n - e) == INVALID and g(at["m"] - e * n + e) == INVALID and g(at["me"]) == INVALID
+    assert f(n=0, mo=at["m"], vo=at["m"]) == 0                       # no values: nothing to share
