@@ -147,7 +147,7 @@ slope_status slope_pack_sparse_mxfp4(slope_dtype dt, const void* values, const u
 
 /* Bytes of device workspace that make slope_spmm_mxfp4_packed fastest: partial sums of up
  * to eight parts of K where T <= 64 tokens of a long K meet few outputs (20480 -> 5120 at 64),
- * 0 elsewhere.  Host-only; errors as the product's. */
+ * 0 elsewhere.  Of the current device.  Host-only; errors as the product's. */
 slope_status slope_spmm_mxfp4_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t* bytes);
 
 /* The 2:4 sparse product on 4-bit floating point:

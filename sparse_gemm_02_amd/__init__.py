@@ -879,17 +879,24 @@ def slope_pack_sparse_mxfp4(values, meta, rows, cols, packed, stream=None) -> No
 
 
 def slope_spmm_mxfp4_workspace_bytes(T: int, K: int, N: int) -> int:
+    """Bytes of workspace that make the product fastest on the current device."""
     b = ctypes.c_int64()
     _check("slope_spmm_mxfp4_workspace_bytes", library().slope_spmm_mxfp4_workspace_bytes(T, K, N, ctypes.byref(b)))
     return b.value
 
 
-_spmm_mxfp4_workspace = functools.lru_cache(maxsize=4096)(slope_spmm_mxfp4_workspace_bytes)
+@functools.lru_cache(maxsize=4096)
+def _spmm_mxfp4_workspace(dev, T, K, N):
+    with torch.cuda.device(dev):
+        return slope_spmm_mxfp4_workspace_bytes(T, K, N)
 
 
 def slope_spmm_mxfp4_packed(codes, exps, K, packed_w, N, Y, workspace=None, stream=None) -> None:
-    """Y [T, N] = Xq . W_q^T on 4-bit rows of K values and a 2:4 weight's 4-bit chunks, any T.  On the
-    current stream and without a workspace the call takes one of slope_spmm_mxfp4_workspace_bytes."""
+    """Y [T, N] = Xq . W_q^T on 4-bit rows of K values and a 2:4 weight's 4-bit chunks, any T.  Without a
+    workspace the call takes one of slope_spmm_mxfp4_workspace_bytes (an allocation of the current
+    stream), but not where `stream` is given: then its sums are in another order where a
+    workspace would have split K, and it is slower.  A workspace of that size gives
+    the same bits on every stream."""
     T = _rows(codes, "codes")[0]
     d = codes.get_device()
     pp, pb = _buffer(packed_w, "packed_w", d)
@@ -897,7 +904,7 @@ def slope_spmm_mxfp4_packed(codes, exps, K, packed_w, N, Y, workspace=None, stre
     if Y.shape != (T, N) or Y.get_device() != d:
         _arg(Y, "Y", (T, N), Y.dtype, d)
     if workspace is None and stream is None and 1 < T <= 64 and d >= 0:
-        need = _spmm_mxfp4_workspace(T, K, N)
+        need = _spmm_mxfp4_workspace(d, T, K, N)
         if need:
             workspace = torch.empty(need, dtype=_u8, device=codes.device)
     wp, wb = (None, 0) if workspace is None else _buffer(workspace, "workspace", d)
