@@ -118,8 +118,9 @@ slope_status slope_quantize_mxfp4(slope_dtype dt, const void* X, int64_t T, int6
                                   void* stream);
 
 /* out [T, K] out_dt <- the values that rows of codes stand for (NaN where the scale is
- * 255).  BF16 and F32 hold them exactly (bfloat16 but for values below 2^-133), F16
- * rounds to its own range.  out needs its element's alignment. */
+ * 255).  BF16 and F32 hold them exactly, down to the least, 2^-128; but from 2^128 on they are
+ * infinities, and a finite value of at least 1.75 * 2^127 is coded as 2^128 (in a product it
+ * counts as that).  F16 rounds to its own range.  out needs its element's alignment. */
 slope_status slope_mxfp4_values(slope_dtype out_dt, const uint8_t* codes, const uint8_t* exps, int64_t T, int64_t K,
                                 void* out, void* stream);
 
