@@ -245,6 +245,8 @@ class SparseAdamW(torch.optim.Optimizer):
 
     A step recorded into a graph repeats its step number (and random bits)."""
 
+    state_bits, seed = 32, 0                         # of an optimizer pickled without them
+
     def __init__(self, modules, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, extra_params=(),
                  state_bits=32, seed=0):
         if state_bits not in (8, 32):
@@ -266,6 +268,9 @@ class SparseAdamW(torch.optim.Optimizer):
                 seen.add(id(p))
                 uniq.append(p)
         super().__init__(uniq, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
+
+    def __getstate__(self):                          # copies and pickles keep what the optimizer is made of
+        return {**super().__getstate__(), "state_bits": self.state_bits, "seed": self.seed, "_layer_of": self._layer_of}
 
     def _state_of(self, p):
         st = self.state[p]

@@ -345,3 +345,27 @@ def test_the_seed_is_part_of_a_checkpoint(monkeypatch, tmp_path):
     assert other.seed == 9
     # 32-bit moments take no random bits, and their checkpoints are as they were
     assert set(_optimizer([p]).state_dict()) == {"state", "param_groups"}
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_copies_of_an_optimizer(monkeypatch, bits):
+    """A deep copy (and a pickled one) saves, loads and steps as the optimizer does, on its own parameters and layers."""
+    import copy
+    import pickle
+    rec = Recorded(monkeypatch)
+    layer = _layer()
+    opt = M.SparseAdamW([layer], extra_params=[_parameter()], state_bits=bits, seed=3)
+    _filled(opt)
+    for make in (copy.deepcopy, lambda o: pickle.loads(pickle.dumps(o))):
+        other = make(opt)
+        saved = other.state_dict()
+        assert saved.get("seed") == (3 if bits == 8 else None) and len(saved["state"]) == 2
+        other.load_state_dict(opt.state_dict())
+        params = other.param_groups[0]["params"]
+        assert not any(p is q for p in params for q in opt.param_groups[0]["params"])
+        for p in params:
+            p.grad = torch.zeros_like(p)
+        rec.calls.clear()
+        other.step()
+        assert [kind for kind, *_ in rec.calls] == ["layer", "list"] and rec.calls[0][1][0] is params[0]
+        assert other.state[params[0]]["step"] == 6 and opt.state[layer.values]["step"] == 5
