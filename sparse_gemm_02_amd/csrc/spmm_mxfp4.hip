@@ -519,11 +519,12 @@ __global__ __launch_bounds__(G::THREADS, 1) void tiles_mxfp4_kernel(const uint8_
 // 1600.  One barrier a stage; a stage's reads of the weight run one stage ahead of its
 // products and the loads three.
 //
-// Measured, 8192 x 9216 x 9216 bf16: 335 to 347 us with the clock that the card holds
-// (1.87 GHz, 51 % of the matrix rate): products and barriers alone 250 to 270, without the loads 344 of 386, without the
-// reads 331, without the products 248, without the expansion 338 (timing copies on one
-// card).  Two groups of four waves half a stage apart, one reading while the other
-// multiplies: 336 to 358; four waves of 128 x 128: 373.
+// Measured, 8192 x 9216 x 9216 bf16: 360 to 426 us a call with random kept positions, 350 to 392 with
+// equal ones (the operands' bits are part of the power); by counters the matrix cores are busy
+// 50 % of the time at 1.72 GHz, LDS 35 %.  Timing copies on one card, equal positions, where the whole
+// took 335 to 347: products and barriers alone 250 to 270, without the loads 344 of 386, without the
+// reads 331, without the products 248, without the expansion 338.  Two groups of four waves half a
+// stage apart, one reading while the other multiplies: 336 to 358; four waves of 128 x 128: 373.
 template <int BM_, int BT_, int WGM_, int WGT_, int NST_>
 struct GeoW {
   static constexpr int BM = BM_, BT = BT_, WGM = WGM_, WGT = WGT_, WAVES = WGM * WGT, THREADS = 64 * WAVES;
