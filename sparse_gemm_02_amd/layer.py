@@ -241,7 +241,10 @@ class SparseAdamW(torch.optim.Optimizer):
     (a quarter of the fp32 moments' memory), rounded stochastically with random
     bits from `seed` and the step; launches as above, but layers whose width is no
     multiple of 64 step with the other parameters and their operands are re-derived.
-    `moments(p)` gives the moments as values.
+    `moments(p)` gives the moments as values; checkpoints hold the seed.
+
+    Parameters that overlap in memory, or whose gradient is another one's memory, step
+    after each other in their order, as calls for each of them would.
 
     A step recorded into a graph repeats its step number (and random bits)."""
 
